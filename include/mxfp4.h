@@ -66,8 +66,12 @@ typedef enum mxfp4_status {
   MXFP4_ERR_ALIGN = 3, /* a tensor pointer is not 16-byte aligned (a
                           status word: not 4-byte aligned) */
   MXFP4_ERR_ENUM = 4,  /* dtype, axis or rounding out of range */
-  MXFP4_ERR_CUDA = 5   /* the launch failed (cudaGetLastError); faults of a
+  MXFP4_ERR_CUDA = 5,  /* the launch failed (cudaGetLastError); faults of a
                           kernel that launched surface on the stream */
+  MXFP4_ERR_VALUE = 6, /* a number (eps, a factor, a step count) is outside
+                          its stated range */
+  MXFP4_ERR_WORKSPACE = 7 /* the workspace is smaller than its entry point's
+                             _workspace function says */
 } mxfp4_status;
 
 typedef enum mxfp4_dtype { MXFP4_F32 = 0, MXFP4_BF16 = 1 } mxfp4_dtype;
@@ -387,6 +391,72 @@ mxfp4_status mxfp4_gemm_quantize_a(const void* x, int64_t m, int64_t n, int64_t 
                                    int rounding, uint64_t seed, const uint8_t* b_codes,
                                    const uint8_t* b_scales, float* c, uint8_t* a_codes,
                                    uint8_t* a_scales, int* status, void* stream);
+
+/*
+ * Layer norm of every row of X, the transform in front of a quantized linear
+ * layer (pre-norm blocks of the pages' vision transformers and LLMs):
+ *   mean = sum_c X[r][c] / cols,   var = sum_c (X[r][c] - mean)^2 / cols,
+ *   rstd = (var + eps)^(-1/2),
+ *   Y[r][c] = (X[r][c] - mean) * rstd * weight[c] + bias[c]
+ * in fp32 (the squares are summed around the mean, not as E[x^2] - mean^2),
+ * rounded once to dtype.
+ *   x      device, rows of cols elements of dtype, row r at x + r * ldx
+ *          elements (ldx >= cols); element alignment suffices, 16-byte
+ *          aligned rows are faster
+ *   weight, bias  device fp32 [cols] or NULL (1 and 0)
+ *   eps    >= 0 and finite
+ *   y      device, written: [rows][cols] of dtype; must not overlap x
+ *   mean, rstd  device fp32 [rows] or NULL: the statistics the backward pass
+ *          takes
+ * Any rows, cols > 0 within the size limit. A row that holds Inf or NaN
+ * gives NaN in that row.
+ */
+mxfp4_status mxfp4_layernorm(const void* x, int dtype, int64_t rows, int64_t cols,
+                             int64_t ldx, const float* weight, const float* bias, float eps,
+                             void* y, float* mean, float* rstd, void* stream);
+
+/*
+ * mxfp4_layernorm fused with the forward quantization of its output: codes
+ * and scales are those of mxfp4_quantize(y, dtype, rows, cols, ROWS, RNE,
+ * ...), bit for bit, without y being read back; y itself is written only
+ * where it is wanted. Source: "Oscillation-Reduced MXFP4 Training for Vision
+ * Transformers", rebuttal Question 2 (Q_D of a linear layer's input in the
+ * forward pass).
+ *   y       as in mxfp4_layernorm, or NULL
+ *   codes, scales  device, ROWS layout; codes 16-byte aligned
+ * cols must be a multiple of 32.
+ */
+mxfp4_status mxfp4_layernorm_quantize(const void* x, int dtype, int64_t rows, int64_t cols,
+                                      int64_t ldx, const float* weight, const float* bias,
+                                      float eps, void* y, float* mean, float* rstd,
+                                      uint8_t* codes, uint8_t* scales, void* stream);
+
+/* Bytes of workspace mxfp4_layernorm_backward needs for dw and db; -1 for a
+ * shape it refuses. */
+int64_t mxfp4_layernorm_backward_workspace(int64_t rows, int64_t cols);
+
+/*
+ * Gradients of mxfp4_layernorm. With h = (x - mean) * rstd and
+ * g = dy * weight, per row:
+ *   dx = rstd * (g - sum_c(g) / cols - h * sum_c(g * h) / cols)
+ * and over the rows, summed in fp32 in a fixed order (the same inputs give
+ * the same bits on the same device):
+ *   dw[c] = sum_r dy * h,   db[c] = sum_r dy
+ *   dy, x   device, of dtype, row strides lddy and ldx (elements)
+ *   weight  device fp32 [cols] or NULL (1)
+ *   mean, rstd  device fp32 [rows], from the forward pass
+ *   dx      device, written: [rows][cols] of dtype; must not overlap dy or x
+ *   dw, db  device fp32 [cols], written; both NULL to leave them out
+ *   workspace  device, 16-byte aligned, workspace_bytes of scratch (at least
+ *           mxfp4_layernorm_backward_workspace); not read by a later call.
+ *           NULL only where dw and db are. Calls that run at the same time
+ *           need workspaces of their own.
+ */
+mxfp4_status mxfp4_layernorm_backward(const void* dy, const void* x, int dtype, int64_t rows,
+                                      int64_t cols, int64_t lddy, int64_t ldx,
+                                      const float* weight, const float* mean, const float* rstd,
+                                      void* dx, float* dw, float* db, void* workspace,
+                                      int64_t workspace_bytes, void* stream);
 
 /* Static text for a status code; never NULL. */
 const char* mxfp4_status_string(int status);

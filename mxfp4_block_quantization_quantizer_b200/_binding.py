@@ -6,6 +6,7 @@ with torch. Every step of the computation runs in the library's kernels.
 There is no fallback: if the library is missing, or a tensor is not on a CUDA
 device, the call raises.
 """
+import contextlib
 import ctypes
 import os
 
@@ -26,7 +27,8 @@ SYMBOLS = ("mxfp4_quantize", "mxfp4_quantize_oas", "mxfp4_dequantize",
            "mxfp4_rht_quantize", "mxfp4_rht_quantize_oas", "mxfp4_osc_step",
            "mxfp4_osc_synthetic_update", "mxfp4_qramp_step", "mxfp4_qema_quantize",
            "mxfp4_scales_to_blocked", "mxfp4_gemm", "mxfp4_gemm_quantize_a",
-           "mxfp4_status_string")
+           "mxfp4_layernorm", "mxfp4_layernorm_quantize", "mxfp4_layernorm_backward",
+           "mxfp4_layernorm_backward_workspace", "mxfp4_status_string")
 
 
 class Mxfp4Error(RuntimeError):
@@ -76,9 +78,19 @@ def lib():
             "mxfp4_gemm_quantize_a": [vp, i64, i64, i64, i32, u64, vp, vp, vp, vp,
                                       vp, vp, vp],
         }
+        f32 = ctypes.c_float
+        sig.update({
+            "mxfp4_layernorm": [vp, i32, i64, i64, i64, vp, vp, f32, vp, vp, vp, vp],
+            "mxfp4_layernorm_quantize": [vp, i32, i64, i64, i64, vp, vp, f32, vp, vp, vp, vp,
+                                         vp, vp],
+            "mxfp4_layernorm_backward": [vp, vp, i32, i64, i64, i64, i64, vp, vp, vp, vp, vp,
+                                         vp, vp, i64, vp],
+        })
         for name, args in sig.items():
             f = getattr(L, name)
             f.argtypes, f.restype = args, i32
+        L.mxfp4_layernorm_backward_workspace.argtypes = [i64, i64]
+        L.mxfp4_layernorm_backward_workspace.restype = i64
         L.mxfp4_status_string.argtypes = [i32]
         L.mxfp4_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -404,7 +416,161 @@ def gemm_quantize_a(x, b_codes, b_blocked, rounding=RNE, seed=0, out=None, want_
     return out
 
 
+def _device_of(t):
+    """Context in which t's device is the current one, where launches go."""
+    return torch.cuda.device(t.device) if t.is_cuda else contextlib.nullcontext()
+
+
+def _rows2d(t, name):
+    """A 2-D tensor whose rows are contiguous (they may lie apart, as in a
+    view of a wider tensor). Returns its row stride in elements."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("%s must be a CUDA tensor" % name)
+    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("%s must be a 2-D tensor with contiguous rows" % name)
+    _on_device(t, name)
+    if t.shape[0] <= 1:
+        return max(1, t.shape[1])
+    if t.stride(0) < t.shape[1]:
+        raise ValueError("the rows of %s overlap" % name)
+    return t.stride(0)
+
+
+def _apart(out, name, *inputs):
+    """Refuse an output whose storage range meets that of an input."""
+    for t in inputs:
+        if t.numel() and out.numel():
+            last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+            a0, a1 = t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
+            b0, b1 = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+            if a0 < b1 and b0 < a1:
+                raise ValueError("%s overlaps an input" % name)
+
+
+def _norm_inputs(x, weight, bias):
+    ldx = _rows2d(x, "x")
+    dt = _dtype_code(x)
+    for name, t in (("weight", weight), ("bias", bias)):
+        if t is not None:
+            _buffer(t, name, torch.float32, x.shape[1], x.device)
+    return ldx, dt
+
+
+def layernorm(x, weight=None, bias=None, eps=1e-5, want_stats=False, out=None, stream=None):
+    """mxfp4_layernorm: y = (x - mean) rstd weight + bias over the rows of x
+    (bf16 or fp32, contiguous rows, any row stride), weight and bias fp32
+    [cols] or None. Returns y, or (y, mean, rstd) with want_stats (out then
+    holds the three)."""
+    ldx, dt = _norm_inputs(x, weight, bias)
+    R, C = x.shape
+    d = x.device
+    if out is None:
+        out = torch.empty((R, C), dtype=x.dtype, device=d)
+        if want_stats:
+            out = (out, torch.empty(R, dtype=torch.float32, device=d),
+                   torch.empty(R, dtype=torch.float32, device=d))
+    y, mean, rstd = out if want_stats else (out, None, None)
+    _buffer(y, "out", x.dtype, R * C, d)
+    _apart(y, "out", x)
+    if want_stats:
+        _buffer(mean, "mean", torch.float32, R, d)
+        _buffer(rstd, "rstd", torch.float32, R, d)
+    with _device_of(x):
+        _check(lib().mxfp4_layernorm(_ptr(x), dt, R, C, ldx, _ptr(weight), _ptr(bias), eps,
+                                     _ptr(y), _ptr(mean), _ptr(rstd), _stream(d, stream)),
+               "mxfp4_layernorm")
+    return out
+
+
+def layernorm_quantize(x, weight=None, bias=None, eps=1e-5, want_y=False, want_stats=False,
+                       out=None, stream=None):
+    """mxfp4_layernorm_quantize: the ROWS-layout (codes, scales) of the
+    nearest-even quantization of layernorm(x, weight, bias, eps), and y, mean
+    and rstd where wanted: (codes, scales[, y][, mean, rstd])."""
+    ldx, dt = _norm_inputs(x, weight, bias)
+    R, C = x.shape
+    d = x.device
+    if out is None:
+        out = (_empty_u8((R, C // 2), d), _empty_u8((R, C // 32), d))
+        if want_y:
+            out += (torch.empty((R, C), dtype=x.dtype, device=d),)
+        if want_stats:
+            out += (torch.empty(R, dtype=torch.float32, device=d),
+                    torch.empty(R, dtype=torch.float32, device=d))
+    if len(out) != 2 + bool(want_y) + 2 * bool(want_stats):
+        raise ValueError("out must hold codes, scales and what is wanted beside them")
+    codes, scales = out[:2]
+    y = out[2] if want_y else None
+    mean, rstd = out[-2:] if want_stats else (None, None)
+    _buffer(codes, "codes", torch.uint8, R * C // 2, d)
+    _buffer(scales, "scales", torch.uint8, R * C // 32, d)
+    if want_y:
+        _buffer(y, "y", x.dtype, R * C, d)
+        _apart(y, "y", x)
+    if want_stats:
+        _buffer(mean, "mean", torch.float32, R, d)
+        _buffer(rstd, "rstd", torch.float32, R, d)
+    with _device_of(x):
+        _check(lib().mxfp4_layernorm_quantize(_ptr(x), dt, R, C, ldx, _ptr(weight), _ptr(bias),
+                                              eps, _ptr(y), _ptr(mean), _ptr(rstd), _ptr(codes),
+                                              _ptr(scales), _stream(d, stream)),
+               "mxfp4_layernorm_quantize")
+    return out
+
+
+def _workspace(workspace, need, device):
+    """A caller's workspace (uint8, at least `need` bytes) or a new one."""
+    if workspace is None:
+        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+    if not isinstance(workspace, torch.Tensor) or workspace.numel() < need:
+        raise ValueError("workspace must be a uint8 tensor of at least %d bytes" % need)
+    return _buffer(workspace, "workspace", torch.uint8, workspace.numel(), device)
+
+
+def layernorm_backward(dy, x, mean, rstd, weight=None, want_params=True, out=None,
+                       workspace=None, stream=None):
+    """mxfp4_layernorm_backward: (dx, dw, db) of layernorm for the gradient
+    dy of its output, with the forward pass's mean and rstd; dx alone with
+    want_params=False. dx has x's type, dw and db are fp32 (the gradients of
+    the weight and the bias). workspace: optional uint8 CUDA tensor."""
+    ldx, dt = _norm_inputs(x, weight, None)
+    lddy = _rows2d(dy, "dy")
+    if dy.dtype != x.dtype or dy.shape != x.shape:
+        raise ValueError("dy must have the type and shape of x")
+    _on_device(dy, "dy", x.device)
+    R, C = x.shape
+    d = x.device
+    _buffer(mean, "mean", torch.float32, R, d)
+    _buffer(rstd, "rstd", torch.float32, R, d)
+    if out is None:
+        out = torch.empty((R, C), dtype=x.dtype, device=d)
+        if want_params:
+            out = (out, torch.empty(C, dtype=torch.float32, device=d),
+                   torch.empty(C, dtype=torch.float32, device=d))
+    dx, dw, db = out if want_params else (out, None, None)
+    _buffer(dx, "out", x.dtype, R * C, d)
+    _apart(dx, "out", x, dy)
+    need = 0
+    if want_params:
+        _buffer(dw, "dw", torch.float32, C, d)
+        _buffer(db, "db", torch.float32, C, d)
+        need = lib().mxfp4_layernorm_backward_workspace(R, C)
+        workspace = _workspace(workspace, need, d)
+    else:
+        workspace = None
+    with _device_of(x):
+        _check(lib().mxfp4_layernorm_backward(_ptr(dy), _ptr(x), dt, R, C, lddy, ldx,
+                                              _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx),
+                                              _ptr(dw), _ptr(db), _ptr(workspace),
+                                              workspace.numel() if workspace is not None else 0,
+                                              _stream(d, stream)), "mxfp4_layernorm_backward")
+    return out
+
+
 # The C names, for callers that prefer them.
+mxfp4_layernorm = layernorm
+mxfp4_layernorm_quantize = layernorm_quantize
+mxfp4_layernorm_backward = layernorm_backward
 mxfp4_quantize = quantize
 
 

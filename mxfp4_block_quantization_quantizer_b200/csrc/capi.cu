@@ -257,6 +257,89 @@ mxfp4_status mxfp4_gemm_quantize_a(const void* x, int64_t m, int64_t n, int64_t 
                                          as_stream(stream)));
 }
 
+namespace {
+
+// An element-aligned pointer (NULL passes).
+bool aligned_to(const void* p, uintptr_t size) {
+  return (reinterpret_cast<uintptr_t>(p) & (size - 1)) == 0;
+}
+
+bool eps_ok(float eps) { return eps >= 0.0f && eps <= 3.4e38f; }
+
+// ld >= cols, and the strided rows stay within the size limit.
+bool stride_ok(int64_t rows, int64_t cols, int64_t ld) {
+  return ld >= cols && ld <= (int64_t(1) << 46) / rows;
+}
+
+mxfp4_status layernorm_args(const void* x, int dtype, int64_t rows, int64_t cols, int64_t ldx,
+                            const float* weight, const float* bias, float eps, const void* y,
+                            const float* mean, const float* rstd) {
+  if (!dtype_ok(dtype)) return MXFP4_ERR_ENUM;
+  if (!dims_ok(rows, cols) || !stride_ok(rows, cols, ldx)) return MXFP4_ERR_SHAPE;
+  if (!eps_ok(eps)) return MXFP4_ERR_VALUE;
+  const uintptr_t size = dtype == MXFP4_BF16 ? 2 : 4;
+  if (!aligned_to(x, size) || !aligned_to(y, size) || !aligned_to(weight, 4) ||
+      !aligned_to(bias, 4) || !aligned_to(mean, 4) || !aligned_to(rstd, 4))
+    return MXFP4_ERR_ALIGN;
+  return MXFP4_OK;
+}
+
+}  // namespace
+
+mxfp4_status mxfp4_layernorm(const void* x, int dtype, int64_t rows, int64_t cols,
+                             int64_t ldx, const float* weight, const float* bias, float eps,
+                             void* y, float* mean, float* rstd, void* stream) {
+  if (!x || !y) return MXFP4_ERR_NULL;
+  const mxfp4_status st =
+      layernorm_args(x, dtype, rows, cols, ldx, weight, bias, eps, y, mean, rstd);
+  if (st != MXFP4_OK) return st;
+  return from_cuda(mxfp4::launch_layernorm(x, dtype == MXFP4_BF16, rows, cols, ldx, weight,
+                                           bias, eps, y, mean, rstd, nullptr, nullptr,
+                                           as_stream(stream)));
+}
+
+mxfp4_status mxfp4_layernorm_quantize(const void* x, int dtype, int64_t rows, int64_t cols,
+                                      int64_t ldx, const float* weight, const float* bias,
+                                      float eps, void* y, float* mean, float* rstd,
+                                      uint8_t* codes, uint8_t* scales, void* stream) {
+  if (!x || !codes || !scales) return MXFP4_ERR_NULL;
+  const mxfp4_status st =
+      layernorm_args(x, dtype, rows, cols, ldx, weight, bias, eps, y, mean, rstd);
+  if (st != MXFP4_OK) return st;
+  if (cols % 32) return MXFP4_ERR_SHAPE;
+  if (!aligned16(codes)) return MXFP4_ERR_ALIGN;
+  return from_cuda(mxfp4::launch_layernorm(x, dtype == MXFP4_BF16, rows, cols, ldx, weight,
+                                           bias, eps, y, mean, rstd, codes, scales,
+                                           as_stream(stream)));
+}
+
+int64_t mxfp4_layernorm_backward_workspace(int64_t rows, int64_t cols) {
+  if (!dims_ok(rows, cols)) return -1;
+  return mxfp4::layernorm_backward_partials(rows) * 2 * cols * int64_t(sizeof(float));
+}
+
+mxfp4_status mxfp4_layernorm_backward(const void* dy, const void* x, int dtype, int64_t rows,
+                                      int64_t cols, int64_t lddy, int64_t ldx,
+                                      const float* weight, const float* mean, const float* rstd,
+                                      void* dx, float* dw, float* db, void* workspace,
+                                      int64_t workspace_bytes, void* stream) {
+  if (!dy || !x || !mean || !rstd || !dx || (dw == nullptr) != (db == nullptr) ||
+      (dw != nullptr && workspace == nullptr))
+    return MXFP4_ERR_NULL;
+  const mxfp4_status st =
+      layernorm_args(x, dtype, rows, cols, ldx, weight, nullptr, 0.0f, dx, mean, rstd);
+  if (st != MXFP4_OK) return st;
+  if (!stride_ok(rows, cols, lddy)) return MXFP4_ERR_SHAPE;
+  if (!aligned_to(dy, dtype == MXFP4_BF16 ? 2 : 4) || !aligned_to(dw, 4) ||
+      !aligned_to(db, 4) || !aligned16(workspace))
+    return MXFP4_ERR_ALIGN;
+  if (dw != nullptr && workspace_bytes < mxfp4_layernorm_backward_workspace(rows, cols))
+    return MXFP4_ERR_WORKSPACE;
+  return from_cuda(mxfp4::launch_layernorm_backward(
+      dy, x, dtype == MXFP4_BF16, rows, cols, lddy, ldx, weight, mean, rstd, dx, dw, db,
+      static_cast<float*>(workspace), as_stream(stream)));
+}
+
 const char* mxfp4_status_string(int status) {
   switch (status) {
     case MXFP4_OK: return "ok";
@@ -268,6 +351,8 @@ const char* mxfp4_status_string(int status) {
       return "a tensor pointer is not 16-byte aligned (a status word: 4-byte)";
     case MXFP4_ERR_ENUM: return "dtype, axis or rounding out of range";
     case MXFP4_ERR_CUDA: return "CUDA launch failed";
+    case MXFP4_ERR_VALUE: return "a numeric argument is outside its stated range";
+    case MXFP4_ERR_WORKSPACE: return "the workspace is too small";
     default: return "unknown status";
   }
 }

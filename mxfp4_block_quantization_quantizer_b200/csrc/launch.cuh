@@ -83,4 +83,24 @@ cudaError_t launch_gemm_qa(const void* x, int64_t m, int64_t n, int64_t k, bool 
                            uint8_t* a_codes, uint8_t* a_scales, int* status,
                            cudaStream_t s);
 
+// Layer norm of the rows of x (row stride ldx elements); weight, bias, y,
+// mean, rstd, codes/scales may be null (see mxfp4_layernorm_quantize).
+cudaError_t launch_layernorm(const void* x, bool bf16, int64_t rows, int64_t cols, int64_t ldx,
+                             const float* weight, const float* bias, float eps, void* y,
+                             float* mean, float* rstd, uint8_t* codes, uint8_t* scales,
+                             cudaStream_t s);
+
+// Partial rows of dw and db ([2][cols] floats each) that the backward pass
+// writes at most.
+constexpr int kLnMaxPartials = 592;
+constexpr int kLnWidePartials = 64;
+int64_t layernorm_backward_partials(int64_t rows);
+
+// Gradients of the layer norm; dw, db and partial are null together.
+cudaError_t launch_layernorm_backward(const void* dy, const void* x, bool bf16, int64_t rows,
+                                      int64_t cols, int64_t lddy, int64_t ldx,
+                                      const float* weight, const float* mean, const float* rstd,
+                                      void* dx, float* dw, float* db, float* partial,
+                                      cudaStream_t s);
+
 }  // namespace mxfp4

@@ -1,0 +1,259 @@
+"""Layer norm and its gradients against the formulas in 64 bits.
+
+Tolerances are forward error bounds of the kernels' fp32 arithmetic. With
+u = 2^-24: a sum over a row is at most `depth` additions deep (32 elements a
+thread, then at most 10 joining steps; wider rows add cols / 512), so it is
+off by at most depth u times the sum of magnitudes; every other operation
+adds u of its result; an output rounded to its type is off by half a step.
+"""
+import numpy as np
+import pytest
+import torch
+
+import mxfp4_block_quantization_quantizer_b200 as m
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+BF, F = torch.bfloat16, torch.float32
+SHAPES = [(1, 1), (1, 4096), (3, 5), (7, 48), (9, 63), (64, 384), (197, 1536), (700, 256),
+          (33, 1111), (620, 1111), (5, 16384), (3, 16392), (2, 20001), (2, 40000), (300, 8192),
+          (1300, 96), (1201, 2048), (310, 5000), (12, 9001)]
+
+
+def depth(cols):
+    return 64 + (cols // 512 if cols > 16384 else 0)
+
+
+def half_step(t):
+    return 0.5 * torch.finfo(t).eps
+
+
+def inputs(rows, cols, dt, seed, offset=0.0):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    chan = torch.exp2(6 * torch.rand(cols, generator=g, device="cuda") - 3)
+    x = (torch.randn(rows, cols, generator=g, device="cuda") * chan + offset).to(dt)
+    dy = torch.randn(rows, cols, generator=g, device="cuda").to(dt)
+    w = 1 + 0.3 * torch.randn(cols, generator=g, device="cuda")
+    b = 0.2 * torch.randn(cols, generator=g, device="cuda")
+    return x, dy, w, b
+
+
+def forward64(x, w, b, eps):
+    x = x.double()
+    mean = x.mean(1, keepdim=True)
+    var = (x - mean).square().mean(1, keepdim=True)
+    rstd = (var + eps) ** -0.5
+    h = (x - mean) * rstd
+    y = h if w is None else h * w.double()
+    return (y if b is None else y + b.double()), mean, rstd, h
+
+
+def check_forward(x, w, b, eps, got, mean, rstd):
+    y, mu, rs, h = forward64(x, w, b, eps)
+    d = depth(x.shape[1])
+    aw = 1.0 if w is None else w.double().abs()
+    ab = 0.0 if b is None else b.double().abs()
+    dm = d * U * x.double().abs().mean(1, keepdim=True)      # of the mean
+    dr = d * U + (dm * rs) ** 2                              # of rstd, relative
+    tol = aw * (dm * rs + h.abs() * dr) + 4 * U * (y.abs() + ab) + 1e-30
+    tol = tol + half_step(x.dtype) * (y.abs() + tol)
+    assert ((got.double() - y).abs() <= tol).all(), ((got.double() - y).abs() / tol).max()
+    assert ((mean.double() - mu[:, 0]).abs() <= dm[:, 0] + 1e-37).all()
+    assert ((rstd.double() - rs[:, 0]).abs() <= dr[:, 0] * rs[:, 0]).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_forward(shape, dt):
+    x, _, w, b = inputs(*shape, dt, 1)
+    check_forward(x, w, b, 1e-5, *m.layernorm(x, w, b, want_stats=True))
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("use_w,use_b", [(False, False), (True, False), (False, True)])
+def test_forward_without_parameters(dt, use_w, use_b):
+    x, _, w, b = inputs(40, 768, dt, 2)
+    w, b = (w if use_w else None), (b if use_b else None)
+    y, mean, rstd = m.layernorm(x, w, b, 1e-6, want_stats=True)
+    check_forward(x, w, b, 1e-6, y, mean, rstd)
+    assert torch.equal(m.layernorm(x, w, b, 1e-6), y)
+
+
+@pytest.mark.parametrize("cols", [768, 771, 18000])
+def test_forward_with_a_large_offset(cols):
+    """A common offset of 1e4 in fp32 data of unit size: the squares are
+    summed around the mean, so only x itself has lost bits."""
+    x, _, w, b = inputs(50, cols, F, 3, offset=1e4)
+    check_forward(x, w, b, 1e-5, *m.layernorm(x, w, b, want_stats=True))
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("cols", [96, 1000, 1003, 17000])
+def test_strided_and_unaligned_rows(dt, cols):
+    """Views of a wider tensor: class tokens (every third row), and columns
+    that start off a 16-byte boundary."""
+    x, dy, w, b = inputs(60, 2 * cols + 1, dt, 4)
+    for xv, dv in ((x[::3, :cols], dy[1::3, 8:cols + 8]), (x[:, 1:cols + 1], dy[:, :cols])):
+        y, mean, rstd = m.layernorm(xv, w[:cols], b[:cols], want_stats=True)
+        assert y.is_contiguous()
+        check_forward(xv, w[:cols], b[:cols], 1e-5, y, mean, rstd)
+        check_backward(dv, xv, mean, rstd, w[:cols],
+                       *m.layernorm_backward(dv, xv, mean, rstd, w[:cols].clone()))
+    ws = torch.zeros(cols + 1, device="cuda")[1:]     # a weight off a 16-byte boundary
+    ws.copy_(w[:cols])
+    xc = x[:, :cols].contiguous()
+    assert torch.allclose(m.layernorm(xc, ws, b[:cols]).float(),
+                          m.layernorm(xc, w[:cols].contiguous(), b[:cols]).float(),
+                          rtol=2 * half_step(dt) + 64 * U, atol=1e-5)
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("cols", [512, 515, 17001])
+def test_special_rows(dt, cols):
+    """A constant row gives the bias; rows with NaN or Inf give NaN and touch
+    no other row; magnitudes near the type's ends stay finite."""
+    x, _, w, b = inputs(8, cols, dt, 5)
+    x[1] = 3.5
+    x[2, cols // 2] = float("nan")
+    x[3, 1] = float("inf")
+    x[4] *= 2.0 ** 50
+    x[5] *= 2.0 ** -60
+    y, mean, rstd = m.layernorm(x, w, b, want_stats=True)
+    assert torch.isnan(y[2]).all() and torch.isnan(y[3]).all()
+    keep = [0, 1, 4, 5, 6, 7]
+    check_forward(x[keep], w, b, 1e-5, y[keep], mean[keep], rstd[keep])
+
+
+def check_backward(dy, x, mean, rstd, w, dx, dw=None, db=None):
+    rows, cols = x.shape
+    dyd, rs = dy.double(), rstd.double()[:, None]
+    h = (x.double() - mean.double()[:, None]) * rs
+    g = dyd if w is None else dyd * w.double()
+    c1, c2 = g.mean(1, keepdim=True), (g * h).mean(1, keepdim=True)
+    want = rs * (g - c1 - h * c2)
+    d = depth(cols)
+    tol = rs.abs() * (4 * U * g.abs() + d * U * g.abs().mean(1, keepdim=True)
+                      + h.abs() * ((d + 4) * U * (g * h).abs().mean(1, keepdim=True)
+                                   + 4 * U * c2.abs())) + 4 * U * want.abs() + 1e-30
+    tol = tol + half_step(x.dtype) * (want.abs() + tol)
+    assert ((dx.double() - want).abs() <= tol).all(), ((dx.double() - want).abs() / tol).max()
+    if dw is not None:
+        # at most rows / 148 rows in one chain (fewer CTAs only where there
+        # are fewer rows; 64 chains for wide rows), then the partial rows
+        r = rows / 64 + 64
+        for got, terms in ((dw, dyd * h), (db, dyd)):
+            bound = (r + 4) * U * terms.abs().sum(0) + 1e-30
+            assert ((got.double() - terms.sum(0)).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("shape", SHAPES)
+def test_backward(shape, dt):
+    x, dy, w, _ = inputs(*shape, dt, 6)
+    _, mean, rstd = m.layernorm(x, w, want_stats=True)
+    out = m.layernorm_backward(dy, x, mean, rstd, w)
+    check_backward(dy, x, mean, rstd, w, *out)
+    dx = m.layernorm_backward(dy, x, mean, rstd, w, want_params=False)
+    check_backward(dy, x, mean, rstd, w, dx)
+    for a, b in zip(out, m.layernorm_backward(dy, x, mean, rstd, w)):
+        assert torch.equal(a, b)      # no order left to chance
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+def test_backward_without_weight(dt):
+    x, dy, _, _ = inputs(77, 640, dt, 7)
+    _, mean, rstd = m.layernorm(x, want_stats=True)
+    check_backward(dy, x, mean, rstd, None, *m.layernorm_backward(dy, x, mean, rstd))
+
+
+def test_backward_against_differences():
+    """Directional derivative of sum(c y) against a central difference of the
+    formula in 64 bits: step s gives an error of order s^2."""
+    x, c, w, b = inputs(6, 40, F, 8)
+    _, mean, rstd = m.layernorm(x, w, b, want_stats=True)
+    dx, dw, db = (t.double() for t in m.layernorm_backward(c, x, mean, rstd, w))
+    g = torch.Generator(device="cuda")
+    g.manual_seed(9)
+    vx, vw, vb = (torch.randn(t.shape, generator=g, device="cuda").double() for t in (x, w, b))
+    s = 1e-5
+    f = lambda k: (c.double() * forward64(x.double() + k * vx, w.double() + k * vw,
+                                          b.double() + k * vb, 1e-5)[0]).sum()
+    want = (f(s) - f(-s)) / (2 * s)
+    got = (dx * vx).sum() + (dw * vw).sum() + (db * vb).sum()
+    # fp32 gradients: each is off by a few hundred u of its terms' magnitudes
+    bound = 512 * U * ((dx * vx).abs().sum() + (dw * vw).abs().sum() + (db * vb).abs().sum())
+    assert (got - want).abs() <= bound + 1e-4 * s * want.abs()
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("shape", [(1, 32), (5, 96), (64, 384), (197, 1536), (400, 1024),
+                                   (6, 16384), (3, 16416), (2, 32768), (600, 4096)])
+def test_quantize_is_the_quantizer_of_the_norm(shape, dt):
+    x, _, w, b = inputs(*shape, dt, 10)
+    if shape[0] > 4:
+        x[1] = 0
+        x[2, 3] = float("nan")
+        x[3] *= 2.0 ** 40
+    y, mean, rstd = m.layernorm(x, w, b, want_stats=True)
+    codes, scales = m.quantize(y)
+    got = m.layernorm_quantize(x, w, b, want_y=True, want_stats=True)
+    same = lambda a, c: torch.equal(a.view(torch.uint8), c.view(torch.uint8))
+    assert torch.equal(got[0], codes) and torch.equal(got[1], scales)
+    assert same(torch.nan_to_num(got[2]), torch.nan_to_num(y))
+    assert same(torch.nan_to_num(got[3]), torch.nan_to_num(mean))
+    alone = m.layernorm_quantize(x, w, b)
+    assert torch.equal(alone[0], codes) and torch.equal(alone[1], scales)
+
+
+def test_outputs_end_where_they_should():
+    """Bytes on both sides of every output stay as they were."""
+    for rows, cols, dt in ((5, 1111, BF), (9, 4096, F), (3, 20001, F), (700, 40, BF)):
+        x, dy, w, b = inputs(rows, cols, dt, 11)
+        n = rows * cols
+        bufs = [torch.full((64 + k + 64,), 7.0, dtype=t, device="cuda")
+                for k, t in ((n, dt), (rows, F), (rows, F), (n, dt), (cols, F), (cols, F))]
+        y, mean, rstd, dx, dw, db = (t[64:-64] for t in bufs)
+        m.layernorm(x, w, b, want_stats=True, out=(y.view(rows, cols), mean, rstd))
+        m.layernorm_backward(dy, x, mean, rstd, w, out=(dx.view(rows, cols), dw, db))
+        torch.cuda.synchronize()
+        for t in bufs:
+            assert (t[:64] == 7).all() and (t[-64:] == 7).all()
+
+
+def test_captured_and_replayed():
+    """Forward and backward in one graph, replayed on new inputs, while eager
+    calls run between the replays."""
+    x, dy, w, b = inputs(300, 1536, BF, 12)
+    ws = torch.empty(m.lib().mxfp4_layernorm_backward_workspace(300, 1536), dtype=torch.uint8,
+                     device="cuda")
+    step = lambda: m.layernorm_backward(dy, x, *m.layernorm(x, w, b, want_stats=True)[1:], w,
+                                        workspace=ws)
+    step()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed in (13, 14):
+        x2, dy2, _, _ = inputs(300, 1536, BF, seed)
+        x.copy_(x2), dy.copy_(dy2)
+        graph.replay()
+        eager = m.layernorm_backward(dy2, x2, *m.layernorm(x2, w, b, want_stats=True)[1:], w)
+        for a, c in zip(out, eager):
+            assert torch.equal(a, c)
+
+
+def test_two_streams_at_once():
+    x, dy, w, b = inputs(2000, 1024, BF, 15)
+    want = m.layernorm_backward(dy, x, *m.layernorm(x, w, b, want_stats=True)[1:], w)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for s in streams:
+        _, mean, rstd = m.layernorm(x, w, b, want_stats=True, stream=s)
+        s.synchronize()
+        with torch.cuda.stream(s):
+            got.append(m.layernorm_backward(dy, x, mean, rstd, w))
+    torch.cuda.synchronize()
+    for g in got:
+        for a, c in zip(g, want):
+            assert torch.equal(a, c)
