@@ -393,6 +393,38 @@ mxfp4_status mxfp4_gemm_quantize_a(const void* x, int64_t m, int64_t n, int64_t 
                                    uint8_t* a_scales, int* status, void* stream);
 
 /*
+ * Product of a few unquantized rows with an MXFP4 weight, the step a model
+ * answers single tokens with (m = 1 to a few dozen):
+ *   Y[m][n] = sum_k X[m][k] * B[n][k]         (fp32 accumulate)
+ * X is bf16 and is not quantized; B is given as in mxfp4_gemm. The products
+ * run on the block-scaled tensor cores: each x enters as the sum of two E4M3
+ * values with a power-of-two scale per 32 elements each, which is x exactly
+ * unless |x| is below 2^-13 of the largest magnitude of its group of 32, and
+ * off by at most 2^-21 of that magnitude then. Sums are fp32; Y is rounded
+ * once. The sums of one call do not depend on anything but its arguments
+ * (the same bits every time).
+ *   x        device bf16, row i at x + i * ldx elements; 16-byte aligned,
+ *            ldx >= k a multiple of 8
+ *   b_codes  device [n][k/2], 16-byte aligned (32-byte aligned codes with k
+ *            a multiple of 128 take the tensor cores, other ones the
+ *            slower CUDA cores, which take x as it is)
+ *   b_scales device, blocked order (rows = n, groups = k/32), 16-byte aligned
+ *   y        device [m][n] of y_dtype, 16-byte aligned, written; must not
+ *            overlap x
+ *   status   device int or NULL (MXFP4_STATUS_WAIT_TIMEOUT above); the tiles
+ *            of a CTA whose wait ran out hold NaN
+ * k must be a multiple of 32, m at most 2^19. A group of x that holds Inf or
+ * NaN gives NaN in its row of Y, a scale byte of 0xFF in its column.
+ * Any m works; from about a hundred rows on, quantizing X (mxfp4_gemm) or
+ * decoding B (mxfp4_dequantize) and a dense product are faster.
+ * Source: "Microscaling FP4 Quantization: MR-GPTQ Achieves 6x Speedup"
+ * (inference with MXFP4 weights).
+ */
+mxfp4_status mxfp4_gemv(const void* x, int64_t m, int64_t n, int64_t k, int64_t ldx,
+                        const uint8_t* b_codes, const uint8_t* b_scales, void* y, int y_dtype,
+                        int* status, void* stream);
+
+/*
  * Layer norm of every row of X, the transform in front of a quantized linear
  * layer (pre-norm blocks of the pages' vision transformers and LLMs):
  *   mean = sum_c X[r][c] / cols,   var = sum_c (X[r][c] - mean)^2 / cols,

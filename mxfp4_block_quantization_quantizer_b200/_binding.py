@@ -27,7 +27,7 @@ SYMBOLS = ("mxfp4_quantize", "mxfp4_quantize_oas", "mxfp4_dequantize",
            "mxfp4_rht_quantize", "mxfp4_rht_quantize_oas", "mxfp4_osc_step",
            "mxfp4_osc_synthetic_update", "mxfp4_qramp_step", "mxfp4_qema_quantize",
            "mxfp4_scales_to_blocked", "mxfp4_gemm", "mxfp4_gemm_quantize_a",
-           "mxfp4_layernorm", "mxfp4_layernorm_quantize", "mxfp4_layernorm_backward",
+           "mxfp4_gemv", "mxfp4_layernorm", "mxfp4_layernorm_quantize", "mxfp4_layernorm_backward",
            "mxfp4_layernorm_backward_workspace", "mxfp4_status_string")
 
 
@@ -80,6 +80,7 @@ def lib():
         }
         f32 = ctypes.c_float
         sig.update({
+            "mxfp4_gemv": [vp, i64, i64, i64, i64, vp, vp, vp, i32, vp, vp],
             "mxfp4_layernorm": [vp, i32, i64, i64, i64, vp, vp, f32, vp, vp, vp, vp],
             "mxfp4_layernorm_quantize": [vp, i32, i64, i64, i64, vp, vp, f32, vp, vp, vp, vp,
                                          vp, vp],
@@ -447,6 +448,36 @@ def _apart(out, name, *inputs):
                 raise ValueError("%s overlaps an input" % name)
 
 
+def gemv(x, b_codes, b_blocked, out_dtype=torch.bfloat16, out=None, stream=None, status=None):
+    """mxfp4_gemv: Y = x B^T for a few bf16 rows x [m, k] (contiguous rows,
+    any row stride that is a multiple of 8; not quantized) and an MXFP4
+    weight B given as K-major codes [n, k/2] and blocked scales. Y is bf16 or
+    fp32 [m, n]. status: optional int32 CUDA tensor of one element, the
+    timeout status word."""
+    ldx = _rows2d(x, "x")
+    if x.dtype != torch.bfloat16:
+        raise TypeError("x must be bfloat16")
+    m, k = x.shape
+    d = x.device
+    _cuda2d(b_codes, "b_codes")
+    n = b_codes.shape[0]
+    _buffer(b_codes, "b_codes", torch.uint8, n * k // 2, d)
+    if b_codes.shape[1] * 2 != k:
+        raise ValueError("b_codes must have k/2 bytes per row")
+    _buffer(b_blocked, "b_blocked", torch.uint8, -(-n // 128) * 128 * (-(-k // 128) * 4), d)
+    if out is None:
+        out = torch.empty((m, n), dtype=out_dtype, device=d)
+    else:
+        _buffer(out, "out", out.dtype, m * n, d)
+        _apart(out, "out", x)
+    dt = _dtype_code(out)
+    st = _status_word(status, d)
+    with _device_of(x):
+        _check(lib().mxfp4_gemv(_ptr(x), m, n, k, ldx, _ptr(b_codes), _ptr(b_blocked), _ptr(out),
+                                dt, st, _stream(d, stream)), "mxfp4_gemv")
+    return out
+
+
 def _norm_inputs(x, weight, bias):
     ldx = _rows2d(x, "x")
     dt = _dtype_code(x)
@@ -568,6 +599,7 @@ def layernorm_backward(dy, x, mean, rstd, weight=None, want_params=True, out=Non
 
 
 # The C names, for callers that prefer them.
+mxfp4_gemv = gemv
 mxfp4_layernorm = layernorm
 mxfp4_layernorm_quantize = layernorm_quantize
 mxfp4_layernorm_backward = layernorm_backward

@@ -1,0 +1,574 @@
+// Products of a few bf16 rows with an MXFP4 weight (sm_100a):
+//   Y[t][i] = sum_k X[t][k] W[i][k],  W[i][k] = G(code) 2^(scale byte - 127)
+// with one scale per 32 elements along k. X is not quantized: this is the
+// product a model answers with, where mxfp4_gemm's 4-bit activations would
+// cost accuracy and where a step reads the whole weight for a few rows.
+//
+// Bound by reading the weight once (17/32 byte per element). The tensor cores
+// take E2M1 operands directly, so the weight goes from memory to them without
+// passing through a register: a tensor-memory-access (TMA) load spreads each
+// 16 packed codes over 16 bytes of shared memory (the operand layout of
+// kind::mxf8f6f4), the blocked scale tile is copied to tensor memory, and one
+// thread issues the MMAs. Decoding on the CUDA cores instead costs about 1.5
+// instructions per weight, 2 issue slots per clock and SM of the 4 there are
+// at full memory speed, before any arithmetic on x.
+//
+// X as an MMA operand: every bf16 x is split into two E4M3 values with a
+// power-of-two scale per 32 elements of each,
+//   hi = e4m3(x 2^-s),  lo = e4m3((x - hi 2^s) 2^-s'),
+// s from the group's largest |x| and s' from its largest remainder. hi keeps
+// 4 of bf16's 8 significant bits and lo the other 4, so the split is exact
+// unless |x| is below 2^-13 of its group's maximum, and off by at most 2^-21
+// of that maximum then (the products are summed in fp32). hi and lo are two
+// rows of the B operand, their products two accumulator columns that the
+// epilogue adds.
+//
+// One CTA takes 128 weight rows, T tokens (N = 2 T columns) and a slab of k;
+// the CTAs of a cluster take the slabs of the same rows and add their sums
+// through distributed shared memory in the order of their ranks (no atomics).
+//   warp 0:    one thread issues the loads of codes (128 rows x 128 k) and
+//              scale tiles into a ring of stages;
+//   warp 1:    tensor memory; one thread issues per stage the two scale
+//              copies and four MMAs (M = 128, N = 2 T, K = 32);
+//   warps 2-5: split X into the stages (warp w takes stages w, w + 4, ...),
+//              then read the accumulator and store Y.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "launch.cuh"
+#include "mxfp4_device.cuh"
+#include "tc_common.cuh"
+
+namespace mxfp4 {
+
+namespace {
+
+constexpr int kVM = 128;                 // weight rows of a CTA
+constexpr int kVWorkers = 4;
+constexpr int kVThreads = 32 * (2 + kVWorkers);
+constexpr uint32_t kVNaN = 0x7FC00000u;
+
+template <int T>
+struct VLayout {
+  static constexpr int kN = 2 * T;
+  static constexpr int kStages = T <= 16 ? 5 : (T == 32 ? 4 : 3);
+  static constexpr uint32_t kA = kVM * 128, kB = kN * 128, kSf = 512;
+  // per ring: codes, x planes, scales of both
+  static constexpr uint32_t kAOff = 0;
+  static constexpr uint32_t kBOff = kAOff + kStages * kA;
+  static constexpr uint32_t kSfaOff = kBOff + kStages * kB;
+  static constexpr uint32_t kSfbOff = kSfaOff + kStages * kSf;
+  static constexpr uint32_t kBarOff = kSfbOff + kStages * kSf;
+  static constexpr uint32_t kBytes = kBarOff + 256;
+  static constexpr uint32_t kTmemCols = kN + 8 <= 32 ? 32 : (kN + 8 <= 64 ? 64 : (kN + 8 <= 128 ? 128 : 256));
+  static constexpr uint32_t kSfaCol = kN, kSfbCol = kN + 4;
+  // kind::mxf8f6f4: A E2M1 (5), B E4M3 (0), both K-major, N / 8, E8M0
+  // scales, M / 16
+  static constexpr uint32_t kIdesc =
+      (5u << 7) | (0u << 10) | (uint32_t(kN >> 3) << 17) | (1u << 23) | (uint32_t(kVM >> 4) << 24);
+};
+
+__device__ __forceinline__ void mma_mxf8f6f4(uint32_t tmem_c, uint64_t adesc, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate, uint32_t tsfa,
+                                             uint32_t tsfb) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.block32 [%0], %1, %2, "
+      "%3, [%5], [%6], p;\n\t}\n" ::"r"(tmem_c),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(tsfa), "r"(tsfb));
+}
+
+__device__ __forceinline__ void v_copy_scales(uint32_t taddr, const void* tile) {
+  const uint64_t d = smem_desc(tile, 16, 128);
+  asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d));
+}
+
+__device__ __forceinline__ void v_bulk_load(void* dst, const void* src, uint32_t bytes,
+                                            unsigned long long* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], "
+      "%2, [%3];" ::"r"(smem_u32(dst)),
+      "l"(src), "r"(bytes), "r"(smem_u32(bar))
+      : "memory");
+}
+
+// wait_parity_or_failed with a lower limit (these kernels run for
+// microseconds): gives up as soon as another role of the CTA has.
+constexpr long long kVWaitLimit = 1ll << 20;
+__device__ __forceinline__ bool v_wait(unsigned long long* bar, uint32_t parity,
+                                       const int* failed, long long limit = kVWaitLimit) {
+  const uint32_t a = smem_u32(bar);
+  for (long long i = 0; i < limit; ++i) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(done)
+        : "r"(a), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (failed != nullptr && (i & 63) == 63 && failed_flag(failed)) return false;
+  }
+  return false;
+}
+
+__device__ __forceinline__ uint32_t v_cluster_rank() {
+  uint32_t r;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void v_cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float v_peer_load(uint32_t a, uint32_t rank) {
+  uint32_t d;
+  float v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(rank));
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(d) : "memory");
+  return v;
+}
+
+// E4M3 code pairs (nearest, saturating at 448) of two fp32 values, and back.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
+  uint16_t d;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+__device__ __forceinline__ void e4m3x2_decode(uint32_t c, float* out) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 t;\n\tcvt.u16.u32 t, %1;\n\t"
+      "cvt.rn.f16x2.e4m3x2 %0, t;\n\t}"
+      : "=r"(h)
+      : "r"(c));
+  asm("{\n\t.reg .f16 l, u;\n\t"
+      "mov.b32 {l, u}, %2;\n\t"
+      "cvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, u;\n\t}"
+      : "=f"(out[0]), "=f"(out[1])
+      : "r"(h));
+}
+
+// Scale byte that puts a maximum of the given fp32 bit pattern into
+// [128, 256) (smaller where the byte stops at 0); 0xFF for Inf and NaN.
+__device__ __forceinline__ uint32_t plane_scale(uint32_t amax_bits) {
+  const uint32_t E = amax_bits >> 23;
+  return amax_bits >= 0x7F800000u ? 0xFFu : (E > 7u ? E - 7u : 0u);
+}
+
+// Both planes of 8 values of a group that 4 adjacent lanes share.
+struct Planes {
+  uint2 hi, lo;
+  uint32_t s_hi, s_lo;
+};
+__device__ __forceinline__ Planes split8(uint4 raw) {
+  Planes p;
+  uint32_t am = bf16x8_absmax(raw);
+  am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
+  am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
+  p.s_hi = plane_scale(am);
+  const bool bad = p.s_hi == 0xFFu;
+  const float mul = inv_scale(p.s_hi);
+  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+  float r[8];
+  uint32_t c[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float a = __fmul_rn(bf16_lo(w[j]), mul), b = __fmul_rn(bf16_hi(w[j]), mul);
+    c[j] = e4m3x2(a, b);
+    float d[2];
+    e4m3x2_decode(c[j], d);
+    r[2 * j] = __fsub_rn(a, d[0]);  // exact: in units of 2^s_hi
+    r[2 * j + 1] = __fsub_rn(b, d[1]);
+  }
+  p.hi = bad ? make_uint2(0, 0) : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  uint32_t rm = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) rm = max(rm, __float_as_uint(r[j]) & 0x7FFFFFFFu);
+  if (bad) rm = 0;
+  rm = max(rm, __shfl_xor_sync(0xFFFFFFFFu, rm, 1));
+  rm = max(rm, __shfl_xor_sync(0xFFFFFFFFu, rm, 2));
+  // the remainders are at most 8 (half a step of 4 significant bits); the
+  // remainders get a scale of their own, relative to s_hi and never below
+  // 2^-127 (remainders below 2^-113 of s_hi, far under fp32's reach, shrink)
+  const uint32_t E = rm >> 23;
+  int rel = rm == 0 ? 0 : max(int(E) - 127 - 7, -120);
+  if (int(p.s_hi) + rel < 0) rel = -int(p.s_hi);
+  p.s_lo = bad ? 0u : uint32_t(int(p.s_hi) + rel);
+  const float mul2 = __uint_as_float(uint32_t(127 - rel) << 23);
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    c[j] = e4m3x2(__fmul_rn(r[2 * j], mul2), __fmul_rn(r[2 * j + 1], mul2));
+  p.lo = bad ? make_uint2(0, 0) : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  return p;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
+  if (BF16)
+    static_cast<uint16_t*>(y)[at] = uint16_t(pack_bf16x2(v, 0.0f));
+  else
+    static_cast<float*>(y)[at] = v;
+}
+
+template <int T, bool BF16>
+__global__ void __launch_bounds__(kVThreads)
+    k_gemv(const __grid_constant__ CUtensorMap tm_w, const uint8_t* __restrict__ sfw,
+           const uint16_t* __restrict__ x, int64_t ldx, int m, int64_t n, int kblocks, int split,
+           void* __restrict__ y, int* __restrict__ status) {
+  using L = VLayout<T>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned long long* full = reinterpret_cast<unsigned long long*>(sm + L::kBarOff);
+  unsigned long long* empty = full + L::kStages;
+  unsigned long long* acc_full = empty + L::kStages;
+  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(acc_full + 1);
+  int* failed = reinterpret_cast<int*>(tmem_base + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rank = split > 1 ? int(v_cluster_rank()) : 0;
+  const int64_t tile = blockIdx.x / split;
+  const int64_t n0 = tile * kVM;
+  const int t0 = int(blockIdx.y) * T;
+  const int tokens = min(T, m - t0);
+  // this CTA's slab of 128-element k blocks
+  const int kb0 = int(int64_t(kblocks) * rank / split);
+  const int kb1 = int(int64_t(kblocks) * (rank + 1) / split);
+
+  if (tid == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 2;" ::"r"(smem_u32(&full[s])));
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&empty[s])));
+    }
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(acc_full)));
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    *failed = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_base)),
+                 "r"(L::kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  if (warp >= 2) {
+    // rows of absent tokens stay zero, and so do their scales
+    uint4* b = reinterpret_cast<uint4*>(sm + L::kBOff);
+    for (int i = tid - 64; i < int(L::kStages * L::kB / 16); i += 32 * kVWorkers)
+      b[i] = make_uint4(0, 0, 0, 0);
+    uint4* f = reinterpret_cast<uint4*>(sm + L::kSfbOff);
+    for (int i = tid - 64; i < int(L::kStages * L::kSf / 16); i += 32 * kVWorkers)
+      f[i] = make_uint4(0, 0, 0, 0);
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;");
+  const uint32_t tmem = *tmem_base;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t s = 0, ph = 0, issued = 0, last_ph = 0;
+      const uint8_t* sf = sfw + tile * kblocks * 512;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!v_wait(&empty[s], ph ^ 1u, failed)) {
+          atomicExch(failed, 1);
+          break;
+        }
+        issued |= 1u << s;
+        last_ph = (last_ph & ~(1u << s)) | (ph << s);
+        // the load counts the packed codes: half of the bytes it fills
+        expect_tx(&full[s], L::kA / 2 + L::kSf);
+        tma_load_2d(sm + L::kAOff + s * L::kA, &tm_w, kb * 128, int(n0), &full[s]);
+        v_bulk_load(sm + L::kSfaOff + s * L::kSf, sf + int64_t(kb) * 512, L::kSf, &full[s]);
+        if (++s == L::kStages) s = 0, ph ^= 1u;
+      }
+      // every load has landed before the CTA can end (the workers' arrival
+      // completes the phase too; after a failure the wait is only bounded)
+      for (uint32_t st = 0; st < L::kStages; ++st)
+        if ((issued >> st) & 1u) v_wait(&full[st], (last_ph >> st) & 1u, nullptr);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t s = 0, ph = 0;
+      bool ok = true;
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!v_wait(&full[s], ph, failed)) {
+          ok = false;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;");
+        v_copy_scales(tmem + L::kSfaCol, sm + L::kSfaOff + s * L::kSf);
+        v_copy_scales(tmem + L::kSfbCol, sm + L::kSfbOff + s * L::kSf);
+        const uint64_t ad = smem_desc_sw128(sm + L::kAOff + s * L::kA);
+        const uint64_t bd = smem_desc_sw128(sm + L::kBOff + s * L::kB);
+#pragma unroll
+        for (uint32_t g = 0; g < 4; ++g)
+          mma_mxf8f6f4(tmem, ad + 2 * g, bd + 2 * g, L::kIdesc | (g << 29) | (g << 4),
+                       (kb > kb0 || g > 0) ? 1u : 0u, (tmem + L::kSfaCol) | (g << 30),
+                       (tmem + L::kSfbCol) | (g << 30));
+        commit_to(&empty[s]);
+        if (++s == L::kStages) s = 0, ph ^= 1u;
+      }
+      if (!ok) atomicExch(failed, 1);
+      commit_to(acc_full);
+      // the MMAs issued have completed before shared or tensor memory goes
+      if (!v_wait(acc_full, 0, nullptr)) atomicExch(failed, 1);
+    }
+    __syncwarp();
+  } else {
+    // split X: warp w takes every fourth stage; a lane holds 8 elements of a
+    // token's 128 (16 lanes a token), two tokens a round
+    const int w = warp - 2;
+    const int half = lane >> 4, l16 = lane & 15;
+    constexpr int kRounds = T / 2;
+    constexpr int kBatch = kRounds < 4 ? kRounds : 4;  // loads in flight
+    uint4 raw[kBatch];
+    bool ok = true;
+    for (int kb = kb0 + w; kb < kb1 && ok; kb += kVWorkers) {
+      const int it = kb - kb0;
+      const uint32_t s = uint32_t(it % L::kStages), ph = uint32_t(it / L::kStages) & 1u;
+      const uint16_t* xp = x + int64_t(kb) * 128 + l16 * 8;
+      for (int r0 = 0; r0 < kRounds && 2 * r0 < tokens; r0 += kBatch) {
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int t = 2 * (r0 + j) + half;
+          raw[j] = t < tokens ? ld_l1(xp + int64_t(t0 + t) * ldx) : make_uint4(0, 0, 0, 0);
+        }
+        if (r0 == 0) {
+          ok = __all_sync(0xFFFFFFFFu, v_wait(&empty[s], ph ^ 1u, failed));
+          if (!ok) break;
+        }
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+          const int t = 2 * (r0 + j) + half;
+          if (2 * (r0 + j) >= tokens) break;
+          const Planes p = split8(raw[j]);
+          if (t < tokens) {
+            uint8_t* b = sm + L::kBOff + s * L::kB;
+            // row r of the 128-byte swizzled K-major operand: 16-byte chunk
+            // c at c ^ (r % 8); this lane's 8 codes are half a chunk
+            const uint32_t c = uint32_t(l16 >> 1), o = uint32_t(l16 & 1) * 8;
+            const uint32_t rl = uint32_t(T + t);
+            *reinterpret_cast<uint2*>(b + t * 128 + ((c ^ (t & 7)) << 4) + o) = p.hi;
+            *reinterpret_cast<uint2*>(b + rl * 128 + ((c ^ (rl & 7)) << 4) + o) = p.lo;
+            if ((lane & 3) == 0) {
+              uint8_t* f = sm + L::kSfbOff + s * L::kSf + (l16 >> 2);
+              f[16 * (t & 31) + 4 * (t >> 5)] = uint8_t(p.s_hi);
+              f[16 * (rl & 31) + 4 * (rl >> 5)] = uint8_t(p.s_lo);
+            }
+          }
+        }
+      }
+      if (!ok) {
+        atomicExch(failed, 1);
+        break;
+      }
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&full[s]))
+                     : "memory");
+    }
+  }
+  __syncthreads();
+
+  // epilogue: worker warp with lane quarter q holds rows 32 q + lane
+  float* part = reinterpret_cast<float*>(sm);  // [T][128], over the ring
+  if (warp >= 2) {
+    asm volatile("tcgen05.fence::after_thread_sync;");
+    const bool bad = failed_flag(failed) || !v_wait(acc_full, 0, nullptr, kAccWaitLimit);
+    if (bad) atomicExch(failed, 1);
+    const int q = warp & 3, row = 32 * q + lane;
+    const uint32_t tb = tmem + (uint32_t(32 * q) << 16);
+#pragma unroll
+    for (int c = 0; c < T; c += 8) {
+      uint32_t a[8], b[8];
+      asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]),
+                     "=r"(a[6]), "=r"(a[7])
+                   : "r"(tb + c));
+      asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                   : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]),
+                     "=r"(b[6]), "=r"(b[7])
+                   : "r"(tb + T + c));
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int t = c + j;
+        const float v = bad ? __uint_as_float(kVNaN)
+                            : __fadd_rn(__uint_as_float(a[j]), __uint_as_float(b[j]));
+        if (split > 1)
+          part[t * kVM + row] = v;
+        else if (t < tokens && n0 + row < n)
+          store_y<BF16>(y, int64_t(t0 + t) * n + n0 + row, v);
+      }
+    }
+    asm volatile("tcgen05.fence::before_thread_sync;");
+  }
+  if (split > 1) {
+    // each rank adds its share of the (token, row) sums over all ranks, in
+    // rank order, and keeps its own sums alive until every rank has read them
+    v_cluster_sync();
+    const uint32_t pa = smem_u32(part);
+    const int items = tokens * kVM;
+    for (int i = rank * kVThreads + tid; i < items; i += split * kVThreads) {
+      float v = v_peer_load(pa + 4 * i, 0);
+      for (int r = 1; r < split; ++r) v = __fadd_rn(v, v_peer_load(pa + 4 * i, uint32_t(r)));
+      const int t = i / kVM, row = i % kVM;
+      if (n0 + row < n) store_y<BF16>(y, int64_t(t0 + t) * n + n0 + row, v);
+    }
+    v_cluster_sync();
+  } else {
+    __syncthreads();
+  }
+  report_failure(status, failed);
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(L::kTmemCols));
+}
+
+// Any k that is a multiple of 32 (the tensor-core kernel takes multiples of
+// 128) and codes that are not 32-byte aligned: a warp takes a weight row, a
+// lane a group of 32 (16 bytes of codes) at a time, for TB tokens.
+template <int TB, bool BF16>
+__global__ void __launch_bounds__(256)
+    k_gemv_simt(const uint8_t* __restrict__ codes, const uint8_t* __restrict__ sf,
+                const uint16_t* __restrict__ x, int64_t ldx, int m, int64_t n, int64_t k,
+                void* __restrict__ y) {
+  const int lane = threadIdx.x & 31;
+  const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  const int t0 = int(blockIdx.y) * TB;
+  if (row >= n) return;
+  const int64_t groups = k / 32, k_tiles = (groups + 3) / 4;
+  const uint8_t* c = codes + row * (k / 2);
+  const uint8_t* f = sf + (row / 128) * k_tiles * 512 + 16 * (row % 32) + 4 * (row % 128 / 32);
+  float acc[TB];
+#pragma unroll
+  for (int t = 0; t < TB; ++t) acc[t] = 0.0f;
+  for (int64_t g = lane; g < groups; g += 32) {
+    const uint4 cw = ld_stream(c + 16 * g);
+    const uint32_t sb = __ldg(f + (g >> 2) * 512 + (g & 3));
+    const float scale = sb == 0xFFu ? __uint_as_float(kVNaN) : scale_value(sb);
+    const uint32_t w[4] = {cw.x, cw.y, cw.z, cw.w};
+    float sum[TB];
+#pragma unroll
+    for (int t = 0; t < TB; ++t) sum[t] = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float wv[8];
+      e2m1x8_decode(w[j], wv);
+#pragma unroll
+      for (int t = 0; t < TB; ++t) {
+        const int tt = min(t0 + t, m - 1);
+        const uint4 xv = ld_l1(x + int64_t(tt) * ldx + g * 32 + 8 * j);
+        const uint32_t xw[4] = {xv.x, xv.y, xv.z, xv.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[t] = __fmaf_rn(wv[2 * i], bf16_lo(xw[i]), sum[t]);
+          sum[t] = __fmaf_rn(wv[2 * i + 1], bf16_hi(xw[i]), sum[t]);
+        }
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < TB; ++t) acc[t] = __fmaf_rn(sum[t], scale, acc[t]);
+  }
+#pragma unroll
+  for (int t = 0; t < TB; ++t) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      acc[t] = __fadd_rn(acc[t], __shfl_xor_sync(0xFFFFFFFFu, acc[t], o));
+    if (lane == t && t0 + t < m) store_y<BF16>(y, int64_t(t0 + t) * n + row, acc[t]);
+  }
+}
+
+// Tensor map of the codes [n][k / 2]: boxes of 128 elements x 128 rows, each
+// 16 codes spread over 16 bytes of shared memory, 128-byte swizzle.
+bool encode_codes(CUtensorMap* map, const void* codes, int64_t n, int64_t k) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {cuuint64_t(k), cuuint64_t(n)};
+  const cuuint64_t strides[1] = {cuuint64_t(k / 2)};
+  const cuuint32_t box[2] = {128, uint32_t(kVM)};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void*>(codes), dims,
+             strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct GemvArgs {
+  const uint16_t* x;
+  int64_t m, n, k, ldx;
+  const uint8_t *codes, *scales;
+  void* y;
+  int* status;
+  cudaStream_t s;
+};
+
+// Slabs of k: enough CTAs to give every SM about two (the loads of two CTAs
+// keep an SM's share of the memory bandwidth busy), at least two k blocks a
+// slab, powers of two up to the portable cluster size.
+int gemv_split(int64_t tiles, int64_t kblocks) {
+  int split = 1;
+  while (split < 8 && tiles * split * 2 <= 296 && kblocks / (split * 2) >= 2) split *= 2;
+  return split;
+}
+
+template <int T, bool BF16>
+cudaError_t gemv_tc(const GemvArgs& a) {
+  using L = VLayout<T>;
+  CUtensorMap tm;
+  if (!encode_codes(&tm, a.codes, a.n, a.k)) return cudaErrorInvalidValue;
+  auto kern = k_gemv<T, BF16>;
+  constexpr size_t smem = L::kBytes + 1024;
+  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (a.n + kVM - 1) / kVM, t_tiles = (a.m + T - 1) / T;
+  const int64_t kblocks = a.k / 128;
+  const int split = gemv_split(tiles * t_tiles, kblocks);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(tiles * split), unsigned(t_tiles));
+  cfg.blockDim = dim3(kVThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = a.s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(split);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, tm, a.scales, a.x, a.ldx, int(a.m), a.n, int(kblocks),
+                            split, a.y, a.status);
+}
+
+template <bool BF16>
+cudaError_t gemv_any(const GemvArgs& a) {
+  if (a.k % 128 == 0 && (reinterpret_cast<uintptr_t>(a.codes) & 31u) == 0) {
+    if (a.m <= 8) return gemv_tc<8, BF16>(a);
+    if (a.m <= 16) return gemv_tc<16, BF16>(a);
+    if (a.m <= 32) return gemv_tc<32, BF16>(a);
+    return gemv_tc<64, BF16>(a);
+  }
+  const dim3 grid(unsigned((a.n + 7) / 8), unsigned(a.m == 1 ? 1 : (a.m + 7) / 8));
+  if (a.m == 1)
+    k_gemv_simt<1, BF16><<<grid, 256, 0, a.s>>>(a.codes, a.scales, a.x, a.ldx, int(a.m), a.n, a.k,
+                                                a.y);
+  else
+    k_gemv_simt<8, BF16><<<grid, 256, 0, a.s>>>(a.codes, a.scales, a.x, a.ldx, int(a.m), a.n, a.k,
+                                                a.y);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_gemv(const void* x, int64_t m, int64_t n, int64_t k, int64_t ldx,
+                        const uint8_t* codes, const uint8_t* scales, void* y, bool bf16_out,
+                        int* status, cudaStream_t s) {
+  const GemvArgs a = {static_cast<const uint16_t*>(x), m, n, k, ldx, codes, scales, y, status, s};
+  return bf16_out ? gemv_any<true>(a) : gemv_any<false>(a);
+}
+
+}  // namespace mxfp4

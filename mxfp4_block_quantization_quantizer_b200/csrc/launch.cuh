@@ -83,6 +83,13 @@ cudaError_t launch_gemm_qa(const void* x, int64_t m, int64_t n, int64_t k, bool 
                            uint8_t* a_codes, uint8_t* a_scales, int* status,
                            cudaStream_t s);
 
+// Y[m][n] = X W^T with bf16 X (row stride ldx) left unquantized and W as MXFP4
+// codes and blocked scales; bf16_out: Y bf16, else fp32; status as for
+// launch_rht_quant.
+cudaError_t launch_gemv(const void* x, int64_t m, int64_t n, int64_t k, int64_t ldx,
+                        const uint8_t* codes, const uint8_t* scales, void* y, bool bf16_out,
+                        int* status, cudaStream_t s);
+
 // Layer norm of the rows of x (row stride ldx elements); weight, bias, y,
 // mean, rstd, codes/scales may be null (see mxfp4_layernorm_quantize).
 cudaError_t launch_layernorm(const void* x, bool bf16, int64_t rows, int64_t cols, int64_t ldx,
