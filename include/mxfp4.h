@@ -424,6 +424,46 @@ mxfp4_status mxfp4_gemv(const void* x, int64_t m, int64_t n, int64_t k, int64_t 
                         const uint8_t* b_codes, const uint8_t* b_scales, void* y, int y_dtype,
                         int* status, void* stream);
 
+/* Largest rows and cols of mxfp4_newton_schulz. */
+#define MXFP4_NS_MAX_DIM ((int64_t)1 << 20)
+
+/* Bytes of workspace mxfp4_newton_schulz needs (about 6 bytes per element and
+ * 4 per element of the smaller square); -1 for a shape it refuses. */
+int64_t mxfp4_newton_schulz_workspace(int64_t rows, int64_t cols);
+
+/*
+ * A weight's update made nearly orthogonal by Newton-Schulz products (the
+ * optimizer step whose result mxfp4_osc_step and mxfp4_qramp_step follow;
+ * with scale = minus the step size, OUT in fp32 is mxfp4_qramp_step's delta):
+ *   X = G / (|G|_F + eps)
+ *   `steps` times:  A = X X^T,  B = b A + c A A,  X = a X + B X
+ *   OUT = scale * X
+ * (for rows > cols the same with X^T). Each step moves every singular value s
+ * of X to a s + b s^3 + c s^5. The products take fp16 operands with fp32
+ * sums, X is carried with about 22 bits between steps, the norm is summed in
+ * fp64: OUT is within about 2e-3 of the exact result relative to its norm
+ * (before the rounding to out_dtype; measured for five steps of 3.4445,
+ * -4.775, 2.0315 on normal and on nearly low-rank matrices). The
+ * same inputs give the same bits. Values are held times 2^12 in fp16, so the
+ * entries of X, A and B must stay below 15.9 in magnitude; coefficients that
+ * keep the singular values of X below 2 do.
+ *   g        device, [rows][cols] of dtype, 16-byte aligned, read only
+ *   steps    1 to 1000; a, b, c within 1e4 in magnitude; eps >= 0
+ *   out      device, [rows][cols] of out_dtype, 16-byte aligned, written; it
+ *            may be g itself where the two types are the same
+ *   workspace  device, 256-byte aligned, workspace_bytes of scratch (at
+ *            least mxfp4_newton_schulz_workspace); calls that run at the same
+ *            time need workspaces of their own
+ *   status   device int or NULL (MXFP4_STATUS_WAIT_TIMEOUT above); OUT holds
+ *            NaN when it is set
+ * Any rows, cols up to MXFP4_NS_MAX_DIM. G of zeros gives zeros (eps > 0);
+ * Inf or NaN in G gives NaN.
+ */
+mxfp4_status mxfp4_newton_schulz(const void* g, int dtype, int64_t rows, int64_t cols, int steps,
+                                 float a, float b, float c, float eps, float scale, void* out,
+                                 int out_dtype, void* workspace, int64_t workspace_bytes,
+                                 int* status, void* stream);
+
 /*
  * Layer norm of every row of X, the transform in front of a quantized linear
  * layer (pre-norm blocks of the pages' vision transformers and LLMs):

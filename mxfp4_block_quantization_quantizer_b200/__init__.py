@@ -8,8 +8,8 @@ from ._binding import (  # noqa: F401
     double_quantize, gemm, gemm_quantize_a, gemv, layernorm, layernorm_backward, layernorm_quantize,
     lib, mxfp4_dequantize, mxfp4_double_quantize,
     mxfp4_gemm, mxfp4_gemm_quantize_a, mxfp4_gemv, mxfp4_layernorm, mxfp4_layernorm_backward,
-    mxfp4_layernorm_quantize,
+    mxfp4_layernorm_quantize, mxfp4_newton_schulz,
     mxfp4_osc_step, mxfp4_osc_synthetic_update, mxfp4_qema_quantize, mxfp4_qramp_step,
     mxfp4_quantize, mxfp4_quantize_oas, mxfp4_rht_quantize, mxfp4_scales_to_blocked,
-    mxfp4_status_string, osc_step, osc_synthetic_update, qema_quantize,
+    mxfp4_status_string, newton_schulz, osc_step, osc_synthetic_update, qema_quantize,
     qramp_step, quantize, rht_quantize, scales_to_blocked, status_string)

@@ -27,7 +27,8 @@ SYMBOLS = ("mxfp4_quantize", "mxfp4_quantize_oas", "mxfp4_dequantize",
            "mxfp4_rht_quantize", "mxfp4_rht_quantize_oas", "mxfp4_osc_step",
            "mxfp4_osc_synthetic_update", "mxfp4_qramp_step", "mxfp4_qema_quantize",
            "mxfp4_scales_to_blocked", "mxfp4_gemm", "mxfp4_gemm_quantize_a",
-           "mxfp4_gemv", "mxfp4_layernorm", "mxfp4_layernorm_quantize", "mxfp4_layernorm_backward",
+           "mxfp4_gemv", "mxfp4_newton_schulz", "mxfp4_newton_schulz_workspace",
+           "mxfp4_layernorm", "mxfp4_layernorm_quantize", "mxfp4_layernorm_backward",
            "mxfp4_layernorm_backward_workspace", "mxfp4_status_string")
 
 
@@ -81,6 +82,8 @@ def lib():
         f32 = ctypes.c_float
         sig.update({
             "mxfp4_gemv": [vp, i64, i64, i64, i64, vp, vp, vp, i32, vp, vp],
+            "mxfp4_newton_schulz": [vp, i32, i64, i64, i32, f32, f32, f32, f32, f32, vp, i32, vp,
+                                    i64, vp, vp],
             "mxfp4_layernorm": [vp, i32, i64, i64, i64, vp, vp, f32, vp, vp, vp, vp],
             "mxfp4_layernorm_quantize": [vp, i32, i64, i64, i64, vp, vp, f32, vp, vp, vp, vp,
                                          vp, vp],
@@ -90,8 +93,8 @@ def lib():
         for name, args in sig.items():
             f = getattr(L, name)
             f.argtypes, f.restype = args, i32
-        L.mxfp4_layernorm_backward_workspace.argtypes = [i64, i64]
-        L.mxfp4_layernorm_backward_workspace.restype = i64
+        for f in (L.mxfp4_layernorm_backward_workspace, L.mxfp4_newton_schulz_workspace):
+            f.argtypes, f.restype = [i64, i64], i64
         L.mxfp4_status_string.argtypes = [i32]
         L.mxfp4_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -598,8 +601,38 @@ def layernorm_backward(dy, x, mean, rstd, weight=None, want_params=True, out=Non
     return out
 
 
+def newton_schulz(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=1.0,
+                  out_dtype=None, out=None, workspace=None, stream=None, status=None):
+    """mxfp4_newton_schulz: scale times the nearly orthogonal matrix that
+    `steps` Newton-Schulz steps with coefficients (a, b, c) make of g (bf16
+    or fp32, any sides), in out_dtype (g's by default). workspace: optional
+    uint8 CUDA tensor of mxfp4_newton_schulz_workspace(rows, cols) bytes;
+    status: optional int32 CUDA tensor of one element."""
+    _cuda2d(g, "g")
+    dt = _dtype_code(g)
+    R, C = g.shape
+    d = g.device
+    if out is None:
+        out = torch.empty((R, C), dtype=out_dtype or g.dtype, device=d)
+    else:
+        _buffer(out, "out", out.dtype, R * C, d)
+        if out.data_ptr() != g.data_ptr() or out.dtype != g.dtype:
+            _apart(out, "out", g)
+    odt = _dtype_code(out)
+    need = lib().mxfp4_newton_schulz_workspace(R, C)
+    workspace = _workspace(workspace, need, d)
+    st = _status_word(status, d)
+    a, b, c = coeffs
+    with _device_of(g):
+        _check(lib().mxfp4_newton_schulz(_ptr(g), dt, R, C, steps, a, b, c, eps, scale, _ptr(out),
+                                         odt, _ptr(workspace), workspace.numel(), st,
+                                         _stream(d, stream)), "mxfp4_newton_schulz")
+    return out
+
+
 # The C names, for callers that prefer them.
 mxfp4_gemv = gemv
+mxfp4_newton_schulz = newton_schulz
 mxfp4_layernorm = layernorm
 mxfp4_layernorm_quantize = layernorm_quantize
 mxfp4_layernorm_backward = layernorm_backward

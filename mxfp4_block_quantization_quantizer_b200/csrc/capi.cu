@@ -301,6 +301,33 @@ mxfp4_status mxfp4_gemv(const void* x, int64_t m, int64_t n, int64_t k, int64_t 
                                       y_dtype == MXFP4_BF16, status, as_stream(stream)));
 }
 
+int64_t mxfp4_newton_schulz_workspace(int64_t rows, int64_t cols) {
+  if (!dims_ok(rows, cols) || rows > MXFP4_NS_MAX_DIM || cols > MXFP4_NS_MAX_DIM) return -1;
+  return mxfp4::newton_schulz_workspace(rows, cols);
+}
+
+mxfp4_status mxfp4_newton_schulz(const void* g, int dtype, int64_t rows, int64_t cols, int steps,
+                                 float a, float b, float c, float eps, float scale, void* out,
+                                 int out_dtype, void* workspace, int64_t workspace_bytes,
+                                 int* status, void* stream) {
+  if (!dtype_ok(dtype) || !dtype_ok(out_dtype)) return MXFP4_ERR_ENUM;
+  if (!g || !out || !workspace) return MXFP4_ERR_NULL;
+  const int64_t need = mxfp4_newton_schulz_workspace(rows, cols);
+  if (need < 0) return MXFP4_ERR_SHAPE;
+  const float lim = 1e4f;
+  if (steps < 1 || steps > 1000 || !eps_ok(eps) || !(a >= -lim && a <= lim) ||
+      !(b >= -lim && b <= lim) || !(c >= -lim && c <= lim) ||
+      !(scale >= -3.4e38f && scale <= 3.4e38f))
+    return MXFP4_ERR_VALUE;
+  if (!aligned16(g) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || !aligned4(status))
+    return MXFP4_ERR_ALIGN;
+  if (workspace_bytes < need) return MXFP4_ERR_WORKSPACE;
+  return from_cuda(mxfp4::launch_newton_schulz(g, dtype == MXFP4_BF16, rows, cols, steps, a, b,
+                                               c, eps, scale, out, out_dtype == MXFP4_BF16,
+                                               workspace, status, as_stream(stream)));
+}
+
 mxfp4_status mxfp4_layernorm(const void* x, int dtype, int64_t rows, int64_t cols,
                              int64_t ldx, const float* weight, const float* bias, float eps,
                              void* y, float* mean, float* rstd, void* stream) {

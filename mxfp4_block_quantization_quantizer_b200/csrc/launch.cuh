@@ -90,6 +90,13 @@ cudaError_t launch_gemv(const void* x, int64_t m, int64_t n, int64_t k, int64_t 
                         const uint8_t* codes, const uint8_t* scales, void* y, bool bf16_out,
                         int* status, cudaStream_t s);
 
+// Newton-Schulz orthogonalization of g [rows][cols] into out (see
+// mxfp4_newton_schulz), and the bytes of workspace it takes.
+int64_t newton_schulz_workspace(int64_t rows, int64_t cols);
+cudaError_t launch_newton_schulz(const void* g, bool bf16, int64_t rows, int64_t cols, int steps,
+                                 float a, float b, float c, float eps, float scale, void* out,
+                                 bool out_bf16, void* workspace, int* status, cudaStream_t st);
+
 // Layer norm of the rows of x (row stride ldx elements); weight, bias, y,
 // mean, rstd, codes/scales may be null (see mxfp4_layernorm_quantize).
 cudaError_t launch_layernorm(const void* x, bool bf16, int64_t rows, int64_t cols, int64_t ldx,

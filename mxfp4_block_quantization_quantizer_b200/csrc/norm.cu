@@ -42,14 +42,10 @@ __device__ __forceinline__ F2 f2(float lo, float hi) {
   return r;
 }
 __device__ __forceinline__ float f2_lo(F2 a) {
-  float lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
-  return lo;
+  return __uint_as_float(static_cast<uint32_t>(a.v));
 }
 __device__ __forceinline__ float f2_hi(F2 a) {
-  float lo, hi;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(a.v));
-  return hi;
+  return __uint_as_float(static_cast<uint32_t>(a.v >> 32));
 }
 __device__ __forceinline__ F2 add2(F2 a, F2 b) {
   F2 r;

@@ -1,0 +1,645 @@
+// Newton-Schulz orthogonalization of a weight's update (sm_100a).
+//
+//   X = G / (|G|_F + eps);  repeat: A = X X^T, B = b A + c A A, X = a X + B X
+// (for more rows than columns A = X^T X and X = a X + X B, the same numbers).
+// Every singular value s of X moves to a s + b s^3 + c s^5, towards 1, while
+// the singular vectors stay.
+//
+// Bound by the tensor cores: with s <= l the sides, a step costs s s l flops
+// for A (half of a symmetric product), s^3 for A A (half) and 2 s s l for
+// B X. Three launches a step, each a persistent tcgen05 GEMM with a fused
+// epilogue; only the tiles on and above the diagonal of A and B are computed
+// and written to both sides.
+//
+// Numbers: operands are fp16, not bf16, at the same tensor rate and with
+// three more significant bits. Their range suffices because everything here
+// is bounded (singular values of X below about 1.2): X, A and B are stored
+// times 2^12, where entries up to 15.9 fit and entries from 2^-26 up keep
+// all their bits. X itself is carried as two fp16 values (hi + lo, about 22
+// bits): a X in the epilogue uses both, the products use hi. With the carry
+// rounded to fp16 the error of five steps on a matrix with strong and weak
+// directions (rank 64 plus noise 20 times smaller, 512 x 512) is 4.8e-3 of
+// the result, with both halves 3.9e-4; with bf16 operands and carry 5.9e-2.
+// Sums are fp32 in tensor memory, the norm's in fp64.
+#include <cuda.h>
+#include <cudaTypedefs.h>
+#include <cuda_fp16.h>
+
+#include "launch.cuh"
+#include "mxfp4_device.cuh"
+#include "tc_common.cuh"
+
+namespace mxfp4 {
+
+namespace {
+
+constexpr float kNsScale = 4096.0f, kNsInv = 1.0f / 4096.0f;
+constexpr int kSM = 128;            // tile rows
+constexpr int kSK = 64;             // K elements of a stage: one swizzle row
+constexpr int kSEpiWarps = 8;
+constexpr int kSThreads = 32 * (2 + kSEpiWarps);
+constexpr int kNsPartials = 592;    // partial sums of the norm
+
+// What a product's epilogue does.
+enum NsMode { kGram = 0, kSquare = 1, kStep = 2, kLast = 3 };
+
+struct NsArgs {
+  int64_t m, n, k;      // product: [m][k] x [n][k]
+  int64_t ldd;          // pitch of c_hi, c_lo, d_hi, d_lo (elements)
+  float alpha, beta;    // D = alpha acc + beta C, all times 2^12
+  const __half *c_hi, *c_lo;
+  __half *d_hi, *d_lo;
+  void* out;            // kLast: [m][n] of the caller's type
+  int out_bf16;
+  float out_scale;
+  int* status;
+};
+
+template <int BN>
+struct NsLayout {
+  static constexpr int kStages = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
+  static constexpr uint32_t kA = kSM * 128, kB = BN * 128;
+  static constexpr uint32_t kBOff = kStages * kA;
+  static constexpr uint32_t kBarOff = kBOff + kStages * kB;
+  static constexpr uint32_t kBytes = kBarOff + 256;
+  static constexpr uint32_t kTmemCols = 2 * BN;
+  // kind::f16: fp32 accumulator, fp16 operands (0), majorness bits 15, 16
+  __host__ __device__ static constexpr uint32_t idesc(bool a_mn, bool b_mn) {
+    return (1u << 4) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
+           (uint32_t(BN >> 3) << 17) | (uint32_t(kSM >> 4) << 24);
+  }
+};
+
+__device__ __forceinline__ void mma_f16(uint32_t tmem_c, uint64_t adesc, uint64_t bdesc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem_c),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+
+// Descriptor of an operand stored with K along the rows of shared memory
+// (MN-major): boxes of 64 MN elements (128 bytes, 128-byte swizzle) x 64 K
+// rows; 8-row groups 1024 bytes apart, boxes 8192 bytes apart. A K step of
+// 16 moves the start by 2048 bytes.
+__device__ __forceinline__ uint64_t smem_desc_mn(const void* p) {
+  uint64_t d = (smem_u32(p) >> 4) & 0x3FFFu;
+  d |= uint64_t(8192 >> 4) << 16;
+  d |= uint64_t(1024 >> 4) << 32;
+  d |= uint64_t(1) << 46;
+  d |= uint64_t(2) << 61;
+  return d;
+}
+
+// Tile `t` of the order that all roles walk. Full products: groups of 16 row
+// tiles swept across all column tiles (their panels stay in L2). Symmetric
+// products: the tiles that reach the diagonal or above, 256 (or BN) columns'
+// worth of rows at a time.
+template <int BN, bool SYM>
+__device__ __forceinline__ void ns_tile(int64_t t, int64_t mt, int64_t nt, int64_t& m0,
+                                        int64_t& n0) {
+  if constexpr (SYM) {
+    // row tile i starts at column tile i * 128 / BN
+    if constexpr (BN >= kSM) {
+      constexpr int R = BN / kSM;  // row tiles per column tile
+      int64_t j = nt - 1;
+      for (; j > 0; --j) {
+        const int64_t rows = (j + 1) * R < mt ? (j + 1) * R : mt;
+        if (t < rows) break;
+        t -= rows;
+      }
+      n0 = j * BN, m0 = t * kSM;
+    } else {
+      constexpr int R = kSM / BN;  // column tiles per row tile
+      int64_t i = 0;
+      for (; i < mt - 1; ++i) {
+        const int64_t cols = nt - i * R;
+        if (t < cols) break;
+        t -= cols;
+      }
+      m0 = i * kSM, n0 = (i * R + t) * BN;
+    }
+  } else {
+    constexpr int64_t G = 16;
+    const int64_t per = G * nt, g = t / per, r = t % per;
+    const int64_t gm = mt - g * G < G ? mt - g * G : G;
+    m0 = (g * G + r % gm) * kSM;
+    n0 = (r / gm) * BN;
+  }
+}
+template <int BN>
+__host__ __device__ inline int64_t ns_tiles(bool sym, int64_t mt, int64_t nt) {
+  if (!sym) return mt * nt;
+  int64_t n = 0;
+  if (BN >= kSM) {
+    for (int64_t j = 0; j < nt; ++j) {
+      const int64_t rows = (j + 1) * (BN / kSM);
+      n += rows < mt ? rows : mt;
+    }
+  } else {
+    for (int64_t i = 0; i < mt; ++i) n += nt - i * (kSM / BN);
+  }
+  return n;
+}
+
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float2 unpack_h2(uint32_t w) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&w));
+}
+
+#define MXFP4_TMEM_LD32(d, addr)                                                               \
+  asm volatile(                                                                                \
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, "                   \
+      "%7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, "                    \
+      "%21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"                         \
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3]), "=r"(d[4]), "=r"(d[5]), "=r"(d[6]),    \
+        "=r"(d[7]), "=r"(d[8]), "=r"(d[9]), "=r"(d[10]), "=r"(d[11]), "=r"(d[12]),             \
+        "=r"(d[13]), "=r"(d[14]), "=r"(d[15]), "=r"(d[16]), "=r"(d[17]), "=r"(d[18]),          \
+        "=r"(d[19]), "=r"(d[20]), "=r"(d[21]), "=r"(d[22]), "=r"(d[23]), "=r"(d[24]),          \
+        "=r"(d[25]), "=r"(d[26]), "=r"(d[27]), "=r"(d[28]), "=r"(d[29]), "=r"(d[30]),          \
+        "=r"(d[31])                                                                            \
+      : "r"(addr))
+
+template <int BN, bool A_MN, bool B_MN, int MODE>
+__global__ void __launch_bounds__(kSThreads, 1)
+    k_ns_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+              const NsArgs p) {
+  using L = NsLayout<BN>;
+  constexpr bool kSym = MODE == kGram || MODE == kSquare;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned long long* full = reinterpret_cast<unsigned long long*>(sm + L::kBarOff);
+  unsigned long long* empty = full + L::kStages;
+  unsigned long long* acc_full = empty + L::kStages;  // two accumulators
+  unsigned long long* acc_empty = acc_full + 2;
+  unsigned long long* drain = acc_empty + 2;
+  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drain + 1);
+  int* failed = reinterpret_cast<int*>(tmem_base + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int64_t mt = (p.m + kSM - 1) / kSM, nt = (p.n + BN - 1) / BN;
+  const int64_t n_tiles = ns_tiles<BN>(kSym, mt, nt);
+  const int64_t n_kb = (p.k + kSK - 1) / kSK;
+
+  if (tid == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&full[s])));
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&empty[s])));
+    }
+    for (int s = 0; s < 2; ++s) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&acc_full[s])));
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&acc_empty[s])),
+                   "r"(kSEpiWarps));
+    }
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(drain)));
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    *failed = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_base)),
+                 "r"(L::kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;");
+  const uint32_t tmem = *tmem_base;
+  // the next launch may set itself up now; this one reads what the launch
+  // before it wrote, so every thread waits for that to have finished
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  if (warp == 0) {
+    if (lane == 0) {
+      uint32_t s = 0, ph = 0, issued = 0, last_ph = 0;
+      for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x) {
+        int64_t m0, n0;
+        ns_tile<BN, kSym>(t, mt, nt, m0, n0);
+        bool stop = false;
+        for (int64_t kb = 0; kb < n_kb; ++kb) {
+          if (!wait_parity_or_failed<false>(&empty[s], ph ^ 1u, failed)) {
+            atomicExch(failed, 1);
+            stop = true;
+            break;
+          }
+          issued |= 1u << s;
+          last_ph = (last_ph & ~(1u << s)) | (ph << s);
+          uint8_t* a = sm + s * L::kA;
+          uint8_t* b = sm + L::kBOff + s * L::kB;
+          const int k0 = int(kb) * kSK;
+          expect_tx(&full[s], L::kA + L::kB);
+          if constexpr (A_MN) {
+#pragma unroll
+            for (int j = 0; j < kSM / 64; ++j)
+              tma_load_2d(a + j * 8192, &tm_a, int(m0) + 64 * j, k0, &full[s]);
+          } else {
+            tma_load_2d(a, &tm_a, k0, int(m0), &full[s]);
+          }
+          if constexpr (B_MN) {
+#pragma unroll
+            for (int j = 0; j < BN / 64; ++j)
+              tma_load_2d(b + j * 8192, &tm_b, int(n0) + 64 * j, k0, &full[s]);
+          } else {
+            tma_load_2d(b, &tm_b, k0, int(n0), &full[s]);
+          }
+          if (++s == L::kStages) s = 0, ph ^= 1u;
+        }
+        if (stop || failed_flag(failed)) break;
+      }
+      for (uint32_t st = 0; st < L::kStages; ++st)
+        if ((issued >> st) & 1u) wait_parity(&full[st], (last_ph >> st) & 1u);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      uint32_t s = 0, ph = 0;
+      int64_t ti = 0;
+      for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x, ++ti) {
+        const uint32_t buf = uint32_t(ti & 1), bph = uint32_t(ti >> 1) & 1u;
+        if (!wait_parity_or_failed<false>(&acc_empty[buf], bph ^ 1u, failed) ||
+            failed_flag(failed)) {
+          atomicExch(failed, 1);
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;");
+        const uint32_t acc = tmem + buf * BN;
+        bool ok = true;
+        for (int64_t kb = 0; kb < n_kb; ++kb) {
+          if (!wait_parity_or_failed<false>(&full[s], ph, failed)) {
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;");
+          const uint8_t* a = sm + s * L::kA;
+          const uint8_t* b = sm + L::kBOff + s * L::kB;
+          const uint64_t ad = A_MN ? smem_desc_mn(a) : smem_desc_sw128(a);
+          const uint64_t bd = B_MN ? smem_desc_mn(b) : smem_desc_sw128(b);
+#pragma unroll
+          for (uint32_t j = 0; j < kSK / 16; ++j)
+            mma_f16(acc, ad + j * (A_MN ? 128u : 2u), bd + j * (B_MN ? 128u : 2u),
+                    L::idesc(A_MN, B_MN), (kb > 0 || j > 0) ? 1u : 0u);
+          commit_to(&empty[s]);
+          if (++s == L::kStages) s = 0, ph ^= 1u;
+        }
+        if (!ok) atomicExch(failed, 1);
+        commit_to(&acc_full[buf]);
+        if (!ok) break;
+      }
+      commit_to(drain);
+      if (!wait_parity(drain, 0)) atomicExch(failed, 1);
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    constexpr int kCols = BN / 2;  // columns of a warp
+    int64_t ti = 0;
+    for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x, ++ti) {
+      int64_t m0, n0;
+      ns_tile<BN, kSym>(t, mt, nt, m0, n0);
+      const uint32_t buf = uint32_t(ti & 1), bph = uint32_t(ti >> 1) & 1u;
+      const bool ok = __all_sync(0xFFFFFFFFu, !failed_flag(failed) &&
+                                                  wait_parity(&acc_full[buf], bph, kAccWaitLimit));
+      if (!ok) atomicExch(failed, 1);
+      asm volatile("tcgen05.fence::after_thread_sync;");
+      const int64_t row = m0 + 32 * q + lane;
+      const uint32_t tb = tmem + buf * BN + (uint32_t(32 * q) << 16) + uint32_t(kCols * half);
+#pragma unroll 1
+      for (int cb = 0; cb < kCols; cb += 32) {
+        uint32_t v[32];
+        MXFP4_TMEM_LD32(v, tb + cb);
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+        if (!ok || failed_flag(failed)) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = 0x7FC00000u;
+        }
+        const int64_t c0 = n0 + kCols * half + cb;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int64_t c = c0 + 8 * g;
+          if (row >= p.m || c >= p.n) break;
+          float o[8];
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[j] = __fmul_rn(p.alpha, __uint_as_float(v[8 * g + j]));
+          if constexpr (MODE != kGram) {
+            // rows are padded to whole 16-byte chunks
+            const uint4 h = *reinterpret_cast<const uint4*>(p.c_hi + row * p.ldd + c);
+            const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
+            float cv[8];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = unpack_h2(hw[j]);
+              cv[2 * j] = f.x, cv[2 * j + 1] = f.y;
+            }
+            if constexpr (MODE == kStep || MODE == kLast) {
+              const uint4 l = *reinterpret_cast<const uint4*>(p.c_lo + row * p.ldd + c);
+              const uint32_t lw[4] = {l.x, l.y, l.z, l.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 f = unpack_h2(lw[j]);
+                cv[2 * j] = __fadd_rn(cv[2 * j], f.x);
+                cv[2 * j + 1] = __fadd_rn(cv[2 * j + 1], f.y);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) o[j] = __fmaf_rn(p.beta, cv[j], o[j]);
+          }
+          if constexpr (MODE == kLast) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if (c + j >= p.n) break;
+              const float y = __fmul_rn(o[j], p.out_scale);
+              if (p.out_bf16)
+                static_cast<uint16_t*>(p.out)[row * p.n + c + j] = uint16_t(pack_bf16x2(y, 0.0f));
+              else
+                static_cast<float*>(p.out)[row * p.n + c + j] = y;
+            }
+          } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) w[j] = pack_h2(o[2 * j], o[2 * j + 1]);
+            if constexpr (kSym) {
+              // each entry of the symmetric result has one writer: the
+              // element on or above the diagonal, for both sides
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const __half hv = __ushort_as_half(uint16_t(w[j / 2] >> (16 * (j & 1))));
+                if (c + j >= row && c + j < p.n) {
+                  p.d_hi[(c + j) * p.ldd + row] = hv;
+                  if (c < row) p.d_hi[row * p.ldd + c + j] = hv;
+                }
+              }
+              if (c >= row)
+                *reinterpret_cast<uint4*>(p.d_hi + row * p.ldd + c) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+              *reinterpret_cast<uint4*>(p.d_hi + row * p.ldd + c) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+              uint32_t lw[4];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float2 f = unpack_h2(w[j]);
+                lw[j] = pack_h2(__fsub_rn(o[2 * j], f.x), __fsub_rn(o[2 * j + 1], f.y));
+              }
+              *reinterpret_cast<uint4*>(p.d_lo + row * p.ldd + c) =
+                  make_uint4(lw[0], lw[1], lw[2], lw[3]);
+            }
+          }
+        }
+        __syncwarp();
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;");
+      __syncwarp();
+      if (ok && lane == 0)
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&acc_empty[buf]))
+                     : "memory");
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;");
+  __syncthreads();
+  report_failure(p.status, failed);
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(L::kTmemCols));
+}
+
+// Sum of the squares of G in fp64: partial[b] over this CTA's elements.
+template <bool BF16>
+__device__ __forceinline__ float ns_load(const void* g, int64_t i) {
+  return BF16 ? __uint_as_float(uint32_t(__ldg(static_cast<const uint16_t*>(g) + i)) << 16)
+              : __ldg(static_cast<const float*>(g) + i);
+}
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+    k_ns_norm(const void* __restrict__ g, int64_t n, double* __restrict__ partial) {
+  constexpr int VEC = BF16 ? 8 : 4;
+  __shared__ double sh[8];
+  double s = 0.0;
+  const int64_t nv = n / VEC, stride = int64_t(gridDim.x) * 256;
+  const int64_t me = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  for (int64_t i = me; i < nv; i += stride) {
+    const uint4 r = ld_stream(static_cast<const uint8_t*>(g) + 16 * i);
+    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if constexpr (BF16) {
+        const double a = bf16_lo(w[j]), b = bf16_hi(w[j]);
+        s += a * a + b * b;
+      } else {
+        const double a = __uint_as_float(w[j]);
+        s += a * a;
+      }
+    }
+  }
+  for (int64_t i = nv * VEC + me; i < n; i += stride) {
+    const double a = ns_load<BF16>(g, i);
+    s += a * a;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+  if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int i = 1; i < 8; ++i) s += sh[i];
+    partial[blockIdx.x] = s;
+  }
+}
+
+// X = 2^12 G / (|G|_F + eps) as hi + lo, pitch ld. Every CTA adds the
+// partial sums itself, in one order.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+    k_ns_start(const void* __restrict__ g, int64_t rows, int64_t cols, int64_t ld, float eps,
+               const double* __restrict__ partial, int n_partial, __half* __restrict__ hi,
+               __half* __restrict__ lo) {
+  __shared__ float f[2];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (threadIdx.x < 32) {
+    double s = 0.0;
+    for (int i = threadIdx.x; i < n_partial; i += 32) s += partial[i];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+    if (threadIdx.x == 0) {
+      // the factor as a power of two and a rest in [1, 2): G may be far from 1
+      const double k = double(kNsScale) / (sqrt(s) + double(eps));
+      int e = 0;
+      if (k > 0.0 && k < 1e300) e = ilogb(k);
+      e = e < -126 ? -126 : (e > 127 ? 127 : e);
+      f[0] = exp2f(float(e));
+      f[1] = float(scalbn(k, -e));
+    }
+  }
+  __syncthreads();
+  const float p = f[0], r = f[1];
+  const int64_t chunks = (cols + 7) / 8;
+  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < rows * chunks;
+       i += int64_t(gridDim.x) * 256) {
+    const int64_t row = i / chunks, c = i % chunks * 8;
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? ns_load<BF16>(g, row * cols + c + j) : 0.0f;
+    uint32_t hw[4], lw[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = __fmul_rn(__fmul_rn(v[2 * j], p), r);
+      const float b = __fmul_rn(__fmul_rn(v[2 * j + 1], p), r);
+      hw[j] = pack_h2(a, b);
+      const float2 h = unpack_h2(hw[j]);
+      lw[j] = pack_h2(__fsub_rn(a, h.x), __fsub_rn(b, h.y));
+    }
+    *reinterpret_cast<uint4*>(hi + row * ld + c) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+    *reinterpret_cast<uint4*>(lo + row * ld + c) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+  }
+}
+
+// Tensor map over fp16 [rows][cols] with pitch ld: boxes of 64 columns (one
+// 128-byte swizzle row) x box_rows.
+bool encode_half(CUtensorMap* map, const __half* base, int64_t rows, int64_t cols, int64_t ld,
+                 uint32_t box_rows) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return false;
+  const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+  const cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
+  const cuuint32_t box[2] = {64, box_rows};
+  const cuuint32_t estr[2] = {1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<__half*>(base), dims, strides,
+             box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int ns_sms() {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess)
+    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms;
+}
+
+template <typename... P, typename... A>
+cudaError_t ns_launch(void (*kern)(P...), int grid, int threads, size_t smem, cudaStream_t s,
+                      A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// An fp16 matrix of the workspace and how a product reads it: K along its
+// columns (K-major) or along its rows (MN-major).
+struct NsOperand {
+  const __half* p;
+  int64_t rows, cols, ld;
+  bool mn;
+};
+
+template <int BN, bool A_MN, bool B_MN, int MODE>
+cudaError_t ns_gemm_bn(const NsOperand& a, const NsOperand& b, const NsArgs& args,
+                       cudaStream_t s) {
+  using L = NsLayout<BN>;
+  CUtensorMap ta, tb;
+  if (!encode_half(&ta, a.p, a.rows, a.cols, a.ld, A_MN ? kSK : kSM) ||
+      !encode_half(&tb, b.p, b.rows, b.cols, b.ld, B_MN ? kSK : BN))
+    return cudaErrorInvalidValue;
+  auto kern = k_ns_gemm<BN, A_MN, B_MN, MODE>;
+  constexpr size_t smem = L::kBytes + 1024;
+  const cudaError_t e =
+      cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                           cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = ns_tiles<BN>(MODE == kGram || MODE == kSquare, (args.m + kSM - 1) / kSM,
+                                     (args.n + BN - 1) / BN);
+  const int sms = ns_sms();
+  return ns_launch(kern, int(tiles < sms ? tiles : sms), kSThreads, smem, s, ta, tb, args);
+}
+
+// Tile width: 256 columns reuse the most; narrower tiles where 256 would
+// leave SMs idle (fewer tiles than SMs).
+template <bool A_MN, bool B_MN, int MODE>
+cudaError_t ns_gemm(const NsOperand& a, const NsOperand& b, const NsArgs& args, cudaStream_t s) {
+  constexpr bool sym = MODE == kGram || MODE == kSquare;
+  const int64_t mt = (args.m + kSM - 1) / kSM;
+  if (ns_tiles<256>(sym, mt, (args.n + 255) / 256) >= 148)
+    return ns_gemm_bn<256, A_MN, B_MN, MODE>(a, b, args, s);
+  if (ns_tiles<128>(sym, mt, (args.n + 127) / 128) >= 148)
+    return ns_gemm_bn<128, A_MN, B_MN, MODE>(a, b, args, s);
+  return ns_gemm_bn<64, A_MN, B_MN, MODE>(a, b, args, s);
+}
+
+int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
+int64_t pad256(int64_t v) { return (v + 255) / 256 * 256; }
+
+}  // namespace
+
+int64_t newton_schulz_workspace(int64_t rows, int64_t cols) {
+  const int64_t s = rows < cols ? rows : cols;
+  return 3 * pad256(rows * pad64(cols) * 2) + 2 * pad256(s * pad64(s) * 2) + kNsPartials * 8;
+}
+
+cudaError_t launch_newton_schulz(const void* g, bool bf16, int64_t rows, int64_t cols, int steps,
+                                 float a, float b, float c, float eps, float scale, void* out,
+                                 bool out_bf16, void* workspace, int* status, cudaStream_t st) {
+  const int64_t ldx = pad64(cols), s = rows < cols ? rows : cols, lds = pad64(s);
+  const bool tall = rows > cols;
+  uint8_t* w = static_cast<uint8_t*>(workspace);
+  const int64_t xb = pad256(rows * ldx * 2), sb = pad256(s * lds * 2);
+  __half* x[2] = {reinterpret_cast<__half*>(w), reinterpret_cast<__half*>(w + xb)};
+  __half* xl = reinterpret_cast<__half*>(w + 2 * xb);
+  __half* ga = reinterpret_cast<__half*>(w + 3 * xb);
+  __half* gb = reinterpret_cast<__half*>(w + 3 * xb + sb);
+  double* partial = reinterpret_cast<double*>(w + 3 * xb + 2 * sb);
+
+  const int64_t n = rows * cols;
+  const int64_t want = (n / 8 + 255) / 256;
+  const int n_partial = int(want < 1 ? 1 : (want < kNsPartials ? want : kNsPartials));
+  if (bf16)
+    k_ns_norm<true><<<n_partial, 256, 0, st>>>(g, n, partial);
+  else
+    k_ns_norm<false><<<n_partial, 256, 0, st>>>(g, n, partial);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int64_t chunk_blocks = (rows * ((cols + 7) / 8) + 255) / 256;
+  const int start_grid = int(chunk_blocks < 148 * 8 ? chunk_blocks : 148 * 8);
+  e = bf16 ? ns_launch(k_ns_start<true>, start_grid, 256, 0, st, g, rows, cols, ldx, eps,
+                       static_cast<const double*>(partial), n_partial, x[0], xl)
+           : ns_launch(k_ns_start<false>, start_grid, 256, 0, st, g, rows, cols, ldx, eps,
+                       static_cast<const double*>(partial), n_partial, x[0], xl);
+  const NsOperand og = {ga, s, s, lds, false}, ob = {gb, s, s, lds, false};
+  for (int i = 0; i < steps && e == cudaSuccess; ++i) {
+    const __half* xi = x[i & 1];
+    NsArgs p = {};
+    p.status = status;
+    // A = X X^T (X^T X): K along the longer side
+    p.m = p.n = s, p.k = tall ? rows : cols;
+    p.ldd = lds, p.alpha = kNsInv, p.d_hi = ga;
+    NsOperand ox = {xi, rows, cols, ldx, tall};
+    e = tall ? ns_gemm<true, true, kGram>(ox, ox, p, st) : ns_gemm<false, false, kGram>(ox, ox, p, st);
+    if (e != cudaSuccess) break;
+    // B = b A + c A A
+    p.k = s, p.alpha = c * kNsInv, p.beta = b, p.c_hi = ga, p.d_hi = gb;
+    e = ns_gemm<false, false, kSquare>(og, og, p, st);
+    if (e != cudaSuccess) break;
+    // X = a X + B X (a X + X B)
+    p.m = rows, p.n = cols, p.k = s, p.ldd = ldx;
+    p.alpha = kNsInv, p.beta = a, p.c_hi = xi, p.c_lo = xl, p.d_hi = x[(i + 1) & 1], p.d_lo = xl;
+    p.out = out, p.out_bf16 = out_bf16, p.out_scale = scale * kNsInv;
+    ox.mn = !tall;
+    if (i + 1 < steps)
+      e = tall ? ns_gemm<false, false, kStep>(ox, ob, p, st) : ns_gemm<false, true, kStep>(ob, ox, p, st);
+    else
+      e = tall ? ns_gemm<false, false, kLast>(ox, ob, p, st) : ns_gemm<false, true, kLast>(ob, ox, p, st);
+  }
+  return e;
+}
+
+}  // namespace mxfp4
