@@ -6,7 +6,6 @@ with torch. Every step of the computation runs in the library's kernels.
 There is no fallback: if the library is missing, or a tensor is not on a CUDA
 device, the call raises.
 """
-import contextlib
 import ctypes
 import os
 
@@ -420,9 +419,23 @@ def gemm_quantize_a(x, b_codes, b_blocked, rounding=RNE, seed=0, out=None, want_
     return out
 
 
-def _device_of(t):
-    """Context in which t's device is the current one, where launches go."""
-    return torch.cuda.device(t.device) if t.is_cuda else contextlib.nullcontext()
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _call(name, device, stream, *args):
+    """Call the entry point `name` on `stream` (by default the current stream
+    of `device`) with `device` as the current one, where its launches go."""
+    i = device.index
+    s = torch._C._cuda_getCurrentRawStream(i) if stream is None else stream.cuda_stream
+    fn = getattr(lib(), name)
+    if torch._C._cuda_getDevice() == i:
+        status = fn(*args, s)
+    else:
+        with torch.cuda.device(i):
+            status = fn(*args, s)
+    if status != 0:
+        raise Mxfp4Error(status, name)
 
 
 def _rows2d(t, name):
@@ -430,14 +443,18 @@ def _rows2d(t, name):
     view of a wider tensor). Returns its row stride in elements."""
     if not isinstance(t, torch.Tensor):
         raise TypeError("%s must be a CUDA tensor" % name)
-    if t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+    if t.dim() != 2:
+        raise ValueError("%s must be a 2-D tensor with contiguous rows" % name)
+    rows, cols = t.shape
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError("%s must be a 2-D tensor with contiguous rows" % name)
     _on_device(t, name)
-    if t.shape[0] <= 1:
-        return max(1, t.shape[1])
-    if t.stride(0) < t.shape[1]:
+    if rows <= 1:
+        return max(1, cols)
+    if ld < cols:
         raise ValueError("the rows of %s overlap" % name)
-    return t.stride(0)
+    return ld
 
 
 def _apart(out, name, *inputs):
@@ -473,11 +490,9 @@ def gemv(x, b_codes, b_blocked, out_dtype=torch.bfloat16, out=None, stream=None,
     else:
         _buffer(out, "out", out.dtype, m * n, d)
         _apart(out, "out", x)
-    dt = _dtype_code(out)
-    st = _status_word(status, d)
-    with _device_of(x):
-        _check(lib().mxfp4_gemv(_ptr(x), m, n, k, ldx, _ptr(b_codes), _ptr(b_blocked), _ptr(out),
-                                dt, st, _stream(d, stream)), "mxfp4_gemv")
+    st = None if status is None else _addr(_buffer(status, "status", torch.int32, 1, d))
+    _call("mxfp4_gemv", d, stream, x.data_ptr(), m, n, k, ldx, b_codes.data_ptr(),
+          b_blocked.data_ptr(), out.data_ptr(), _dtype_code(out), st)
     return out
 
 
@@ -498,21 +513,23 @@ def layernorm(x, weight=None, bias=None, eps=1e-5, want_stats=False, out=None, s
     ldx, dt = _norm_inputs(x, weight, bias)
     R, C = x.shape
     d = x.device
+    mean = rstd = None
     if out is None:
-        out = torch.empty((R, C), dtype=x.dtype, device=d)
+        out = y = torch.empty((R, C), dtype=x.dtype, device=d)
         if want_stats:
-            out = (out, torch.empty(R, dtype=torch.float32, device=d),
-                   torch.empty(R, dtype=torch.float32, device=d))
-    y, mean, rstd = out if want_stats else (out, None, None)
-    _buffer(y, "out", x.dtype, R * C, d)
-    _apart(y, "out", x)
-    if want_stats:
-        _buffer(mean, "mean", torch.float32, R, d)
-        _buffer(rstd, "rstd", torch.float32, R, d)
-    with _device_of(x):
-        _check(lib().mxfp4_layernorm(_ptr(x), dt, R, C, ldx, _ptr(weight), _ptr(bias), eps,
-                                     _ptr(y), _ptr(mean), _ptr(rstd), _stream(d, stream)),
-               "mxfp4_layernorm")
+            mean, rstd = (torch.empty(R, dtype=torch.float32, device=d),
+                          torch.empty(R, dtype=torch.float32, device=d))
+            out = (y, mean, rstd)
+    else:
+        y = out
+        if want_stats:
+            y, mean, rstd = out
+            _buffer(mean, "mean", torch.float32, R, d)
+            _buffer(rstd, "rstd", torch.float32, R, d)
+        _buffer(y, "out", x.dtype, R * C, d)
+        _apart(y, "out", x)
+    _call("mxfp4_layernorm", d, stream, x.data_ptr(), dt, R, C, ldx, _addr(weight), _addr(bias),
+          eps, y.data_ptr(), _addr(mean), _addr(rstd))
     return out
 
 
@@ -544,11 +561,9 @@ def layernorm_quantize(x, weight=None, bias=None, eps=1e-5, want_y=False, want_s
     if want_stats:
         _buffer(mean, "mean", torch.float32, R, d)
         _buffer(rstd, "rstd", torch.float32, R, d)
-    with _device_of(x):
-        _check(lib().mxfp4_layernorm_quantize(_ptr(x), dt, R, C, ldx, _ptr(weight), _ptr(bias),
-                                              eps, _ptr(y), _ptr(mean), _ptr(rstd), _ptr(codes),
-                                              _ptr(scales), _stream(d, stream)),
-               "mxfp4_layernorm_quantize")
+    _call("mxfp4_layernorm_quantize", d, stream, x.data_ptr(), dt, R, C, ldx, _addr(weight),
+          _addr(bias), eps, _addr(y), _addr(mean), _addr(rstd), codes.data_ptr(),
+          scales.data_ptr())
     return out
 
 
@@ -576,28 +591,30 @@ def layernorm_backward(dy, x, mean, rstd, weight=None, want_params=True, out=Non
     d = x.device
     _buffer(mean, "mean", torch.float32, R, d)
     _buffer(rstd, "rstd", torch.float32, R, d)
+    dw = db = None
     if out is None:
-        out = torch.empty((R, C), dtype=x.dtype, device=d)
+        out = dx = torch.empty((R, C), dtype=x.dtype, device=d)
         if want_params:
-            out = (out, torch.empty(C, dtype=torch.float32, device=d),
-                   torch.empty(C, dtype=torch.float32, device=d))
-    dx, dw, db = out if want_params else (out, None, None)
-    _buffer(dx, "out", x.dtype, R * C, d)
-    _apart(dx, "out", x, dy)
-    need = 0
+            dw, db = (torch.empty(C, dtype=torch.float32, device=d),
+                      torch.empty(C, dtype=torch.float32, device=d))
+            out = (dx, dw, db)
+    else:
+        dx = out
+        if want_params:
+            dx, dw, db = out
+            _buffer(dw, "dw", torch.float32, C, d)
+            _buffer(db, "db", torch.float32, C, d)
+        _buffer(dx, "out", x.dtype, R * C, d)
+        _apart(dx, "out", x, dy)
+    size = 0
     if want_params:
-        _buffer(dw, "dw", torch.float32, C, d)
-        _buffer(db, "db", torch.float32, C, d)
-        need = lib().mxfp4_layernorm_backward_workspace(R, C)
-        workspace = _workspace(workspace, need, d)
+        workspace = _workspace(workspace, lib().mxfp4_layernorm_backward_workspace(R, C), d)
+        size = workspace.numel()
     else:
         workspace = None
-    with _device_of(x):
-        _check(lib().mxfp4_layernorm_backward(_ptr(dy), _ptr(x), dt, R, C, lddy, ldx,
-                                              _ptr(weight), _ptr(mean), _ptr(rstd), _ptr(dx),
-                                              _ptr(dw), _ptr(db), _ptr(workspace),
-                                              workspace.numel() if workspace is not None else 0,
-                                              _stream(d, stream)), "mxfp4_layernorm_backward")
+    _call("mxfp4_layernorm_backward", d, stream, dy.data_ptr(), x.data_ptr(), dt, R, C, lddy, ldx,
+          _addr(weight), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), _addr(dw), _addr(db),
+          _addr(workspace), size)
     return out
 
 
@@ -621,12 +638,10 @@ def newton_schulz(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=
     odt = _dtype_code(out)
     need = lib().mxfp4_newton_schulz_workspace(R, C)
     workspace = _workspace(workspace, need, d)
-    st = _status_word(status, d)
+    st = None if status is None else _addr(_buffer(status, "status", torch.int32, 1, d))
     a, b, c = coeffs
-    with _device_of(g):
-        _check(lib().mxfp4_newton_schulz(_ptr(g), dt, R, C, steps, a, b, c, eps, scale, _ptr(out),
-                                         odt, _ptr(workspace), workspace.numel(), st,
-                                         _stream(d, stream)), "mxfp4_newton_schulz")
+    _call("mxfp4_newton_schulz", d, stream, g.data_ptr(), dt, R, C, steps, a, b, c, eps, scale,
+          out.data_ptr(), odt, workspace.data_ptr(), workspace.numel(), st)
     return out
 
 

@@ -522,8 +522,7 @@ cudaError_t gemv_tc(const GemvArgs& a) {
   if (!encode_codes(&tm, a.codes, a.n, a.k)) return cudaErrorInvalidValue;
   auto kern = k_gemv<T, BF16>;
   constexpr size_t smem = L::kBytes + 1024;
-  cudaError_t e = cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = (a.n + kVM - 1) / kVM, t_tiles = (a.m + T - 1) / T;
   const int64_t kblocks = a.k / 128;

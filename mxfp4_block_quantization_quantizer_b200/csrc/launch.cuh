@@ -12,6 +12,10 @@ namespace mxfp4 {
 int persistent_grid(const void* kernel, int threads, size_t smem,
                     int64_t work_blocks);
 
+// Lets `kernel` take `bytes` of dynamic shared memory on the current device
+// (asked of the runtime when the limit has to grow).
+cudaError_t allow_smem(const void* kernel, size_t bytes);
+
 // oas: the overflow-aware scale rule instead of the OCP one.
 cudaError_t launch_quant_rows(const void* x, bool bf16, int64_t rows,
                               int64_t cols, bool sr, uint64_t seed,

@@ -10,17 +10,27 @@
 //   dw = sum_r dy h,  db = sum_r dy.
 //
 // Bound by memory: forward reads x and writes y, backward reads x and dy and
-// writes dx, once each. A row lives in the registers of W warps (E = VEC NV
-// elements a thread); the next row's loads are issued before this row's
-// reductions, so loads stay in flight across them. Every statistic is fp32:
-// each warp takes its own mean first and sums squares around it, and the
-// warps' pairs (sum, squares) are joined with the exact correction
-// n_w (mean_w - mean)^2, so a large common offset costs no precision.
-// Persistent grid: the W warps keep their columns from row to row, so w and b
-// stay in registers, and so do the column sums of the backward pass (for
-// wide rows, in shared memory); each CTA writes one partial row of dw and db
-// and a second small kernel adds those in a fixed order (no atomics: the
-// same inputs give the same bits).
+// writes dx, once each. W warps take whole rows (E = VEC NV elements a thread
+// in registers; rows too wide for one CTA are split over a cluster of two).
+// The loads of the next kLnDepth rows are in flight at any time as 16-byte
+// asynchronous copies into shared memory: each thread copies what it will
+// read itself, so no barrier orders them, and no register holds them. Every
+// statistic is fp32: each warp takes its own mean first and sums squares
+// around it, and the warps' pairs (sum, squares) are joined with the exact
+// correction n_w (mean_w - mean)^2, so a large common offset costs no
+// precision. Persistent grid: the warps keep their columns from row to row,
+// so w and b stay in registers, and so do the column sums of the backward
+// pass; each CTA writes one partial row of dw and db and a second small
+// kernel adds those in a fixed order (no atomics: the same inputs give the
+// same bits).
+//
+// Rows that are no whole number of 16-byte vectors start off a 16-byte
+// boundary, each at its own distance `off`; but rows VEC apart start at the
+// same distance, so with a row stride between a group's rows that is a
+// multiple of VEC a thread still keeps its columns, and everything but the
+// two ends of a row moves as aligned 16-byte vectors (vectors that reach into
+// a neighbouring row are read whole and masked, and stored element by
+// element).
 #include "launch.cuh"
 #include "mxfp4_device.cuh"
 
@@ -28,7 +38,10 @@ namespace mxfp4 {
 
 namespace {
 
-constexpr int kLnMaxWarps = 16;      // warps that share a row
+constexpr int kLnMaxWarps = 16;      // warps of a CTA that share a row
+constexpr int kLnMaxParts = 32;      // ... and of a cluster
+constexpr int kLnDepth = 3;          // rows in flight per group
+constexpr int64_t kLnMaxCols = 1 << 16;  // far above what a cluster holds
 constexpr int kLnGenThreads = 512;   // the kernels for wider rows
 constexpr int kLnRedThreads = 1024;
 
@@ -63,19 +76,12 @@ __device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
   return r;
 }
 
-// A vector of VEC elements as loaded (16 bytes, or one element for rows that
-// are not 16-byte aligned), and its fp32 pairs. A single element fills the
-// low half of one pair; its high half stays zero and is never counted.
+// A vector of VEC elements as loaded (16 bytes), and its fp32 pairs.
 template <bool BF16, int VEC>
 struct Vec;
 template <>
 struct Vec<true, 8> {
-  static constexpr int kPairs = 4;
   uint4 r;
-  __device__ __forceinline__ void load(const void* base, int64_t e) {
-    r = ld_stream(static_cast<const uint16_t*>(base) + e);
-  }
-  __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void unpack(F2* p) const {
     p[0] = f2(bf16_lo(r.x), bf16_hi(r.x)), p[1] = f2(bf16_lo(r.y), bf16_hi(r.y));
     p[2] = f2(bf16_lo(r.z), bf16_hi(r.z)), p[3] = f2(bf16_lo(r.w), bf16_hi(r.w));
@@ -84,18 +90,10 @@ struct Vec<true, 8> {
     r = make_uint4(pack_bf16x2(f2_lo(p[0]), f2_hi(p[0])), pack_bf16x2(f2_lo(p[1]), f2_hi(p[1])),
                    pack_bf16x2(f2_lo(p[2]), f2_hi(p[2])), pack_bf16x2(f2_lo(p[3]), f2_hi(p[3])));
   }
-  __device__ __forceinline__ void store(void* base, int64_t e) const {
-    __stcs(reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + e), r);
-  }
 };
 template <>
 struct Vec<false, 4> {
-  static constexpr int kPairs = 2;
   uint4 r;
-  __device__ __forceinline__ void load(const void* base, int64_t e) {
-    r = ld_stream(static_cast<const float*>(base) + e);
-  }
-  __device__ __forceinline__ void zero() { r = make_uint4(0, 0, 0, 0); }
   __device__ __forceinline__ void unpack(F2* p) const {
     p[0] = f2(__uint_as_float(r.x), __uint_as_float(r.y));
     p[1] = f2(__uint_as_float(r.z), __uint_as_float(r.w));
@@ -104,70 +102,27 @@ struct Vec<false, 4> {
     r = make_uint4(__float_as_uint(f2_lo(p[0])), __float_as_uint(f2_hi(p[0])),
                    __float_as_uint(f2_lo(p[1])), __float_as_uint(f2_hi(p[1])));
   }
-  __device__ __forceinline__ void store(void* base, int64_t e) const {
-    __stcs(reinterpret_cast<uint4*>(static_cast<float*>(base) + e), r);
-  }
 };
-template <bool BF16>
-struct Vec<BF16, 1> {
-  static constexpr int kPairs = 1;
-  uint32_t r;  // fp32 bits
-  __device__ __forceinline__ void load(const void* base, int64_t e) {
-    r = BF16 ? uint32_t(__ldg(static_cast<const uint16_t*>(base) + e)) << 16
-             : __ldg(static_cast<const uint32_t*>(base) + e);
-  }
-  __device__ __forceinline__ void zero() { r = 0; }
-  __device__ __forceinline__ void unpack(F2* p) const { p[0] = f2(__uint_as_float(r), 0.0f); }
-  __device__ __forceinline__ void pack(const F2* p) {
-    r = BF16 ? pack_bf16x2(f2_lo(p[0]), 0.0f) : __float_as_uint(f2_lo(p[0]));
-  }
-  __device__ __forceinline__ void store(void* base, int64_t e) const {
-    if (BF16)
-      static_cast<uint16_t*>(base)[e] = uint16_t(r);
-    else
-      static_cast<uint32_t*>(base)[e] = r;
-  }
-};
-
-// VEC fp32 parameters of columns e .. e + VEC - 1 (16-byte aligned where
-// VEC > 1) as pairs; `fill` where there is no parameter tensor.
+// VEC fp32 parameters of columns e .. e + VEC - 1 as pairs (columns outside
+// the row: zero); `fill` where there is no parameter tensor.
 template <int VEC>
-__device__ __forceinline__ void load_param(const float* p, int64_t e, float fill, F2* out) {
-  if constexpr (VEC == 1) {
-    out[0] = f2(p != nullptr ? __ldg(p + e) : fill, 0.0f);
-  } else {
+__device__ __forceinline__ void load_param(const float* p, int e, int cols, bool vec, float fill,
+                                           F2* out) {
+  if (p != nullptr && vec && e >= 0 && e + VEC <= cols) {
 #pragma unroll
     for (int j = 0; j < VEC / 4; ++j) {
-      float4 v = make_float4(fill, fill, fill, fill);
-      if (p != nullptr) v = __ldg(reinterpret_cast<const float4*>(p + e) + j);
+      const float4 v = __ldg(reinterpret_cast<const float4*>(p + e) + j);
       out[2 * j] = f2(v.x, v.y), out[2 * j + 1] = f2(v.z, v.w);
     }
-  }
-}
-
-// The same for VEC fp32 values in shared memory.
-template <int VEC>
-__device__ __forceinline__ void load_shared(const float* p, F2* out) {
-  if constexpr (VEC == 1) {
-    out[0] = f2(*p, 0.0f);
   } else {
+    float v[VEC];
 #pragma unroll
-    for (int j = 0; j < VEC / 4; ++j) {
-      const float4 v = reinterpret_cast<const float4*>(p)[j];
-      out[2 * j] = f2(v.x, v.y), out[2 * j + 1] = f2(v.z, v.w);
+    for (int j = 0; j < VEC; ++j) {
+      const bool in = e + j >= 0 && e + j < cols;
+      v[j] = !in ? 0.0f : (p != nullptr ? __ldg(p + e + j) : fill);
     }
-  }
-}
-template <int VEC>
-__device__ __forceinline__ void store_shared(float* p, const F2* in) {
-  if constexpr (VEC == 1) {
-    *p = f2_lo(in[0]);
-  } else {
 #pragma unroll
-    for (int j = 0; j < VEC / 4; ++j)
-      reinterpret_cast<float4*>(p)[j] =
-          make_float4(f2_lo(in[2 * j]), f2_hi(in[2 * j]), f2_lo(in[2 * j + 1]),
-                      f2_hi(in[2 * j + 1]));
+    for (int j = 0; j < VEC / 2; ++j) out[j] = f2(v[2 * j], v[2 * j + 1]);
   }
 }
 
@@ -198,148 +153,260 @@ __device__ __forceinline__ void group_sync(int g, int W) {
   else
     asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(W * 32) : "memory");
 }
-
-// Where a thread stands: the W warps of group g take whole rows; thread t of
-// them holds vectors t, t + 32 W, ... of the row's nvec.
-struct Place {
-  int W, P, g, G, w, lane, t;
-};
-__device__ __forceinline__ Place place(int W, int P) {
-  Place p;
-  p.W = W, p.P = P;
-  const int warp = threadIdx.x >> 5;
-  p.g = warp / W, p.G = (blockDim.x >> 5) / W;
-  p.w = warp % W, p.lane = threadIdx.x & 31;
-  p.t = p.w * 32 + p.lane;
-  return p;
+// Every thread of both CTAs of a cluster (release, then acquire).
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void store_pair(float2* p, float2 v, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(v.x), "f"(v.y)
+               : "memory");
 }
 
-// Forward. QUANT also (or only) writes the 1x32 codes and scales of the
-// rounded y: a group is 32 / VEC adjacent lanes (rows are 16-byte aligned
-// and cols is a multiple of 32, so a group never splits over warps).
-template <bool BF16, int VEC, int NV, bool QUANT>
-__global__ void __launch_bounds__(512)
-    k_ln_fwd(const void* __restrict__ x, int64_t rows, int cols, int64_t ldx,
-             const float* __restrict__ weight, const float* __restrict__ bias, float eps,
-             void* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out,
-             uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, int W, int P) {
-  using V = Vec<BF16, VEC>;
-  constexpr int NP = V::kPairs;
-  // w and b stay in registers where the row's share leaves room for them
-  constexpr bool kKeep = VEC * NV <= (BF16 ? 24 : 16);
-  __shared__ float2 red[2][kLnMaxWarps];
-  const Place p = place(W, P);
-  const int nvec = cols / VEC, step = 32 * W;
-  const int64_t stride = int64_t(gridDim.x) * p.G;
-  const float inv_n = __fdiv_rn(1.0f, float(cols));
+// How rows are shared out: W warps of a CTA (times CS CTAs of a cluster) take
+// a row, G groups a CTA; P = the power of two from W CS on.
+struct LnSplit {
+  int W, P, CS, G;
+};
 
-  // valid elements of this warp, and of warp `lane` of the group
-  float my_n = 0.0f, lane_n = 0.0f;
+// Where a thread stands: its vectors are v0, v0 + step, ... of the row's
+// nvec, which starts `off` elements after a 16-byte boundary.
+struct Place {
+  int W, CS, P, g, G, w, lane, rank, v0, step, off, nvec, cols;
+  int64_t row0, stride;
+};
+template <int VEC, int NV>
+__device__ __forceinline__ Place place(const LnSplit& s, int cols, int64_t ld, int misaligned) {
+  Place p;
+  p.W = s.W, p.CS = s.CS, p.P = s.P, p.G = s.G, p.cols = cols;
+  const int warp = threadIdx.x >> 5;
+  p.g = warp / s.W, p.w = warp % s.W, p.lane = threadIdx.x & 31;
+  p.rank = s.CS > 1 ? int(blockIdx.x & 1) : 0;
+  p.step = 32 * s.W;
+  p.v0 = p.rank * NV * p.step + p.w * 32 + p.lane;
+  p.row0 = int64_t(blockIdx.x / s.CS) * s.G + p.g;
+  p.stride = int64_t(gridDim.x / s.CS) * s.G;
+  p.off = int((misaligned + p.row0 * ld) & (VEC - 1));
+  p.nvec = (cols + p.off + VEC - 1) / VEC;
+  return p;
+}
+// Elements of the row that warp w of CTA `rank` holds.
+template <int VEC, int NV>
+__device__ __forceinline__ float warp_count(const Place& p, int rank, int w) {
+  int n = 0;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    my_n += float(min(max(nvec - i * step - p.w * 32, 0), 32) * VEC);
-    lane_n += float(min(max(nvec - i * step - p.lane * 32, 0), 32) * VEC);
+    const int e = (rank * NV * p.step + i * p.step + w * 32) * VEC - p.off;
+    n += min(max(e + 32 * VEC, 0), p.cols) - min(max(e, 0), p.cols);
   }
-  const float my_inv = my_n > 0.0f ? __fdiv_rn(1.0f, my_n) : 0.0f;
-  const float lane_inv = lane_n > 0.0f && p.lane < W ? __fdiv_rn(1.0f, lane_n) : 0.0f;
+  return float(n);
+}
 
-  F2 wk[kKeep ? NV * NP : 1], bk[kKeep ? NV * NP : 1];
-  if constexpr (kKeep) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = p.t + i * step;
-      if (v < nvec) {
-        load_param<VEC>(weight, int64_t(v) * VEC, 1.0f, wk + i * NP);
-        load_param<VEC>(bias, int64_t(v) * VEC, 0.0f, bk + i * NP);
-      } else {
-#pragma unroll
-        for (int j = 0; j < NP; ++j) wk[i * NP + j] = bk[i * NP + j] = f2(0.0f, 0.0f);
+// A thread's way down the rows of one tensor: `at` is its first vector in the
+// next row to load (or store).
+struct Walk {
+  const uint8_t* at;
+  int64_t step;  // bytes from a row of the group to its next
+};
+template <bool BF16>
+__device__ __forceinline__ Walk walk(const void* base, int64_t ld, const Place& p) {
+  constexpr int kSize = BF16 ? 2 : 4, VEC = 16 / kSize;
+  Walk w;
+  w.at = static_cast<const uint8_t*>(base) + (p.row0 * ld + p.v0 * VEC - p.off) * kSize;
+  w.step = p.stride * ld * kSize;
+  return w;
+}
+
+// Starts the copy of vector v (at `src`) into dst; `in`: the vector exists.
+// EDGE: the vectors at the tensor's two ends (first, last byte after it) may
+// reach past it and are cut.
+template <bool BF16, bool EDGE>
+__device__ __forceinline__ void fetch_vec(uint4* dst, const uint8_t* src, bool in,
+                                          const void* base, const uint8_t* end) {
+  if constexpr (!EDGE) {
+    cp_async16(dst, in ? src : static_cast<const uint8_t*>(base), in);
+  } else {
+    const uint8_t* first = static_cast<const uint8_t*>(base);
+    if (in && src < first) {
+      // ahead of the first element: single elements, by plain loads
+      uint32_t w[4] = {0, 0, 0, 0};
+      for (int b = int(first - src); b < 16; b += BF16 ? 2 : 4) {
+        if (src + b >= end) break;
+        if constexpr (BF16)
+          w[b / 4] |= uint32_t(__ldg(reinterpret_cast<const uint16_t*>(src + b))) << (8 * (b & 2));
+        else
+          w[b / 4] = __ldg(reinterpret_cast<const uint32_t*>(src + b));
       }
+      *dst = make_uint4(w[0], w[1], w[2], w[3]);
+      return;
     }
+    const int64_t left = end - src;
+    const int bytes = !in ? 0 : (left < 16 ? int(left) : 16);
+    // (nothing is read where bytes is 0; the address is still in range)
+    const uint8_t* from =
+        in ? src : reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(first) & ~uintptr_t(15));
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_addr(dst)),
+                 "l"(from), "r"(bytes)
+                 : "memory");
+  }
+}
+
+// Zero the elements of a row's first or last vector that are not its own.
+template <int VEC>
+__device__ __forceinline__ void mask_vec(F2* a, int e, int cols) {
+#pragma unroll
+  for (int j = 0; j < VEC / 2; ++j) {
+    const bool l = e + 2 * j >= 0 && e + 2 * j < cols, h = e + 2 * j + 1 >= 0 && e + 2 * j + 1 < cols;
+    a[j] = f2(l ? f2_lo(a[j]) : 0.0f, h ? f2_hi(a[j]) : 0.0f);
+  }
+}
+template <bool BF16, int VEC>
+__device__ __forceinline__ void store_part(void* to, int e, int cols, uint4 r) {
+  const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    if (e + j < 0 || e + j >= cols) continue;
+    if constexpr (BF16)
+      static_cast<uint16_t*>(to)[j] = uint16_t(w[j / 2] >> (16 * (j & 1)));
+    else
+      static_cast<uint32_t*>(to)[j] = w[j];
+  }
+}
+
+// Forward. EDGE: rows may start off a 16-byte boundary. QUANT also (or only)
+// writes the 1x32 codes and scales of the rounded y: a group is 32 / VEC
+// adjacent lanes (cols is a multiple of 32 and rows are aligned, so a group
+// never splits over warps).
+template <bool BF16, int NV, bool EDGE, bool QUANT>
+__global__ void __launch_bounds__(512)
+    k_ln_fwd(const void* __restrict__ x, int64_t rows, int cols, int64_t ldx, int misaligned,
+             const float* __restrict__ weight, const float* __restrict__ bias, bool vec_params,
+             float eps, void* __restrict__ y, float* __restrict__ mean_out,
+             float* __restrict__ rstd_out, uint8_t* __restrict__ codes,
+             uint8_t* __restrict__ scales, LnSplit split) {
+  constexpr int VEC = BF16 ? 8 : 4, NP = VEC / 2;
+  using V = Vec<BF16, VEC>;
+  extern __shared__ __align__(16) uint4 ring[];  // [kLnDepth][NV][threads]
+  __shared__ float2 red[2][kLnMaxParts];
+  const Place p = place<VEC, NV>(split, cols, ldx, misaligned);
+  const float inv_n = __fdiv_rn(1.0f, float(cols));
+  const int parts = p.W * p.CS, l = p.lane & (p.P - 1);
+
+  // elements of this warp, and of warp l of the row
+  const float my_n = warp_count<VEC, NV>(p, p.rank, p.w);
+  const float my_inv = my_n > 0.0f ? __fdiv_rn(1.0f, my_n) : 0.0f;
+  const float l_n = l < parts ? warp_count<VEC, NV>(p, l / p.W, l % p.W) : 0.0f;
+  const float l_inv = l_n > 0.0f ? __fdiv_rn(1.0f, l_n) : 0.0f;
+
+  uint4* const mine = ring + threadIdx.x;
+  const uint8_t* const x_end =
+      static_cast<const uint8_t*>(x) + ((rows - 1) * ldx + cols) * int64_t(16 / VEC);
+  Walk wx = walk<BF16>(x, ldx, p);
+  int64_t frow = p.row0;
+  auto fetch = [&](int d) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      fetch_vec<BF16, EDGE>(mine + (d * NV + i) * blockDim.x, wx.at + i * p.step * 16,
+                            frow < rows && p.v0 + i * p.step < p.nvec, x, x_end);
+    cp_async_commit();
+    wx.at += wx.step;
+    frow += p.stride;
+  };
+#pragma unroll
+  for (int d = 0; d < kLnDepth; ++d) fetch(d);
+  Walk wy = walk<BF16>(y, cols, p);
+
+  F2 wk[NV * NP], bk[NV * NP];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = (p.v0 + i * p.step) * VEC - p.off;
+    load_param<VEC>(weight, e, cols, vec_params, 1.0f, wk + i * NP);
+    load_param<VEC>(bias, e, cols, vec_params, 0.0f, bk + i * NP);
   }
 
-  V nx[NV];
-  auto fetch = [&](int64_t row) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = p.t + i * step;
-      if (row < rows && v < nvec)
-        nx[i].load(x, row * ldx + int64_t(v) * VEC);
-      else
-        nx[i].zero();
-    }
-  };
-  int64_t row = int64_t(blockIdx.x) * p.G + p.g;
-  fetch(row);
-  for (int par = 0; row < rows; row += stride, par ^= 1) {
+  // the cluster's CTAs walk the same rows; so do the warps of a group
+  int d = 0, par = 0;
+  for (int64_t row = p.row0; row < rows; row += p.stride, par ^= 1) {
+    cp_async_wait<kLnDepth - 1>();
     F2 a[NV * NP];
 #pragma unroll
-    for (int i = 0; i < NV; ++i) nx[i].unpack(a + i * NP);
-    fetch(row + stride);
+    for (int i = 0; i < NV; ++i) {
+      V in;
+      in.r = mine[(d * NV + i) * blockDim.x];
+      in.unpack(a + i * NP);
+      if constexpr (EDGE) {
+        const int v = p.v0 + i * p.step;
+        if (v == 0 || v == p.nvec - 1) mask_vec<VEC>(a + i * NP, v * VEC - p.off, cols);
+      }
+    }
+    fetch(d);
+    if (++d == kLnDepth) d = 0;
+
     F2 s2 = f2(0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < NV * NP; ++i) s2 = add2(s2, a[i]);
     const float s = warp_sum(__fadd_rn(f2_lo(s2), f2_hi(s2)));
     float mean = __fmul_rn(s, my_inv);
     F2 q2 = f2(0.0f, 0.0f);
-    const F2 mm = VEC == 1 ? f2(-mean, 0.0f) : f2(-mean, -mean);
+    const F2 mm = f2(-mean, -mean);
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (p.t + i * step < nvec) {
+    for (int i = 0; i < NV; ++i) {
+      const int v = p.v0 + i * p.step;
+      if (v >= p.nvec) continue;
+      F2 dv[NP];
 #pragma unroll
-        for (int j = 0; j < NP; ++j) {
-          const F2 d = add2(a[i * NP + j], mm);
-          q2 = fma2(d, d, q2);
-        }
+      for (int j = 0; j < NP; ++j) dv[j] = add2(a[i * NP + j], mm);
+      if constexpr (EDGE) {
+        if (v == 0 || v == p.nvec - 1) mask_vec<VEC>(dv, v * VEC - p.off, cols);
       }
+#pragma unroll
+      for (int j = 0; j < NP; ++j) q2 = fma2(dv[j], dv[j], q2);
+    }
     float m2 = warp_sum(__fadd_rn(f2_lo(q2), f2_hi(q2)));
-    if (W > 1) {
+    if (parts > 1) {
       // one barrier a row: the buffer of this parity is written again two
       // rows on, past the next row's barrier
       float2* rd = red[par];
-      if (p.lane == 0) rd[p.g * W + p.w] = make_float2(s, m2);
-      group_sync(p.g, W);
-      const int l = p.lane & (P - 1);
-      const float2 o = l < W ? rd[p.g * W + l] : make_float2(0.0f, 0.0f);
-      mean = __fmul_rn(part_sum(o.x, P), inv_n);
-      const float ln = __shfl_sync(0xFFFFFFFFu, lane_n, l);
-      const float li = __shfl_sync(0xFFFFFFFFu, lane_inv, l);
-      const float d = __fsub_rn(__fmul_rn(o.x, li), mean);
-      m2 = part_sum(l < W ? __fmaf_rn(__fmul_rn(ln, d), d, o.y) : 0.0f, P);
+      if (p.CS > 1) {
+        if (p.lane < 2) store_pair(&rd[p.rank * p.W + p.w], make_float2(s, m2), p.lane);
+        pair_sync();
+      } else {
+        if (p.lane == 0) rd[p.g * p.W + p.w] = make_float2(s, m2);
+        group_sync(p.g, p.W);
+      }
+      const float2 o = l < parts ? rd[p.g * p.W + l] : make_float2(0.0f, 0.0f);
+      mean = __fmul_rn(part_sum(o.x, p.P), inv_n);
+      const float dm = __fsub_rn(__fmul_rn(o.x, l_inv), mean);
+      m2 = part_sum(l < parts ? __fmaf_rn(__fmul_rn(l_n, dm), dm, o.y) : 0.0f, p.P);
     }
     const float rstd = rsqrt_exact(__fmaf_rn(m2, inv_n, eps));
-    if (p.t == 0) {
+    if (p.v0 == 0) {
       if (mean_out != nullptr) mean_out[row] = mean;
       if (rstd_out != nullptr) rstd_out[row] = rstd;
     }
     const F2 nm = f2(-mean, -mean), rs = f2(rstd, rstd);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = p.t + i * step;
-      const bool in = v < nvec;
+      const int v = p.v0 + i * p.step;
+      const bool in = v < p.nvec;
       if (!QUANT && !in) continue;
       F2 o[NP];
-      F2 wl[NP], bl[NP];
-      if constexpr (!kKeep) {
-        if (in) {
-          load_param<VEC>(weight, int64_t(v) * VEC, 1.0f, wl);
-          load_param<VEC>(bias, int64_t(v) * VEC, 0.0f, bl);
-        } else {
 #pragma unroll
-          for (int j = 0; j < NP; ++j) wl[j] = bl[j] = f2(0.0f, 0.0f);
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const F2 h = mul2(add2(a[i * NP + j], nm), rs);
-        o[j] = fma2(h, kKeep ? wk[kKeep ? i * NP + j : 0] : wl[j],
-                    kKeep ? bk[kKeep ? i * NP + j : 0] : bl[j]);
-      }
+      for (int j = 0; j < NP; ++j)
+        o[j] = fma2(mul2(add2(a[i * NP + j], nm), rs), wk[i * NP + j], bk[i * NP + j]);
       V out;
       out.pack(o);
-      if (in && y != nullptr) out.store(y, row * cols + int64_t(v) * VEC);
-      if constexpr (QUANT && VEC > 1) {
-        const int64_t e = row * cols + int64_t(v) * VEC;
+      if (in && y != nullptr) {
+        uint8_t* to = const_cast<uint8_t*>(wy.at) + i * p.step * 16;
+        if (EDGE && (v == 0 || v == p.nvec - 1))
+          store_part<BF16, VEC>(to, v * VEC - p.off, cols, out.r);
+        else
+          __stcs(reinterpret_cast<uint4*>(to), out.r);
+      }
+      if constexpr (QUANT) {
+        const int64_t at = row * cols + int64_t(v) * VEC;
         if constexpr (BF16) {
           uint32_t am = bf16x8_absmax(out.r);
           am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
@@ -356,8 +423,8 @@ __global__ void __launch_bounds__(512)
           }
           const uint32_t word = sb == 0xFFu ? 0u : e2m1x8_rn(qv);
           if (in) {
-            *reinterpret_cast<uint32_t*>(codes + e / 2) = word;
-            if ((p.lane & 3) == 0) scales[e / 32] = static_cast<uint8_t>(sb);
+            *reinterpret_cast<uint32_t*>(codes + at / 2) = word;
+            if ((p.lane & 3) == 0) scales[at / 32] = static_cast<uint8_t>(sb);
           }
         } else {
           uint32_t am = max(max(out.r.x & 0x7FFFFFFFu, out.r.y & 0x7FFFFFFFu),
@@ -373,13 +440,16 @@ __global__ void __launch_bounds__(512)
                                __fmul_rn(__uint_as_float(out.r.w), mul), 0, 0, 0, 0};
           const uint32_t word = sb == 0xFFu ? 0u : e2m1x8_rn(qv);
           if (in) {
-            *reinterpret_cast<uint16_t*>(codes + e / 2) = static_cast<uint16_t>(word);
-            if ((p.lane & 7) == 0) scales[e / 32] = static_cast<uint8_t>(sb);
+            *reinterpret_cast<uint16_t*>(codes + at / 2) = static_cast<uint16_t>(word);
+            if ((p.lane & 7) == 0) scales[at / 32] = static_cast<uint8_t>(sb);
           }
         }
       }
     }
+    wy.at += wy.step;
   }
+  cp_async_wait<0>();
+  if (p.CS > 1) pair_sync();  // no CTA ends while the other may still write to it
 }
 
 // Rows wider than the registers of 16 warps: one CTA a row, three passes
@@ -460,128 +530,121 @@ __global__ void __launch_bounds__(kLnGenThreads)
   }
 }
 
-// Backward. SMACC keeps the column sums of dw and db in shared memory
-// ([2][cols] floats) instead of registers; PARAMS = false leaves them out.
-template <bool BF16, int VEC, int NV, bool SMACC, bool PARAMS>
+// Backward; PARAMS = false leaves dw and db out.
+template <bool BF16, int NV, bool EDGE, bool PARAMS>
 __global__ void __launch_bounds__(512)
     k_ln_bwd(const void* __restrict__ dy, const void* __restrict__ x, int64_t rows, int cols,
-             int64_t lddy, int64_t ldx, const float* __restrict__ weight,
-             const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
-             void* __restrict__ dx, float* __restrict__ partial, int W, int P) {
+             int64_t lddy, int64_t ldx, int misaligned, const float* __restrict__ weight,
+             bool vec_params, const float* __restrict__ mean_in,
+             const float* __restrict__ rstd_in, void* __restrict__ dx,
+             float* __restrict__ partial, LnSplit split) {
+  constexpr int VEC = BF16 ? 8 : 4, NP = VEC / 2;
   using V = Vec<BF16, VEC>;
-  constexpr int NP = V::kPairs;
-  constexpr bool kRegAcc = PARAMS && !SMACC;
-  constexpr bool kKeep = !SMACC;  // the weight's columns in registers
-  extern __shared__ __align__(16) float sacc[];
-  __shared__ float2 red[2][kLnMaxWarps];
-  const Place p = place(W, P);
-  const int nvec = cols / VEC, step = 32 * W;
-  const int64_t stride = int64_t(gridDim.x) * p.G;
+  extern __shared__ __align__(16) uint4 ring[];  // [kLnDepth][2 NV][threads]
+  __shared__ float2 red[2][kLnMaxParts];
+  const Place p = place<VEC, NV>(split, cols, ldx, misaligned);
   const float inv_n = __fdiv_rn(1.0f, float(cols));
+  const int parts = p.W * p.CS, l = p.lane & (p.P - 1);
   const F2 zero = f2(0.0f, 0.0f);
 
-  F2 wk[kKeep ? NV * NP : 1];
-  F2 aw[kRegAcc ? NV * NP : 1], ab[kRegAcc ? NV * NP : 1];
+  uint4* const mine = ring + threadIdx.x;
+  const uint8_t* const x_end =
+      static_cast<const uint8_t*>(x) + ((rows - 1) * ldx + cols) * int64_t(16 / VEC);
+  const uint8_t* const dy_end =
+      static_cast<const uint8_t*>(dy) + ((rows - 1) * lddy + cols) * int64_t(16 / VEC);
+  Walk wx = walk<BF16>(x, ldx, p), wg = walk<BF16>(dy, lddy, p);
+  int64_t frow = p.row0;
+  auto fetch = [&](int d) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool in = frow < rows && p.v0 + i * p.step < p.nvec;
+      fetch_vec<BF16, EDGE>(mine + (d * 2 * NV + 2 * i) * blockDim.x, wx.at + i * p.step * 16, in,
+                            x, x_end);
+      fetch_vec<BF16, EDGE>(mine + (d * 2 * NV + 2 * i + 1) * blockDim.x,
+                            wg.at + i * p.step * 16, in, dy, dy_end);
+    }
+    cp_async_commit();
+    wx.at += wx.step, wg.at += wg.step;
+    frow += p.stride;
+  };
+#pragma unroll
+  for (int d = 0; d < kLnDepth; ++d) fetch(d);
+  Walk wo = walk<BF16>(dx, cols, p);
+
+  F2 wk[NV * NP];
+  F2 aw[PARAMS ? NV * NP : 1], ab[PARAMS ? NV * NP : 1];
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int v = p.t + i * step;
-    if constexpr (kKeep) {
-      if (v < nvec) {
-        load_param<VEC>(weight, int64_t(v) * VEC, 1.0f, wk + i * NP);
-      } else {
-#pragma unroll
-        for (int j = 0; j < NP; ++j) wk[i * NP + j] = zero;
-      }
-    }
-    if constexpr (kRegAcc) {
+    load_param<VEC>(weight, (p.v0 + i * p.step) * VEC - p.off, cols, vec_params, 1.0f,
+                    wk + i * NP);
+    if constexpr (PARAMS) {
 #pragma unroll
       for (int j = 0; j < NP; ++j) aw[i * NP + j] = ab[i * NP + j] = zero;
     }
-    if constexpr (PARAMS && SMACC) {
-      if (v < nvec) {
+  }
+
+  float nmean = 0.0f, nrstd = 0.0f;
+  if (p.row0 < rows) nmean = __ldg(mean_in + p.row0), nrstd = __ldg(rstd_in + p.row0);
+  int d = 0, par = 0;
+  for (int64_t row = p.row0; row < rows; row += p.stride, par ^= 1) {
+    const float mean = nmean, rstd = nrstd;
+    if (row + p.stride < rows)
+      nmean = __ldg(mean_in + row + p.stride), nrstd = __ldg(rstd_in + row + p.stride);
+    cp_async_wait<kLnDepth - 1>();
+    F2 h[NV * NP], g[NV * NP];
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          sacc[v * VEC + j] = 0.0f;
-          sacc[cols + v * VEC + j] = 0.0f;
+    for (int i = 0; i < NV; ++i) {
+      V in;
+      in.r = mine[(d * 2 * NV + 2 * i) * blockDim.x];
+      in.unpack(h + i * NP);
+      in.r = mine[(d * 2 * NV + 2 * i + 1) * blockDim.x];
+      in.unpack(g + i * NP);
+      if constexpr (EDGE) {
+        const int v = p.v0 + i * p.step;
+        if (v == 0 || v == p.nvec - 1) {
+          mask_vec<VEC>(h + i * NP, v * VEC - p.off, cols);
+          mask_vec<VEC>(g + i * NP, v * VEC - p.off, cols);
         }
       }
     }
-  }
+    fetch(d);
+    if (++d == kLnDepth) d = 0;
 
-  V nx[NV], ny[NV];
-  float nmean = 0.0f, nrstd = 0.0f;
-  auto fetch = [&](int64_t row) {
-    if (row < rows) nmean = __ldg(mean_in + row), nrstd = __ldg(rstd_in + row);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = p.t + i * step;
-      if (row < rows && v < nvec) {
-        nx[i].load(x, row * ldx + int64_t(v) * VEC);
-        ny[i].load(dy, row * lddy + int64_t(v) * VEC);
-      } else {
-        nx[i].zero(), ny[i].zero();
-      }
-    }
-  };
-  int64_t row = int64_t(blockIdx.x) * p.G + p.g;
-  fetch(row);
-  for (int par = 0; row < rows; row += stride, par ^= 1) {
-    F2 h[NV * NP], g[NV * NP];
-    const float mean = nmean, rstd = nrstd;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) nx[i].unpack(h + i * NP), ny[i].unpack(g + i * NP);
-    fetch(row + stride);
+    // a masked element has g = 0 and w = 0: it adds nothing anywhere
     const F2 nm = f2(-mean, -mean), rs = f2(rstd, rstd);
     F2 c1 = zero, c2 = zero;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int v = p.t + i * step;
-      if (v >= nvec) continue;
-      F2 wl[NP], sw[NP], sb[NP];
-      if constexpr (!kKeep) load_param<VEC>(weight, int64_t(v) * VEC, 1.0f, wl);
-      if constexpr (PARAMS && SMACC) {
-        load_shared<VEC>(sacc + v * VEC, sw);
-        load_shared<VEC>(sacc + cols + v * VEC, sb);
+    for (int k = 0; k < NV * NP; ++k) {
+      h[k] = mul2(add2(h[k], nm), rs);
+      if constexpr (PARAMS) {
+        aw[k] = fma2(g[k], h[k], aw[k]);
+        ab[k] = add2(ab[k], g[k]);
       }
-#pragma unroll
-      for (int j = 0; j < NP; ++j) {
-        const int k = i * NP + j;
-        h[k] = mul2(add2(h[k], nm), rs);
-        if constexpr (kRegAcc) {
-          aw[k] = fma2(g[k], h[k], aw[k]);
-          ab[k] = add2(ab[k], g[k]);
-        }
-        if constexpr (PARAMS && SMACC) {
-          sw[j] = fma2(g[k], h[k], sw[j]);
-          sb[j] = add2(sb[j], g[k]);
-        }
-        g[k] = mul2(g[k], kKeep ? wk[kKeep ? k : 0] : wl[j]);
-        c1 = add2(c1, g[k]);
-        c2 = fma2(g[k], h[k], c2);
-      }
-      if constexpr (PARAMS && SMACC) {
-        store_shared<VEC>(sacc + v * VEC, sw);
-        store_shared<VEC>(sacc + cols + v * VEC, sb);
-      }
+      g[k] = mul2(g[k], wk[k]);
+      c1 = add2(c1, g[k]);
+      c2 = fma2(g[k], h[k], c2);
     }
-    // the high half of a single element's pair is padding
-    float s1 = warp_sum(VEC == 1 ? f2_lo(c1) : __fadd_rn(f2_lo(c1), f2_hi(c1)));
-    float s2 = warp_sum(VEC == 1 ? f2_lo(c2) : __fadd_rn(f2_lo(c2), f2_hi(c2)));
-    if (W > 1) {
+    float s1 = warp_sum(__fadd_rn(f2_lo(c1), f2_hi(c1)));
+    float s2 = warp_sum(__fadd_rn(f2_lo(c2), f2_hi(c2)));
+    if (parts > 1) {
       float2* rd = red[par];
-      if (p.lane == 0) rd[p.g * W + p.w] = make_float2(s1, s2);
-      group_sync(p.g, W);
-      const int l = p.lane & (P - 1);
-      const float2 o = l < W ? rd[p.g * W + l] : make_float2(0.0f, 0.0f);
-      s1 = part_sum(o.x, P);
-      s2 = part_sum(o.y, P);
+      if (p.CS > 1) {
+        if (p.lane < 2) store_pair(&rd[p.rank * p.W + p.w], make_float2(s1, s2), p.lane);
+        pair_sync();
+      } else {
+        if (p.lane == 0) rd[p.g * p.W + p.w] = make_float2(s1, s2);
+        group_sync(p.g, p.W);
+      }
+      const float2 o = l < parts ? rd[p.g * p.W + l] : make_float2(0.0f, 0.0f);
+      s1 = part_sum(o.x, p.P);
+      s2 = part_sum(o.y, p.P);
     }
     const float m1 = -__fmul_rn(s1, inv_n), m2 = -__fmul_rn(s2, inv_n);
     const F2 k1 = f2(m1, m1), k2 = f2(m2, m2);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = p.t + i * step;
-      if (v >= nvec) continue;
+      const int v = p.v0 + i * p.step;
+      if (v >= p.nvec) continue;
       F2 o[NP];
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
@@ -590,49 +653,50 @@ __global__ void __launch_bounds__(512)
       }
       V out;
       out.pack(o);
-      out.store(dx, row * cols + int64_t(v) * VEC);
+      uint8_t* to = const_cast<uint8_t*>(wo.at) + i * p.step * 16;
+      if (EDGE && (v == 0 || v == p.nvec - 1))
+        store_part<BF16, VEC>(to, v * VEC - p.off, cols, out.r);
+      else
+        __stcs(reinterpret_cast<uint4*>(to), out.r);
     }
+    wo.at += wo.step;
   }
+  cp_async_wait<0>();
 
   if constexpr (PARAMS) {
-    float* pw = partial + int64_t(blockIdx.x) * 2 * cols;
-    if constexpr (SMACC) {
-      // one group a CTA: every thread writes the columns it summed
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const int v = p.t + i * step;
-        if (v >= nvec) continue;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          pw[v * VEC + j] = sacc[v * VEC + j];
-          pw[cols + v * VEC + j] = sacc[cols + v * VEC + j];
-        }
-      }
-    } else {
-      // the groups of a CTA add into shared memory one after the other (the
-      // last writes the partial row)
-      for (int g = 0; g < p.G; ++g) {
-        if (g > 0) __syncthreads();
-        if (p.g != g) continue;
+    // the groups of a CTA add into shared memory one after the other (the
+    // last writes the partial row); groups have their own `off`
+    float* pw = partial + int64_t(blockIdx.x / p.CS) * 2 * cols;
+    float* sacc = reinterpret_cast<float*>(ring);
+    if (p.G > 1) {
+      __syncthreads();  // every group is done with the ring
+      for (int c = threadIdx.x; c < 2 * cols; c += blockDim.x) sacc[c] = 0.0f;
+      __syncthreads();
+    }
+    for (int g = 0; g < p.G; ++g) {
+      if (p.g == g) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int v = p.t + i * step;
-          if (v >= nvec) continue;
+          const int e = (p.v0 + i * p.step) * VEC - p.off;
 #pragma unroll
           for (int j = 0; j < VEC; ++j) {
-            float a = (j & 1) ? f2_hi(aw[i * NP + j / 2]) : f2_lo(aw[i * NP + j / 2]);
-            float b = (j & 1) ? f2_hi(ab[i * NP + j / 2]) : f2_lo(ab[i * NP + j / 2]);
-            const int c = v * VEC + j;
-            if (g > 0) a = __fadd_rn(a, sacc[c]), b = __fadd_rn(b, sacc[cols + c]);
-            if (g + 1 == p.G)
+            const int c = e + j;
+            if (c < 0 || c >= cols) continue;
+            const float a = (j & 1) ? f2_hi(aw[i * NP + j / 2]) : f2_lo(aw[i * NP + j / 2]);
+            const float b = (j & 1) ? f2_hi(ab[i * NP + j / 2]) : f2_lo(ab[i * NP + j / 2]);
+            if (p.G == 1)
               pw[c] = a, pw[cols + c] = b;
             else
-              sacc[c] = a, sacc[cols + c] = b;
+              sacc[c] = __fadd_rn(sacc[c], a), sacc[cols + c] = __fadd_rn(sacc[cols + c], b);
           }
         }
       }
+      if (p.G > 1) __syncthreads();
     }
+    if (p.G > 1)
+      for (int c = threadIdx.x; c < 2 * cols; c += blockDim.x) pw[c] = sacc[c];
   }
+  if (p.CS > 1) pair_sync();
 }
 
 // Rows wider than the registers of 16 warps: dx with one CTA a row, and the
@@ -720,7 +784,8 @@ __global__ void __launch_bounds__(kLnRedThreads)
 // ---------------------------------------------------------------------------
 
 struct LnShape {
-  int nv, W, P, G, threads;
+  int nv, threads, clusters;  // clusters: most that `stride` allows, 0: any
+  LnSplit split;
 };
 
 int sm_count() {
@@ -730,33 +795,84 @@ int sm_count() {
   return sms;
 }
 
-// The number of vectors a thread holds (one of `nvs`, ascending) and the
-// warps W of a row: the preferred count `want` unless the row needs more;
-// few rows (less than two an SM) take the smallest count, which spreads a
-// row over the most threads. Narrow rows share a CTA of about 8 warps.
-bool ln_shape(int64_t cols, int vec, const int* nvs, int n_nvs, int want, int64_t rows,
-              int block_warps, LnShape* s) {
-  if (cols % vec != 0) return false;
-  const int64_t nvec = cols / vec;
+// Vectors per thread and warps per row: `big` vectors, or one where a row is
+// narrow (one warp) or rows are few (less than two an SM: one vector a
+// thread spreads a row over the most threads). Rows that 16 warps cannot
+// hold take a cluster of two CTAs. Narrow rows share a CTA of about
+// `block_warps` warps.
+bool ln_shape(int64_t nvec, int big, int64_t rows, int block_warps, LnShape* s) {
   const bool few = rows < 2 * int64_t(sm_count());
-  for (int i = 0; i < n_nvs; ++i) {
-    const int64_t W = (nvec + 32 * nvs[i] - 1) / (32 * nvs[i]);
-    if (W > kLnMaxWarps) continue;
-    if (!few && nvs[i] < want && i + 1 < n_nvs && W > 1) continue;
-    s->nv = nvs[i];
-    s->W = int(W);
-    s->P = 1;
-    while (s->P < s->W) s->P *= 2;
-    s->G = few ? 1 : (block_warps / s->W > 1 ? block_warps / s->W : 1);
-    s->threads = 32 * s->W * s->G;
+  for (int nv = 1; nv <= big; nv += big - 1) {
+    const int64_t W = (nvec + 32 * nv - 1) / (32 * nv);
+    if (nv == 1 && !(W == 1 || (few && W <= kLnMaxWarps)) && big > 1) continue;
+    s->nv = nv;
+    s->split.CS = 1;
+    s->split.W = int(W);
+    if (W > kLnMaxWarps) {
+      if (W > 2 * kLnMaxWarps) return false;
+      s->split.CS = 2;
+      s->split.W = int((W + 1) / 2);
+    }
+    s->split.P = 1;
+    while (s->split.P < s->split.W * s->split.CS) s->split.P *= 2;
+    s->split.G = few || s->split.CS > 1 || W >= block_warps ? 1 : int(block_warps / W);
+    s->threads = 32 * s->split.W * s->split.G;
     return true;
   }
   return false;
 }
 
-bool aligned_rows(const void* p, int64_t ld, int size) {
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * size) % 16 == 0;
+// Whether rows of these tensors (base, stride) can move as 16-byte vectors:
+// every row on a boundary (*edge = false), or all of them without padding
+// and equally far off it (*edge = true, *misaligned = elements).
+bool vector_rows(const void* const* p, const int64_t* ld, int n, int64_t cols, int size,
+                 bool* edge, int* misaligned) {
+  const int vec = 16 / size;
+  bool whole = cols % vec == 0, dense = true;
+  for (int i = 0; i < n; ++i) {
+    if (p[i] == nullptr) continue;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(p[i]) & 15u;
+    if (a != 0 || (ld[i] * size) % 16 != 0) whole = false;
+    if (ld[i] != cols || a != (reinterpret_cast<uintptr_t>(p[0]) & 15u)) dense = false;
+  }
+  *edge = !whole;
+  *misaligned = int((reinterpret_cast<uintptr_t>(p[0]) & 15u) / size);
+  return whole || dense;
 }
+
+// Persistent grid of whole clusters; with rows off the boundary the row
+// stride (clusters x groups) is a multiple of the vector length.
+int ln_grid(const void* kern, const LnShape& sh, size_t smem, int64_t rows, bool edge, int vec,
+            int64_t most) {
+  int64_t want = (rows + sh.split.G - 1) / sh.split.G;
+  if (want > most) want = most;
+  int64_t n = persistent_grid(kern, sh.threads, smem, want * sh.split.CS) / sh.split.CS;
+  if (n < 1) n = 1;
+  if (edge && n * sh.split.G < rows) {
+    const int64_t unit = sh.split.G >= vec ? 1 : vec / sh.split.G;
+    n = n / unit * unit > 0 ? n / unit * unit : unit;
+  }
+  return int(n * sh.split.CS);
+}
+
+template <typename... P, typename... A>
+cudaError_t ln_launch(void (*kern)(P...), int grid, const LnShape& sh, size_t smem,
+                      cudaStream_t s, A... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(grid));
+  cfg.blockDim = dim3(unsigned(sh.threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(sh.split.CS);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = sh.split.CS > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 struct FwdArgs {
   const void* x;
@@ -769,45 +885,38 @@ struct FwdArgs {
   cudaStream_t s;
 };
 
-template <bool BF16, int VEC, int NV, bool QUANT>
-cudaError_t fwd_launch(const FwdArgs& a, const LnShape& sh) {
-  auto kern = k_ln_fwd<BF16, VEC, NV, QUANT>;
-  const int grid = persistent_grid(reinterpret_cast<const void*>(kern), sh.threads, 0,
-                                   (a.rows + sh.G - 1) / sh.G);
-  kern<<<grid, sh.threads, 0, a.s>>>(a.x, a.rows, int(a.cols), a.ldx, a.weight, a.bias, a.eps,
-                                     a.y, a.mean, a.rstd, a.codes, a.scales, sh.W, sh.P);
-  return cudaGetLastError();
+template <bool BF16, int NV, bool EDGE, bool QUANT>
+cudaError_t fwd_launch(const FwdArgs& a, const LnShape& sh, int misaligned) {
+  auto kern = k_ln_fwd<BF16, NV, EDGE, QUANT>;
+  const void* k = reinterpret_cast<const void*>(kern);
+  const size_t smem = size_t(sh.threads) * NV * 16 * kLnDepth;
+  const cudaError_t e = allow_smem(k, smem);
+  if (e != cudaSuccess) return e;
+  const int grid = ln_grid(k, sh, smem, a.rows, EDGE, BF16 ? 8 : 4, int64_t(1) << 30);
+  return ln_launch(kern, grid, sh, smem, a.s, a.x, a.rows, int(a.cols), a.ldx, misaligned,
+                   a.weight, a.bias, !EDGE && aligned16(a.weight) && aligned16(a.bias), a.eps,
+                   a.y, a.mean, a.rstd, a.codes, a.scales, sh.split);
 }
 
-template <bool BF16, bool QUANT>
-cudaError_t fwd_vec(const FwdArgs& a, const LnShape& sh) {
-  constexpr int VEC = BF16 ? 8 : 4;
-  switch (sh.nv) {
-    case 1: return fwd_launch<BF16, VEC, 1, QUANT>(a, sh);
-    case 2: return fwd_launch<BF16, VEC, 2, QUANT>(a, sh);
-    case 3: return fwd_launch<BF16, VEC, 3, QUANT>(a, sh);
-    case 4: return fwd_launch<BF16, VEC, 4, QUANT>(a, sh);
-    default: return fwd_launch<BF16, VEC, 8, QUANT>(a, sh);
-  }
+template <bool BF16, int NV>
+cudaError_t fwd_nv(const FwdArgs& a, const LnShape& sh, bool edge, int misaligned) {
+  if (a.codes != nullptr) return fwd_launch<BF16, NV, false, true>(a, sh, 0);
+  return edge ? fwd_launch<BF16, NV, true, false>(a, sh, misaligned)
+              : fwd_launch<BF16, NV, false, false>(a, sh, 0);
 }
 
 template <bool BF16>
 cudaError_t fwd_any(const FwdArgs& a) {
-  constexpr int kSize = BF16 ? 2 : 4, VEC = 16 / kSize;
-  static const int bf_nvs[] = {1, 2, 3, 4}, f_nvs[] = {1, 2, 4, 8}, one_nvs[] = {8, 16, 32};
+  constexpr int kSize = BF16 ? 2 : 4, VEC = 16 / kSize, BIG = BF16 ? 3 : 4;
   LnShape sh;
-  const bool vec = a.cols % VEC == 0 && aligned_rows(a.x, a.ldx, kSize) &&
-                   (a.y == nullptr || aligned_rows(a.y, a.cols, kSize)) &&
-                   aligned_rows(a.weight, 0, 4) && aligned_rows(a.bias, 0, 4);
-  if (vec && ln_shape(a.cols, VEC, BF16 ? bf_nvs : f_nvs, 4, BF16 ? 3 : 4, a.rows, 8, &sh))
-    return a.codes != nullptr ? fwd_vec<BF16, true>(a, sh) : fwd_vec<BF16, false>(a, sh);
-  if (a.codes == nullptr && ln_shape(a.cols, 1, one_nvs, 3, 16, a.rows, 8, &sh)) {
-    switch (sh.nv) {
-      case 8: return fwd_launch<BF16, 1, 8, false>(a, sh);
-      case 16: return fwd_launch<BF16, 1, 16, false>(a, sh);
-      default: return fwd_launch<BF16, 1, 32, false>(a, sh);
-    }
-  }
+  bool edge;
+  int mis;
+  const void* const ptrs[] = {a.x, a.y};
+  const int64_t lds[] = {a.ldx, a.cols};
+  if (a.cols <= kLnMaxCols && vector_rows(ptrs, lds, 2, a.cols, kSize, &edge, &mis) &&
+      !(edge && a.codes != nullptr) &&
+      ln_shape((a.cols + VEC - 1) / VEC + (edge ? 1 : 0), BIG, a.rows, 4, &sh))
+    return sh.nv == 1 ? fwd_nv<BF16, 1>(a, sh, edge, mis) : fwd_nv<BF16, BIG>(a, sh, edge, mis);
   auto kern = k_ln_fwd_wide<BF16>;
   const int grid =
       persistent_grid(reinterpret_cast<const void*>(kern), kLnGenThreads, 0, a.rows);
@@ -839,62 +948,42 @@ cudaError_t params_launch(const BwdArgs& a, int n) {
                             a.dw, a.db);
 }
 
-template <bool BF16, int VEC, int NV, bool SMACC, bool PARAMS>
-cudaError_t bwd_launch(const BwdArgs& a, const LnShape& sh) {
-  auto kern = k_ln_bwd<BF16, VEC, NV, SMACC, PARAMS>;
-  const size_t smem = PARAMS && (SMACC || sh.G > 1) ? size_t(a.cols) * 8 : 0;
-  if (smem > 0) {
-    const cudaError_t e =
-        cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-    if (e != cudaSuccess) return e;
-  }
-  int64_t blocks = (a.rows + sh.G - 1) / sh.G;
-  if (blocks > kLnMaxPartials) blocks = kLnMaxPartials;
-  const int grid = persistent_grid(reinterpret_cast<const void*>(kern), sh.threads, smem, blocks);
-  kern<<<grid, sh.threads, smem, a.s>>>(a.dy, a.x, a.rows, int(a.cols), a.lddy, a.ldx, a.weight,
-                                        a.mean, a.rstd, a.dx, a.partial, sh.W, sh.P);
-  const cudaError_t e = cudaGetLastError();
+template <bool BF16, int NV, bool EDGE, bool PARAMS>
+cudaError_t bwd_launch(const BwdArgs& a, const LnShape& sh, int misaligned) {
+  auto kern = k_ln_bwd<BF16, NV, EDGE, PARAMS>;
+  const void* k = reinterpret_cast<const void*>(kern);
+  size_t smem = size_t(sh.threads) * 2 * NV * 16 * kLnDepth;
+  if (PARAMS && sh.split.G > 1 && smem < size_t(a.cols) * 8) smem = size_t(a.cols) * 8;
+  cudaError_t e = allow_smem(k, smem);
+  if (e != cudaSuccess) return e;
+  const int grid = ln_grid(k, sh, smem, a.rows, EDGE, BF16 ? 8 : 4, kLnMaxPartials);
+  e = ln_launch(kern, grid, sh, smem, a.s, a.dy, a.x, a.rows, int(a.cols), a.lddy, a.ldx,
+                misaligned, a.weight, !EDGE && aligned16(a.weight), a.mean, a.rstd, a.dx,
+                a.partial, sh.split);
   if (e != cudaSuccess || !PARAMS) return e;
-  return params_launch(a, grid);
+  return params_launch(a, grid / sh.split.CS);
 }
 
-template <bool BF16, int VEC, int NV, bool SMACC>
-cudaError_t bwd_params(const BwdArgs& a, const LnShape& sh) {
-  return a.dw != nullptr ? bwd_launch<BF16, VEC, NV, SMACC, true>(a, sh)
-                         : bwd_launch<BF16, VEC, NV, SMACC, false>(a, sh);
+template <bool BF16, int NV>
+cudaError_t bwd_nv(const BwdArgs& a, const LnShape& sh, bool edge, int misaligned) {
+  if (a.dw != nullptr)
+    return edge ? bwd_launch<BF16, NV, true, true>(a, sh, misaligned)
+                : bwd_launch<BF16, NV, false, true>(a, sh, 0);
+  return edge ? bwd_launch<BF16, NV, true, false>(a, sh, misaligned)
+              : bwd_launch<BF16, NV, false, false>(a, sh, 0);
 }
 
 template <bool BF16>
 cudaError_t bwd_any(const BwdArgs& a) {
-  constexpr int kSize = BF16 ? 2 : 4, VEC = 16 / kSize;
-  static const int bf_nvs[] = {1, 2, 4}, f_nvs[] = {2, 4, 8}, one_nvs[] = {8, 16, 32};
+  constexpr int kSize = BF16 ? 2 : 4, VEC = 16 / kSize, BIG = BF16 ? 2 : 4;
   LnShape sh;
-  const bool vec = a.cols % VEC == 0 && aligned_rows(a.x, a.ldx, kSize) &&
-                   aligned_rows(a.dy, a.lddy, kSize) && aligned_rows(a.dx, a.cols, kSize) &&
-                   aligned_rows(a.weight, 0, 4);
-  if (vec && ln_shape(a.cols, VEC, BF16 ? bf_nvs : f_nvs, 3, BF16 ? 2 : 4, a.rows, 4, &sh)) {
-    if constexpr (BF16) {
-      switch (sh.nv) {
-        case 1: return bwd_params<BF16, VEC, 1, false>(a, sh);
-        case 2: return bwd_params<BF16, VEC, 2, false>(a, sh);
-        default: return bwd_params<BF16, VEC, 4, true>(a, sh);
-      }
-    } else {
-      switch (sh.nv) {
-        case 2: return bwd_params<BF16, VEC, 2, false>(a, sh);
-        case 4: return bwd_params<BF16, VEC, 4, false>(a, sh);
-        default: return bwd_params<BF16, VEC, 8, true>(a, sh);
-      }
-    }
-  }
-  if (ln_shape(a.cols, 1, one_nvs, 3, 8, a.rows, 4, &sh)) {
-    switch (sh.nv) {
-      case 8: return bwd_params<BF16, 1, 8, false>(a, sh);
-      case 16: return bwd_params<BF16, 1, 16, true>(a, sh);
-      default: return bwd_params<BF16, 1, 32, true>(a, sh);
-    }
-  }
+  bool edge;
+  int mis;
+  const void* const ptrs[] = {a.x, a.dy, a.dx};
+  const int64_t lds[] = {a.ldx, a.lddy, a.cols};
+  if (a.cols <= kLnMaxCols && vector_rows(ptrs, lds, 3, a.cols, kSize, &edge, &mis) &&
+      ln_shape((a.cols + VEC - 1) / VEC + (edge ? 1 : 0), BIG, a.rows, 8, &sh))
+    return sh.nv == 1 ? bwd_nv<BF16, 1>(a, sh, edge, mis) : bwd_nv<BF16, BIG>(a, sh, edge, mis);
   auto kern = k_ln_bwd_wide<BF16>;
   const int grid =
       persistent_grid(reinterpret_cast<const void*>(kern), kLnGenThreads, 0, a.rows);

@@ -554,8 +554,7 @@ cudaError_t ns_gemm_bn(const NsOperand& a, const NsOperand& b, const NsArgs& arg
   auto kern = k_ns_gemm<BN, A_MN, B_MN, MODE>;
   constexpr size_t smem = L::kBytes + 1024;
   const cudaError_t e =
-      cudaFuncSetAttribute(reinterpret_cast<const void*>(kern),
-                           cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+      allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = ns_tiles<BN>(MODE == kGram || MODE == kSquare, (args.m + kSM - 1) / kSM,
                                      (args.n + BN - 1) / BN);

@@ -1133,16 +1133,51 @@ __global__ void __launch_bounds__(kDqThreads, 3)
 
 int persistent_grid(const void* kernel, int threads, size_t smem,
                     int64_t work_blocks) {
-  int dev = 0, sms = 148, per_sm = 1;
-  if (cudaGetDevice(&dev) == cudaSuccess)
+  // The resident-block count of a (kernel, launch shape, device) never
+  // changes; asking for it costs about a microsecond per call, so the last
+  // answers are kept (per thread: no locking).
+  struct Entry {
+    const void* kernel;
+    int threads, dev;
+    size_t smem;
+    int64_t grid;
+  };
+  constexpr int kEntries = 64;
+  static thread_local Entry cache[kEntries] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  const size_t h = (reinterpret_cast<uintptr_t>(kernel) >> 4) * 31 + size_t(threads) * 7 + smem;
+  Entry& c = cache[h % kEntries];
+  if (c.kernel != kernel || c.threads != threads || c.smem != smem || c.dev != dev) {
+    int sms = 148, per_sm = 1;
     cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads,
-                                                    smem) != cudaSuccess ||
-      per_sm < 1)
-    per_sm = 1;
-  int64_t g = int64_t(sms) * per_sm;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads,
+                                                      smem) != cudaSuccess ||
+        per_sm < 1)
+      per_sm = 1;
+    c = {kernel, threads, dev, smem, int64_t(sms) * per_sm};
+  }
+  int64_t g = c.grid;
   if (work_blocks < g) g = work_blocks;
   return static_cast<int>(g < 1 ? 1 : g);
+}
+
+cudaError_t allow_smem(const void* kernel, size_t bytes) {
+  struct Entry {
+    const void* kernel;
+    int dev;
+    size_t bytes;
+  };
+  constexpr int kEntries = 64;
+  static thread_local Entry cache[kEntries] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  Entry& c = cache[(reinterpret_cast<uintptr_t>(kernel) >> 4) % kEntries];
+  if (c.kernel == kernel && c.dev == dev && c.bytes >= bytes) return cudaSuccess;
+  const cudaError_t e = cudaFuncSetAttribute(
+      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  if (e == cudaSuccess) c = {kernel, dev, bytes};
+  return e;
 }
 
 template <bool BF16, bool SR, bool OAS>
