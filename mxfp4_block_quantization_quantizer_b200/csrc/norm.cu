@@ -40,7 +40,11 @@ namespace {
 
 constexpr int kLnMaxWarps = 16;      // warps of a CTA that share a row
 constexpr int kLnMaxParts = 32;      // ... and of a cluster
-constexpr int kLnDepth = 3;          // rows in flight per group
+// Rows in flight per group, and what the forward kernels are compiled for:
+// the largest vector counts run with at most 8 warps a CTA, three CTAs an SM.
+__host__ __device__ constexpr int ln_depth(int nv) { return nv == 1 ? 4 : 2; }
+__host__ __device__ constexpr int ln_threads(bool bf16, int nv) { return nv == (bf16 ? 6 : 8) ? 256 : 512; }
+__host__ __device__ constexpr int ln_blocks(bool bf16, int nv) { return nv == (bf16 ? 6 : 8) ? 3 : 1; }
 constexpr int64_t kLnMaxCols = 1 << 16;  // far above what a cluster holds
 constexpr int kLnGenThreads = 512;   // the kernels for wider rows
 constexpr int kLnRedThreads = 1024;
@@ -103,29 +107,6 @@ struct Vec<false, 4> {
                    __float_as_uint(f2_lo(p[1])), __float_as_uint(f2_hi(p[1])));
   }
 };
-// VEC fp32 parameters of columns e .. e + VEC - 1 as pairs (columns outside
-// the row: zero); `fill` where there is no parameter tensor.
-template <int VEC>
-__device__ __forceinline__ void load_param(const float* p, int e, int cols, bool vec, float fill,
-                                           F2* out) {
-  if (p != nullptr && vec && e >= 0 && e + VEC <= cols) {
-#pragma unroll
-    for (int j = 0; j < VEC / 4; ++j) {
-      const float4 v = __ldg(reinterpret_cast<const float4*>(p + e) + j);
-      out[2 * j] = f2(v.x, v.y), out[2 * j + 1] = f2(v.z, v.w);
-    }
-  } else {
-    float v[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const bool in = e + j >= 0 && e + j < cols;
-      v[j] = !in ? 0.0f : (p != nullptr ? __ldg(p + e + j) : fill);
-    }
-#pragma unroll
-    for (int j = 0; j < VEC / 2; ++j) out[j] = f2(v[2 * j], v[2 * j + 1]);
-  }
-}
-
 __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
@@ -171,85 +152,119 @@ struct LnSplit {
   int W, P, CS, G;
 };
 
-// Where a thread stands: its vectors are v0, v0 + step, ... of the row's
-// nvec, which starts `off` elements after a 16-byte boundary.
+// Where a thread stands. Its vectors are v0, v0 + 32, ... of the row's nvec,
+// which starts `off` elements after a 16-byte boundary. Its group takes `n`
+// rows: row0, row0 + stride, ...; where rows may start off the boundary
+// (EDGE), a CTA keeps to rows that are equal modulo VEC, which all start at
+// one `off`.
 struct Place {
-  int W, CS, P, g, G, w, lane, rank, v0, step, off, nvec, cols;
+  int W, CS, P, g, w, lane, rank, warp, v0, off, nvec, cols, n;
   int64_t row0, stride;
 };
-template <int VEC, int NV>
-__device__ __forceinline__ Place place(const LnSplit& s, int cols, int64_t ld, int misaligned) {
+template <int VEC, int NV, bool EDGE>
+__device__ __forceinline__ Place place(const LnSplit& s, int64_t rows, int cols, int64_t ld,
+                                       int misaligned) {
   Place p;
-  p.W = s.W, p.CS = s.CS, p.P = s.P, p.G = s.G, p.cols = cols;
-  const int warp = threadIdx.x >> 5;
-  p.g = warp / s.W, p.w = warp % s.W, p.lane = threadIdx.x & 31;
+  p.W = s.W, p.CS = s.CS, p.P = s.P, p.cols = cols;
+  p.warp = threadIdx.x >> 5;
+  p.g = p.warp / s.W, p.w = p.warp % s.W, p.lane = threadIdx.x & 31;
   p.rank = s.CS > 1 ? int(blockIdx.x & 1) : 0;
-  p.step = 32 * s.W;
-  p.v0 = p.rank * NV * p.step + p.w * 32 + p.lane;
-  p.row0 = int64_t(blockIdx.x / s.CS) * s.G + p.g;
-  p.stride = int64_t(gridDim.x / s.CS) * s.G;
-  p.off = int((misaligned + p.row0 * ld) & (VEC - 1));
+  p.v0 = (p.rank * s.W + p.w) * NV * 32 + p.lane;
+  const int64_t b = blockIdx.x / s.CS, nb = gridDim.x / s.CS;
+  if constexpr (EDGE) {
+    p.row0 = b % VEC + ((b / VEC) * s.G + p.g) * VEC;
+    p.stride = nb * s.G;  // nb is a multiple of VEC
+  } else {
+    p.row0 = b * s.G + p.g;
+    p.stride = nb * s.G;
+  }
+  p.n = p.row0 < rows ? int((rows - p.row0 + p.stride - 1) / p.stride) : 0;
+  p.off = EDGE ? int((misaligned + (b % VEC) * ld) & (VEC - 1)) : 0;
   p.nvec = (cols + p.off + VEC - 1) / VEC;
   return p;
 }
-// Elements of the row that warp w of CTA `rank` holds.
+// Elements of the row that warp `part` (of W CS) holds.
 template <int VEC, int NV>
-__device__ __forceinline__ float warp_count(const Place& p, int rank, int w) {
-  int n = 0;
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = (rank * NV * p.step + i * p.step + w * 32) * VEC - p.off;
-    n += min(max(e + 32 * VEC, 0), p.cols) - min(max(e, 0), p.cols);
-  }
-  return float(n);
+__device__ __forceinline__ float part_count(const Place& p, int part) {
+  const int e = part * NV * 32 * VEC - p.off;
+  return float(min(max(e + NV * 32 * VEC, 0), p.cols) - min(max(e, 0), p.cols));
 }
 
-// A thread's way down the rows of one tensor: `at` is its first vector in the
-// next row to load (or store).
+// Starts the copy of the vector at `src` into dst. EDGE: the vectors at the
+// tensor's two ends may reach past it and are cut.
+template <bool BF16, bool EDGE>
+__device__ __forceinline__ void fetch_vec(uint4* dst, const uint8_t* src, const uint8_t* first,
+                                          const uint8_t* end) {
+  if (EDGE && src < first) {
+    // ahead of the first element: single elements, by plain loads
+    uint32_t w[4] = {0, 0, 0, 0};
+    for (int b = int(first - src); b < 16; b += BF16 ? 2 : 4) {
+      if (src + b >= end) break;
+      if constexpr (BF16)
+        w[b / 4] |= uint32_t(__ldg(reinterpret_cast<const uint16_t*>(src + b))) << (8 * (b & 2));
+      else
+        w[b / 4] = __ldg(reinterpret_cast<const uint32_t*>(src + b));
+    }
+    *dst = make_uint4(w[0], w[1], w[2], w[3]);
+  } else if (EDGE && end - src < 16) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_addr(dst)),
+                 "l"(src), "r"(int(end - src))
+                 : "memory");
+  } else {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"(smem_addr(dst)), "l"(src)
+                 : "memory");
+  }
+}
+
+// A thread's way down the rows of one input: `at` is its first vector in the
+// next row to load, [first, end) the tensor.
 struct Walk {
-  const uint8_t* at;
+  const uint8_t *at, *first, *end;
   int64_t step;  // bytes from a row of the group to its next
 };
 template <bool BF16>
-__device__ __forceinline__ Walk walk(const void* base, int64_t ld, const Place& p) {
+__device__ __forceinline__ Walk walk(const void* base, int64_t rows, int64_t ld, const Place& p) {
   constexpr int kSize = BF16 ? 2 : 4, VEC = 16 / kSize;
   Walk w;
-  w.at = static_cast<const uint8_t*>(base) + (p.row0 * ld + p.v0 * VEC - p.off) * kSize;
+  w.first = static_cast<const uint8_t*>(base);
+  w.end = w.first + ((rows - 1) * ld + p.cols) * kSize;
+  w.at = w.first + (p.row0 * ld + int64_t(p.v0) * VEC - p.off) * kSize;
   w.step = p.stride * ld * kSize;
   return w;
 }
 
-// Starts the copy of vector v (at `src`) into dst; `in`: the vector exists.
-// EDGE: the vectors at the tensor's two ends (first, last byte after it) may
-// reach past it and are cut.
-template <bool BF16, bool EDGE>
-__device__ __forceinline__ void fetch_vec(uint4* dst, const uint8_t* src, bool in,
-                                          const void* base, const uint8_t* end) {
-  if constexpr (!EDGE) {
-    cp_async16(dst, in ? src : static_cast<const uint8_t*>(base), in);
-  } else {
-    const uint8_t* first = static_cast<const uint8_t*>(base);
-    if (in && src < first) {
-      // ahead of the first element: single elements, by plain loads
-      uint32_t w[4] = {0, 0, 0, 0};
-      for (int b = int(first - src); b < 16; b += BF16 ? 2 : 4) {
-        if (src + b >= end) break;
-        if constexpr (BF16)
-          w[b / 4] |= uint32_t(__ldg(reinterpret_cast<const uint16_t*>(src + b))) << (8 * (b & 2));
-        else
-          w[b / 4] = __ldg(reinterpret_cast<const uint32_t*>(src + b));
-      }
-      *dst = make_uint4(w[0], w[1], w[2], w[3]);
-      return;
+// A parameter (fp32 [cols], nullptr: `fill`) of this CTA's vectors in shared
+// memory: [VEC / 4][slots] float4, slot s = vector rank W NV 32 + s (so that
+// a warp's 16-byte reads touch every bank once); asynchronous copies. Outside the row:
+// zero, or `fill` (nothing there is stored).
+template <int VEC, int NV, bool EDGE>
+__device__ __forceinline__ void stage_param(const float* param, float fill, const Place& p,
+                                            float* to) {
+  const int slots = p.W * NV * 32, base = p.rank * slots * VEC - p.off;
+  if (param == nullptr) {
+    for (int i = threadIdx.x; i < slots * VEC; i += blockDim.x) to[i] = fill;
+  } else if (EDGE || (reinterpret_cast<uintptr_t>(param) & 15u) != 0) {
+    for (int i = threadIdx.x; i < slots * VEC; i += blockDim.x) {
+      const int c = base + i, s = i / VEC, j = i % VEC;
+      const bool in = c >= 0 && c < p.cols;
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(
+                       smem_addr(to + (j / 4 * slots + s) * 4 + j % 4)),
+                   "l"(param + (in ? c : 0)), "r"(in ? 4 : 0)
+                   : "memory");
     }
-    const int64_t left = end - src;
-    const int bytes = !in ? 0 : (left < 16 ? int(left) : 16);
-    // (nothing is read where bytes is 0; the address is still in range)
-    const uint8_t* from =
-        in ? src : reinterpret_cast<const uint8_t*>(reinterpret_cast<uintptr_t>(first) & ~uintptr_t(15));
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;\n" ::"r"(smem_addr(dst)),
-                 "l"(from), "r"(bytes)
-                 : "memory");
+  } else {
+    for (int i = threadIdx.x; i < slots * (VEC / 4); i += blockDim.x) {
+      const int c = base + 4 * i, s = i / (VEC / 4), j = i % (VEC / 4);
+      cp_async16(to + (j * slots + s) * 4, param + (c < p.cols ? c : 0), c < p.cols);
+    }
+  }
+}
+template <int VEC>
+__device__ __forceinline__ void read_param(const float* from, int slots, int s, F2* out) {
+#pragma unroll
+  for (int j = 0; j < VEC / 4; ++j) {
+    const float4 v = reinterpret_cast<const float4*>(from)[j * slots + s];
+    out[2 * j] = f2(v.x, v.y), out[2 * j + 1] = f2(v.z, v.w);
   }
 }
 
@@ -275,85 +290,94 @@ __device__ __forceinline__ void store_part(void* to, int e, int cols, uint4 r) {
   }
 }
 
-// Forward. EDGE: rows may start off a 16-byte boundary. QUANT also (or only)
-// writes the 1x32 codes and scales of the rounded y: a group is 32 / VEC
-// adjacent lanes (cols is a multiple of 32 and rows are aligned, so a group
-// never splits over warps).
-template <bool BF16, int NV, bool EDGE, bool QUANT>
-__global__ void __launch_bounds__(512)
+// Forward. EDGE: rows may start off a 16-byte boundary. MULTI: several warps
+// share a row. QUANT also (or only) writes the 1x32 codes and scales of the
+// rounded y: a group is 32 / VEC adjacent lanes (cols is a multiple of 32 and
+// rows are aligned, so a group never splits over warps).
+template <bool BF16, int NV, bool EDGE, bool MULTI, bool QUANT>
+__global__ void __launch_bounds__(ln_threads(BF16, NV), ln_blocks(BF16, NV))
     k_ln_fwd(const void* __restrict__ x, int64_t rows, int cols, int64_t ldx, int misaligned,
-             const float* __restrict__ weight, const float* __restrict__ bias, bool vec_params,
-             float eps, void* __restrict__ y, float* __restrict__ mean_out,
-             float* __restrict__ rstd_out, uint8_t* __restrict__ codes,
-             uint8_t* __restrict__ scales, LnSplit split) {
-  constexpr int VEC = BF16 ? 8 : 4, NP = VEC / 2;
+             const float* __restrict__ weight, const float* __restrict__ bias, float eps,
+             void* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out,
+             uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, LnSplit split) {
+  constexpr int VEC = BF16 ? 8 : 4, NP = VEC / 2, D = ln_depth(NV);
   using V = Vec<BF16, VEC>;
-  extern __shared__ __align__(16) uint4 ring[];  // [kLnDepth][NV][threads]
+  extern __shared__ __align__(16) uint4 ring[];  // [warps][D][NV][32], then w, b
   __shared__ float2 red[2][kLnMaxParts];
-  const Place p = place<VEC, NV>(split, cols, ldx, misaligned);
-  const float inv_n = __fdiv_rn(1.0f, float(cols));
-  const int parts = p.W * p.CS, l = p.lane & (p.P - 1);
+  const Place p = place<VEC, NV, EDGE>(split, rows, cols, ldx, misaligned);
+  const int slots = p.W * NV * 32, s0 = p.w * NV * 32 + p.lane;
+  float* const sw = reinterpret_cast<float*>(ring + (blockDim.x >> 5) * (D * NV * 32));
+  float* const sb = sw + slots * VEC;
+  uint4* const mine = ring + p.warp * (D * NV * 32) + p.lane;
 
-  // elements of this warp, and of warp l of the row
-  const float my_n = warp_count<VEC, NV>(p, p.rank, p.w);
-  const float my_inv = my_n > 0.0f ? __fdiv_rn(1.0f, my_n) : 0.0f;
-  const float l_n = l < parts ? warp_count<VEC, NV>(p, l / p.W, l % p.W) : 0.0f;
-  const float l_inv = l_n > 0.0f ? __fdiv_rn(1.0f, l_n) : 0.0f;
-
-  uint4* const mine = ring + threadIdx.x;
-  const uint8_t* const x_end =
-      static_cast<const uint8_t*>(x) + ((rows - 1) * ldx + cols) * int64_t(16 / VEC);
-  Walk wx = walk<BF16>(x, ldx, p);
-  int64_t frow = p.row0;
+  Walk wx = walk<BF16>(x, rows, ldx, p);
+  int to_fetch = p.n;
   auto fetch = [&](int d) {
+    if (to_fetch > 0) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      fetch_vec<BF16, EDGE>(mine + (d * NV + i) * blockDim.x, wx.at + i * p.step * 16,
-                            frow < rows && p.v0 + i * p.step < p.nvec, x, x_end);
+      for (int i = 0; i < NV; ++i)
+        if (p.v0 + 32 * i < p.nvec)
+          fetch_vec<BF16, EDGE>(mine + (d * NV + i) * 32, wx.at + 512 * i, wx.first, wx.end);
+    }
     cp_async_commit();
     wx.at += wx.step;
-    frow += p.stride;
+    --to_fetch;
   };
+  // vectors past the row's end are zeros that nothing overwrites
 #pragma unroll
-  for (int d = 0; d < kLnDepth; ++d) fetch(d);
-  Walk wy = walk<BF16>(y, cols, p);
+  for (int i = 0; i < NV; ++i)
+    if (p.v0 + 32 * i >= p.nvec) {
+#pragma unroll
+      for (int d = 0; d < D; ++d) mine[(d * NV + i) * 32] = make_uint4(0, 0, 0, 0);
+    }
+  stage_param<VEC, NV, EDGE>(weight, 1.0f, p, sw);
+  stage_param<VEC, NV, EDGE>(bias, 0.0f, p, sb);
+  cp_async_commit();
+#pragma unroll
+  for (int d = 0; d < D; ++d) fetch(d);
+  uint8_t* to = static_cast<uint8_t*>(y) +
+                (p.row0 * cols + int64_t(p.v0) * VEC - p.off) * (BF16 ? 2 : 4);
+  const int64_t to_step = p.stride * cols * (BF16 ? 2 : 4);
 
-  F2 wk[NV * NP], bk[NV * NP];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = (p.v0 + i * p.step) * VEC - p.off;
-    load_param<VEC>(weight, e, cols, vec_params, 1.0f, wk + i * NP);
-    load_param<VEC>(bias, e, cols, vec_params, 0.0f, bk + i * NP);
-  }
+  // elements of this warp, and of warp l of the row
+  const float inv_n = __fdiv_rn(1.0f, float(cols));
+  const int parts = p.W * p.CS, l = p.lane & (p.P - 1);
+  const float my_n = part_count<VEC, NV>(p, p.rank * p.W + p.w);
+  const float my_inv = my_n > 0.0f ? __fdiv_rn(1.0f, my_n) : 0.0f;
+  const float l_n = MULTI && l < parts ? part_count<VEC, NV>(p, l) : 0.0f;
+  const float l_inv = l_n > 0.0f ? __fdiv_rn(1.0f, l_n) : 0.0f;
+  cp_async_wait<D>();  // the parameters
+  __syncthreads();
 
   // the cluster's CTAs walk the same rows; so do the warps of a group
   int d = 0, par = 0;
-  for (int64_t row = p.row0; row < rows; row += p.stride, par ^= 1) {
-    cp_async_wait<kLnDepth - 1>();
+  int64_t row = p.row0;
+  for (int left = p.n; left > 0; --left, row += p.stride, par ^= 1) {
+    cp_async_wait<D - 1>();
     F2 a[NV * NP];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       V in;
-      in.r = mine[(d * NV + i) * blockDim.x];
+      in.r = mine[(d * NV + i) * 32];
       in.unpack(a + i * NP);
       if constexpr (EDGE) {
-        const int v = p.v0 + i * p.step;
+        const int v = p.v0 + 32 * i;
         if (v == 0 || v == p.nvec - 1) mask_vec<VEC>(a + i * NP, v * VEC - p.off, cols);
       }
     }
     fetch(d);
-    if (++d == kLnDepth) d = 0;
+    if (++d == D) d = 0;
 
-    F2 s2 = f2(0.0f, 0.0f);
+    F2 s2 = a[0];
 #pragma unroll
-    for (int i = 0; i < NV * NP; ++i) s2 = add2(s2, a[i]);
+    for (int i = 1; i < NV * NP; ++i) s2 = add2(s2, a[i]);
     const float s = warp_sum(__fadd_rn(f2_lo(s2), f2_hi(s2)));
     float mean = __fmul_rn(s, my_inv);
     F2 q2 = f2(0.0f, 0.0f);
     const F2 mm = f2(-mean, -mean);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = p.v0 + i * p.step;
+      const int v = p.v0 + 32 * i;
       if (v >= p.nvec) continue;
       F2 dv[NP];
 #pragma unroll
@@ -365,7 +389,7 @@ __global__ void __launch_bounds__(512)
       for (int j = 0; j < NP; ++j) q2 = fma2(dv[j], dv[j], q2);
     }
     float m2 = warp_sum(__fadd_rn(f2_lo(q2), f2_hi(q2)));
-    if (parts > 1) {
+    if constexpr (MULTI) {
       // one barrier a row: the buffer of this parity is written again two
       // rows on, past the next row's barrier
       float2* rd = red[par];
@@ -373,7 +397,7 @@ __global__ void __launch_bounds__(512)
         if (p.lane < 2) store_pair(&rd[p.rank * p.W + p.w], make_float2(s, m2), p.lane);
         pair_sync();
       } else {
-        if (p.lane == 0) rd[p.g * p.W + p.w] = make_float2(s, m2);
+        if (p.lane == 0) rd[p.warp] = make_float2(s, m2);
         group_sync(p.g, p.W);
       }
       const float2 o = l < parts ? rd[p.g * p.W + l] : make_float2(0.0f, 0.0f);
@@ -386,24 +410,27 @@ __global__ void __launch_bounds__(512)
       if (mean_out != nullptr) mean_out[row] = mean;
       if (rstd_out != nullptr) rstd_out[row] = rstd;
     }
-    const F2 nm = f2(-mean, -mean), rs = f2(rstd, rstd);
+    // h = x rstd - mean rstd: the product's rounding is of the size that the
+    // mean's own rounding brings
+    const float shift = -__fmul_rn(mean, rstd);
+    const F2 nm = f2(shift, shift), rs = f2(rstd, rstd);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = p.v0 + i * p.step;
+      const int v = p.v0 + 32 * i;
       const bool in = v < p.nvec;
       if (!QUANT && !in) continue;
-      F2 o[NP];
+      F2 o[NP], wv[NP], bv[NP];
+      read_param<VEC>(sw, slots, s0 + 32 * i, wv);
+      read_param<VEC>(sb, slots, s0 + 32 * i, bv);
 #pragma unroll
-      for (int j = 0; j < NP; ++j)
-        o[j] = fma2(mul2(add2(a[i * NP + j], nm), rs), wk[i * NP + j], bk[i * NP + j]);
+      for (int j = 0; j < NP; ++j) o[j] = fma2(fma2(a[i * NP + j], rs, nm), wv[j], bv[j]);
       V out;
       out.pack(o);
       if (in && y != nullptr) {
-        uint8_t* to = const_cast<uint8_t*>(wy.at) + i * p.step * 16;
         if (EDGE && (v == 0 || v == p.nvec - 1))
-          store_part<BF16, VEC>(to, v * VEC - p.off, cols, out.r);
+          store_part<BF16, VEC>(to + 512 * i, v * VEC - p.off, cols, out.r);
         else
-          __stcs(reinterpret_cast<uint4*>(to), out.r);
+          __stcs(reinterpret_cast<uint4*>(to + 512 * i), out.r);
       }
       if constexpr (QUANT) {
         const int64_t at = row * cols + int64_t(v) * VEC;
@@ -411,8 +438,8 @@ __global__ void __launch_bounds__(512)
           uint32_t am = bf16x8_absmax(out.r);
           am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
           am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-          const uint32_t sb = scale_byte(am);
-          const float mul = inv_scale(sb);
+          const uint32_t sbyte = scale_byte(am);
+          const float mul = inv_scale(sbyte);
           float qv[8];
           F2 r8[4];
           out.unpack(r8);
@@ -421,10 +448,10 @@ __global__ void __launch_bounds__(512)
             qv[2 * j] = __fmul_rn(f2_lo(r8[j]), mul);
             qv[2 * j + 1] = __fmul_rn(f2_hi(r8[j]), mul);
           }
-          const uint32_t word = sb == 0xFFu ? 0u : e2m1x8_rn(qv);
+          const uint32_t word = sbyte == 0xFFu ? 0u : e2m1x8_rn(qv);
           if (in) {
             *reinterpret_cast<uint32_t*>(codes + at / 2) = word;
-            if ((p.lane & 3) == 0) scales[at / 32] = static_cast<uint8_t>(sb);
+            if ((p.lane & 3) == 0) scales[at / 32] = static_cast<uint8_t>(sbyte);
           }
         } else {
           uint32_t am = max(max(out.r.x & 0x7FFFFFFFu, out.r.y & 0x7FFFFFFFu),
@@ -432,21 +459,21 @@ __global__ void __launch_bounds__(512)
           am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
           am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
           am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 4));
-          const uint32_t sb = scale_byte(am);
-          const float mul = inv_scale(sb);
+          const uint32_t sbyte = scale_byte(am);
+          const float mul = inv_scale(sbyte);
           const float qv[8] = {__fmul_rn(__uint_as_float(out.r.x), mul),
                                __fmul_rn(__uint_as_float(out.r.y), mul),
                                __fmul_rn(__uint_as_float(out.r.z), mul),
                                __fmul_rn(__uint_as_float(out.r.w), mul), 0, 0, 0, 0};
-          const uint32_t word = sb == 0xFFu ? 0u : e2m1x8_rn(qv);
+          const uint32_t word = sbyte == 0xFFu ? 0u : e2m1x8_rn(qv);
           if (in) {
             *reinterpret_cast<uint16_t*>(codes + at / 2) = static_cast<uint16_t>(word);
-            if ((p.lane & 7) == 0) scales[at / 32] = static_cast<uint8_t>(sb);
+            if ((p.lane & 7) == 0) scales[at / 32] = static_cast<uint8_t>(sbyte);
           }
         }
       }
     }
-    wy.at += wy.step;
+    to += to_step;
   }
   cp_async_wait<0>();
   if (p.CS > 1) pair_sync();  // no CTA ends while the other may still write to it
@@ -531,76 +558,82 @@ __global__ void __launch_bounds__(kLnGenThreads)
 }
 
 // Backward; PARAMS = false leaves dw and db out.
-template <bool BF16, int NV, bool EDGE, bool PARAMS>
+template <bool BF16, int NV, bool EDGE, bool MULTI, bool PARAMS>
 __global__ void __launch_bounds__(512)
     k_ln_bwd(const void* __restrict__ dy, const void* __restrict__ x, int64_t rows, int cols,
              int64_t lddy, int64_t ldx, int misaligned, const float* __restrict__ weight,
-             bool vec_params, const float* __restrict__ mean_in,
-             const float* __restrict__ rstd_in, void* __restrict__ dx,
-             float* __restrict__ partial, LnSplit split) {
-  constexpr int VEC = BF16 ? 8 : 4, NP = VEC / 2;
+             const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
+             void* __restrict__ dx, float* __restrict__ partial, LnSplit split) {
+  constexpr int VEC = BF16 ? 8 : 4, NP = VEC / 2, D = ln_depth(NV);
   using V = Vec<BF16, VEC>;
-  extern __shared__ __align__(16) uint4 ring[];  // [kLnDepth][2 NV][threads]
+  extern __shared__ __align__(16) uint4 ring[];  // [warps][D][2 NV][32], then w
   __shared__ float2 red[2][kLnMaxParts];
-  const Place p = place<VEC, NV>(split, cols, ldx, misaligned);
-  const float inv_n = __fdiv_rn(1.0f, float(cols));
-  const int parts = p.W * p.CS, l = p.lane & (p.P - 1);
-  const F2 zero = f2(0.0f, 0.0f);
+  const Place p = place<VEC, NV, EDGE>(split, rows, cols, ldx, misaligned);
+  const int slots = p.W * NV * 32, s0 = p.w * NV * 32 + p.lane;
+  float* const sw = reinterpret_cast<float*>(ring + (blockDim.x >> 5) * (D * 2 * NV * 32));
+  uint4* const mine = ring + p.warp * (D * 2 * NV * 32) + p.lane;
 
-  uint4* const mine = ring + threadIdx.x;
-  const uint8_t* const x_end =
-      static_cast<const uint8_t*>(x) + ((rows - 1) * ldx + cols) * int64_t(16 / VEC);
-  const uint8_t* const dy_end =
-      static_cast<const uint8_t*>(dy) + ((rows - 1) * lddy + cols) * int64_t(16 / VEC);
-  Walk wx = walk<BF16>(x, ldx, p), wg = walk<BF16>(dy, lddy, p);
-  int64_t frow = p.row0;
+  Walk wx = walk<BF16>(x, rows, ldx, p), wg = walk<BF16>(dy, rows, lddy, p);
+  int to_fetch = p.n;
   auto fetch = [&](int d) {
+    if (to_fetch > 0) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const bool in = frow < rows && p.v0 + i * p.step < p.nvec;
-      fetch_vec<BF16, EDGE>(mine + (d * 2 * NV + 2 * i) * blockDim.x, wx.at + i * p.step * 16, in,
-                            x, x_end);
-      fetch_vec<BF16, EDGE>(mine + (d * 2 * NV + 2 * i + 1) * blockDim.x,
-                            wg.at + i * p.step * 16, in, dy, dy_end);
+      for (int i = 0; i < NV; ++i)
+        if (p.v0 + 32 * i < p.nvec) {
+          fetch_vec<BF16, EDGE>(mine + (d * NV + i) * 64, wx.at + 512 * i, wx.first, wx.end);
+          fetch_vec<BF16, EDGE>(mine + (d * NV + i) * 64 + 32, wg.at + 512 * i, wg.first, wg.end);
+        }
     }
     cp_async_commit();
     wx.at += wx.step, wg.at += wg.step;
-    frow += p.stride;
+    --to_fetch;
   };
+  // vectors past the row's end are zeros that nothing overwrites
 #pragma unroll
-  for (int d = 0; d < kLnDepth; ++d) fetch(d);
-  Walk wo = walk<BF16>(dx, cols, p);
-
-  F2 wk[NV * NP];
-  F2 aw[PARAMS ? NV * NP : 1], ab[PARAMS ? NV * NP : 1];
+  for (int i = 0; i < NV; ++i)
+    if (p.v0 + 32 * i >= p.nvec) {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    load_param<VEC>(weight, (p.v0 + i * p.step) * VEC - p.off, cols, vec_params, 1.0f,
-                    wk + i * NP);
-    if constexpr (PARAMS) {
-#pragma unroll
-      for (int j = 0; j < NP; ++j) aw[i * NP + j] = ab[i * NP + j] = zero;
+      for (int d = 0; d < D; ++d)
+        mine[(d * NV + i) * 64] = mine[(d * NV + i) * 64 + 32] = make_uint4(0, 0, 0, 0);
     }
-  }
+  stage_param<VEC, NV, EDGE>(weight, 1.0f, p, sw);
+  cp_async_commit();
+#pragma unroll
+  for (int d = 0; d < D; ++d) fetch(d);
+  uint8_t* to = static_cast<uint8_t*>(dx) +
+                (p.row0 * cols + int64_t(p.v0) * VEC - p.off) * (BF16 ? 2 : 4);
+  const int64_t to_step = p.stride * cols * (BF16 ? 2 : 4);
 
+  const float inv_n = __fdiv_rn(1.0f, float(cols));
+  const int parts = p.W * p.CS, l = p.lane & (p.P - 1);
+  const F2 zero = f2(0.0f, 0.0f);
+  F2 aw[PARAMS ? NV * NP : 1], ab[PARAMS ? NV * NP : 1];
+  if constexpr (PARAMS) {
+#pragma unroll
+    for (int k = 0; k < NV * NP; ++k) aw[k] = ab[k] = zero;
+  }
   float nmean = 0.0f, nrstd = 0.0f;
-  if (p.row0 < rows) nmean = __ldg(mean_in + p.row0), nrstd = __ldg(rstd_in + p.row0);
+  const float *mp = mean_in + p.row0, *rp = rstd_in + p.row0;
+  if (p.n > 0) nmean = __ldg(mp), nrstd = __ldg(rp);
+  cp_async_wait<D>();  // the weight
+  __syncthreads();
+
   int d = 0, par = 0;
-  for (int64_t row = p.row0; row < rows; row += p.stride, par ^= 1) {
+  for (int left = p.n; left > 0; --left, par ^= 1) {
     const float mean = nmean, rstd = nrstd;
-    if (row + p.stride < rows)
-      nmean = __ldg(mean_in + row + p.stride), nrstd = __ldg(rstd_in + row + p.stride);
-    cp_async_wait<kLnDepth - 1>();
+    mp += p.stride, rp += p.stride;
+    if (left > 1) nmean = __ldg(mp), nrstd = __ldg(rp);
+    cp_async_wait<D - 1>();
     F2 h[NV * NP], g[NV * NP];
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       V in;
-      in.r = mine[(d * 2 * NV + 2 * i) * blockDim.x];
+      in.r = mine[(d * NV + i) * 64];
       in.unpack(h + i * NP);
-      in.r = mine[(d * 2 * NV + 2 * i + 1) * blockDim.x];
+      in.r = mine[(d * NV + i) * 64 + 32];
       in.unpack(g + i * NP);
       if constexpr (EDGE) {
-        const int v = p.v0 + i * p.step;
+        const int v = p.v0 + 32 * i;
         if (v == 0 || v == p.nvec - 1) {
           mask_vec<VEC>(h + i * NP, v * VEC - p.off, cols);
           mask_vec<VEC>(g + i * NP, v * VEC - p.off, cols);
@@ -608,31 +641,37 @@ __global__ void __launch_bounds__(512)
       }
     }
     fetch(d);
-    if (++d == kLnDepth) d = 0;
+    if (++d == D) d = 0;
 
-    // a masked element has g = 0 and w = 0: it adds nothing anywhere
+    // (an element outside the row has g = 0: it adds nothing anywhere)
     const F2 nm = f2(-mean, -mean), rs = f2(rstd, rstd);
     F2 c1 = zero, c2 = zero;
 #pragma unroll
-    for (int k = 0; k < NV * NP; ++k) {
-      h[k] = mul2(add2(h[k], nm), rs);
-      if constexpr (PARAMS) {
-        aw[k] = fma2(g[k], h[k], aw[k]);
-        ab[k] = add2(ab[k], g[k]);
+    for (int i = 0; i < NV; ++i) {
+      F2 wv[NP];
+      read_param<VEC>(sw, slots, s0 + 32 * i, wv);
+#pragma unroll
+      for (int j = 0; j < NP; ++j) {
+        const int k = i * NP + j;
+        h[k] = mul2(add2(h[k], nm), rs);
+        if constexpr (PARAMS) {
+          aw[k] = fma2(g[k], h[k], aw[k]);
+          ab[k] = add2(ab[k], g[k]);
+        }
+        g[k] = mul2(g[k], wv[j]);
+        c1 = add2(c1, g[k]);
+        c2 = fma2(g[k], h[k], c2);
       }
-      g[k] = mul2(g[k], wk[k]);
-      c1 = add2(c1, g[k]);
-      c2 = fma2(g[k], h[k], c2);
     }
     float s1 = warp_sum(__fadd_rn(f2_lo(c1), f2_hi(c1)));
     float s2 = warp_sum(__fadd_rn(f2_lo(c2), f2_hi(c2)));
-    if (parts > 1) {
+    if constexpr (MULTI) {
       float2* rd = red[par];
       if (p.CS > 1) {
         if (p.lane < 2) store_pair(&rd[p.rank * p.W + p.w], make_float2(s1, s2), p.lane);
         pair_sync();
       } else {
-        if (p.lane == 0) rd[p.g * p.W + p.w] = make_float2(s1, s2);
+        if (p.lane == 0) rd[p.warp] = make_float2(s1, s2);
         group_sync(p.g, p.W);
       }
       const float2 o = l < parts ? rd[p.g * p.W + l] : make_float2(0.0f, 0.0f);
@@ -643,7 +682,7 @@ __global__ void __launch_bounds__(512)
     const F2 k1 = f2(m1, m1), k2 = f2(m2, m2);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int v = p.v0 + i * p.step;
+      const int v = p.v0 + 32 * i;
       if (v >= p.nvec) continue;
       F2 o[NP];
 #pragma unroll
@@ -653,48 +692,43 @@ __global__ void __launch_bounds__(512)
       }
       V out;
       out.pack(o);
-      uint8_t* to = const_cast<uint8_t*>(wo.at) + i * p.step * 16;
       if (EDGE && (v == 0 || v == p.nvec - 1))
-        store_part<BF16, VEC>(to, v * VEC - p.off, cols, out.r);
+        store_part<BF16, VEC>(to + 512 * i, v * VEC - p.off, cols, out.r);
       else
-        __stcs(reinterpret_cast<uint4*>(to), out.r);
+        __stcs(reinterpret_cast<uint4*>(to + 512 * i), out.r);
     }
-    wo.at += wo.step;
+    to += to_step;
   }
   cp_async_wait<0>();
 
   if constexpr (PARAMS) {
-    // the groups of a CTA add into shared memory one after the other (the
-    // last writes the partial row); groups have their own `off`
+    // the groups of a CTA (same columns, same `off`) add into shared memory
+    // one after the other; the last one writes the partial row
     float* pw = partial + int64_t(blockIdx.x / p.CS) * 2 * cols;
-    float* sacc = reinterpret_cast<float*>(ring);
-    if (p.G > 1) {
-      __syncthreads();  // every group is done with the ring
-      for (int c = threadIdx.x; c < 2 * cols; c += blockDim.x) sacc[c] = 0.0f;
-      __syncthreads();
-    }
-    for (int g = 0; g < p.G; ++g) {
+    float* sacc = reinterpret_cast<float*>(ring);  // [2][slots VEC]
+    const int G = (blockDim.x >> 5) / p.W;
+    if (G > 1) __syncthreads();  // every group is done with the ring
+    for (int g = 0; g < G; ++g) {
       if (p.g == g) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int e = (p.v0 + i * p.step) * VEC - p.off;
+          const int c0 = (p.v0 + 32 * i) * VEC - p.off;
 #pragma unroll
           for (int j = 0; j < VEC; ++j) {
-            const int c = e + j;
-            if (c < 0 || c >= cols) continue;
-            const float a = (j & 1) ? f2_hi(aw[i * NP + j / 2]) : f2_lo(aw[i * NP + j / 2]);
-            const float b = (j & 1) ? f2_hi(ab[i * NP + j / 2]) : f2_lo(ab[i * NP + j / 2]);
-            if (p.G == 1)
-              pw[c] = a, pw[cols + c] = b;
-            else
-              sacc[c] = __fadd_rn(sacc[c], a), sacc[cols + c] = __fadd_rn(sacc[cols + c], b);
+            const int k = i * NP + j / 2, at = j * slots + s0 + 32 * i;
+            float a = (j & 1) ? f2_hi(aw[k]) : f2_lo(aw[k]);
+            float b = (j & 1) ? f2_hi(ab[k]) : f2_lo(ab[k]);
+            if (g > 0) a = __fadd_rn(a, sacc[at]), b = __fadd_rn(b, sacc[slots * VEC + at]);
+            if (g + 1 < G) {
+              sacc[at] = a, sacc[slots * VEC + at] = b;
+            } else if (c0 + j >= 0 && c0 + j < cols) {
+              pw[c0 + j] = a, pw[cols + c0 + j] = b;
+            }
           }
         }
       }
-      if (p.G > 1) __syncthreads();
+      if (G > 1) __syncthreads();
     }
-    if (p.G > 1)
-      for (int c = threadIdx.x; c < 2 * cols; c += blockDim.x) pw[c] = sacc[c];
   }
   if (p.CS > 1) pair_sync();
 }
@@ -784,7 +818,7 @@ __global__ void __launch_bounds__(kLnRedThreads)
 // ---------------------------------------------------------------------------
 
 struct LnShape {
-  int nv, threads, clusters;  // clusters: most that `stride` allows, 0: any
+  int nv, threads;
   LnSplit split;
 };
 
@@ -795,31 +829,35 @@ int sm_count() {
   return sms;
 }
 
-// Vectors per thread and warps per row: `big` vectors, or one where a row is
-// narrow (one warp) or rows are few (less than two an SM: one vector a
-// thread spreads a row over the most threads). Rows that 16 warps cannot
-// hold take a cluster of two CTAs. Narrow rows share a CTA of about
-// `block_warps` warps.
-bool ln_shape(int64_t nvec, int big, int64_t rows, int block_warps, LnShape* s) {
+// Vectors per thread (one of nvs, ascending) and warps per row. Where one
+// warp can hold a row it does, with the fewest vectors (no barrier, and the
+// work per row that does not grow with its length is done once); longer rows
+// take the largest count while that needs at most four warps, else the one
+// before it, and a cluster of two CTAs where 16 warps are not enough. Few
+// rows (less than two an SM) spread over the most warps. Rows that need less
+// than a CTA of `block_warps` warps share one.
+bool ln_shape(int64_t nvec, const int (&nvs)[3], int64_t rows, int block_warps, LnShape* s) {
   const bool few = rows < 2 * int64_t(sm_count());
-  for (int nv = 1; nv <= big; nv += big - 1) {
-    const int64_t W = (nvec + 32 * nv - 1) / (32 * nv);
-    if (nv == 1 && !(W == 1 || (few && W <= kLnMaxWarps)) && big > 1) continue;
-    s->nv = nv;
-    s->split.CS = 1;
-    s->split.W = int(W);
-    if (W > kLnMaxWarps) {
-      if (W > 2 * kLnMaxWarps) return false;
-      s->split.CS = 2;
-      s->split.W = int((W + 1) / 2);
-    }
-    s->split.P = 1;
-    while (s->split.P < s->split.W * s->split.CS) s->split.P *= 2;
-    s->split.G = few || s->split.CS > 1 || W >= block_warps ? 1 : int(block_warps / W);
-    s->threads = 32 * s->split.W * s->split.G;
-    return true;
+  auto warps = [&](int i) { return (nvec + 32 * nvs[i] - 1) / (32 * nvs[i]); };
+  int i = warps(2) <= 4 ? 2 : 1;
+  if (few && warps(0) <= kLnMaxWarps) i = 0;
+  if (!few || warps(0) == 1)
+    for (int j = 2; j >= 0; --j)
+      if (warps(j) == 1) i = j;
+  int64_t W = warps(i);
+  s->nv = nvs[i];
+  s->split.CS = 1;
+  if (W > kLnMaxWarps) {
+    s->split.CS = 2;
+    W = (W + 1) / 2;
+    if (W > kLnMaxWarps) return false;
   }
-  return false;
+  s->split.W = int(W);
+  s->split.P = 1;
+  while (s->split.P < s->split.W * s->split.CS) s->split.P *= 2;
+  s->split.G = few || s->split.CS > 1 || W >= block_warps ? 1 : int(block_warps / W);
+  s->threads = 32 * s->split.W * s->split.G;
+  return true;
 }
 
 // Whether rows of these tensors (base, stride) can move as 16-byte vectors:
@@ -840,19 +878,16 @@ bool vector_rows(const void* const* p, const int64_t* ld, int n, int64_t cols, i
   return whole || dense;
 }
 
-// Persistent grid of whole clusters; with rows off the boundary the row
-// stride (clusters x groups) is a multiple of the vector length.
+// Persistent grid of whole clusters; with rows off the boundary a multiple of
+// the vector length of them (see Place).
 int ln_grid(const void* kern, const LnShape& sh, size_t smem, int64_t rows, bool edge, int vec,
             int64_t most) {
-  int64_t want = (rows + sh.split.G - 1) / sh.split.G;
+  const int64_t unit = edge ? vec : 1;
+  int64_t want = ((rows + unit - 1) / unit + sh.split.G - 1) / sh.split.G * unit;
   if (want > most) want = most;
-  int64_t n = persistent_grid(kern, sh.threads, smem, want * sh.split.CS) / sh.split.CS;
-  if (n < 1) n = 1;
-  if (edge && n * sh.split.G < rows) {
-    const int64_t unit = sh.split.G >= vec ? 1 : vec / sh.split.G;
-    n = n / unit * unit > 0 ? n / unit * unit : unit;
-  }
-  return int(n * sh.split.CS);
+  const int64_t n =
+      persistent_grid(kern, sh.threads, smem, want * sh.split.CS) / sh.split.CS / unit * unit;
+  return int((n < unit ? unit : n) * sh.split.CS);
 }
 
 template <typename... P, typename... A>
@@ -872,8 +907,6 @@ cudaError_t ln_launch(void (*kern)(P...), int grid, const LnShape& sh, size_t sm
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
 struct FwdArgs {
   const void* x;
   int64_t rows, cols, ldx;
@@ -885,29 +918,31 @@ struct FwdArgs {
   cudaStream_t s;
 };
 
-template <bool BF16, int NV, bool EDGE, bool QUANT>
+template <bool BF16, int NV, bool EDGE, bool MULTI, bool QUANT>
 cudaError_t fwd_launch(const FwdArgs& a, const LnShape& sh, int misaligned) {
-  auto kern = k_ln_fwd<BF16, NV, EDGE, QUANT>;
+  constexpr int VEC = BF16 ? 8 : 4;
+  auto kern = k_ln_fwd<BF16, NV, EDGE, MULTI, QUANT>;
   const void* k = reinterpret_cast<const void*>(kern);
-  const size_t smem = size_t(sh.threads) * NV * 16 * kLnDepth;
+  const size_t smem = size_t(sh.threads) * NV * 16 * ln_depth(NV) +
+                      size_t(sh.split.W) * NV * 32 * VEC * 8;
   const cudaError_t e = allow_smem(k, smem);
   if (e != cudaSuccess) return e;
-  const int grid = ln_grid(k, sh, smem, a.rows, EDGE, BF16 ? 8 : 4, int64_t(1) << 30);
+  const int grid = ln_grid(k, sh, smem, a.rows, EDGE, VEC, int64_t(1) << 30);
   return ln_launch(kern, grid, sh, smem, a.s, a.x, a.rows, int(a.cols), a.ldx, misaligned,
-                   a.weight, a.bias, !EDGE && aligned16(a.weight) && aligned16(a.bias), a.eps,
-                   a.y, a.mean, a.rstd, a.codes, a.scales, sh.split);
+                   a.weight, a.bias, a.eps, a.y, a.mean, a.rstd, a.codes, a.scales, sh.split);
 }
 
-template <bool BF16, int NV>
+template <bool BF16, int NV, bool MULTI>
 cudaError_t fwd_nv(const FwdArgs& a, const LnShape& sh, bool edge, int misaligned) {
-  if (a.codes != nullptr) return fwd_launch<BF16, NV, false, true>(a, sh, 0);
-  return edge ? fwd_launch<BF16, NV, true, false>(a, sh, misaligned)
-              : fwd_launch<BF16, NV, false, false>(a, sh, 0);
+  if (a.codes != nullptr) return fwd_launch<BF16, NV, false, MULTI, true>(a, sh, 0);
+  return edge ? fwd_launch<BF16, NV, true, MULTI, false>(a, sh, misaligned)
+              : fwd_launch<BF16, NV, false, MULTI, false>(a, sh, 0);
 }
 
 template <bool BF16>
 cudaError_t fwd_any(const FwdArgs& a) {
-  constexpr int kSize = BF16 ? 2 : 4, VEC = 16 / kSize, BIG = BF16 ? 3 : 4;
+  constexpr int kSize = BF16 ? 2 : 4, VEC = 16 / kSize;
+  constexpr int kNv[3] = {1, BF16 ? 3 : 4, BF16 ? 6 : 8};
   LnShape sh;
   bool edge;
   int mis;
@@ -915,8 +950,17 @@ cudaError_t fwd_any(const FwdArgs& a) {
   const int64_t lds[] = {a.ldx, a.cols};
   if (a.cols <= kLnMaxCols && vector_rows(ptrs, lds, 2, a.cols, kSize, &edge, &mis) &&
       !(edge && a.codes != nullptr) &&
-      ln_shape((a.cols + VEC - 1) / VEC + (edge ? 1 : 0), BIG, a.rows, 4, &sh))
-    return sh.nv == 1 ? fwd_nv<BF16, 1>(a, sh, edge, mis) : fwd_nv<BF16, BIG>(a, sh, edge, mis);
+      ln_shape((a.cols + VEC - 1) / VEC + (edge ? 1 : 0), kNv, a.rows, 8, &sh)) {
+    const bool multi = sh.split.W * sh.split.CS > 1;
+    if (sh.nv == kNv[0])
+      return multi ? fwd_nv<BF16, kNv[0], true>(a, sh, edge, mis)
+                   : fwd_nv<BF16, kNv[0], false>(a, sh, edge, mis);
+    if (sh.nv == kNv[1])
+      return multi ? fwd_nv<BF16, kNv[1], true>(a, sh, edge, mis)
+                   : fwd_nv<BF16, kNv[1], false>(a, sh, edge, mis);
+    return multi ? fwd_nv<BF16, kNv[2], true>(a, sh, edge, mis)
+                 : fwd_nv<BF16, kNv[2], false>(a, sh, edge, mis);
+  }
   auto kern = k_ln_fwd_wide<BF16>;
   const int grid =
       persistent_grid(reinterpret_cast<const void*>(kern), kLnGenThreads, 0, a.rows);
@@ -948,42 +992,51 @@ cudaError_t params_launch(const BwdArgs& a, int n) {
                             a.dw, a.db);
 }
 
-template <bool BF16, int NV, bool EDGE, bool PARAMS>
+template <bool BF16, int NV, bool EDGE, bool MULTI, bool PARAMS>
 cudaError_t bwd_launch(const BwdArgs& a, const LnShape& sh, int misaligned) {
-  auto kern = k_ln_bwd<BF16, NV, EDGE, PARAMS>;
+  constexpr int VEC = BF16 ? 8 : 4;
+  auto kern = k_ln_bwd<BF16, NV, EDGE, MULTI, PARAMS>;
   const void* k = reinterpret_cast<const void*>(kern);
-  size_t smem = size_t(sh.threads) * 2 * NV * 16 * kLnDepth;
-  if (PARAMS && sh.split.G > 1 && smem < size_t(a.cols) * 8) smem = size_t(a.cols) * 8;
+  const size_t params = size_t(sh.split.W) * NV * 32 * VEC * 4;
+  size_t smem = size_t(sh.threads) * 2 * NV * 16 * ln_depth(NV) + params;
+  if (smem < 2 * params) smem = 2 * params;  // the groups' sums, at the end
   cudaError_t e = allow_smem(k, smem);
   if (e != cudaSuccess) return e;
-  const int grid = ln_grid(k, sh, smem, a.rows, EDGE, BF16 ? 8 : 4, kLnMaxPartials);
+  const int grid = ln_grid(k, sh, smem, a.rows, EDGE, VEC, kLnMaxPartials);
   e = ln_launch(kern, grid, sh, smem, a.s, a.dy, a.x, a.rows, int(a.cols), a.lddy, a.ldx,
-                misaligned, a.weight, !EDGE && aligned16(a.weight), a.mean, a.rstd, a.dx,
-                a.partial, sh.split);
+                misaligned, a.weight, a.mean, a.rstd, a.dx, a.partial, sh.split);
   if (e != cudaSuccess || !PARAMS) return e;
   return params_launch(a, grid / sh.split.CS);
 }
 
-template <bool BF16, int NV>
+template <bool BF16, int NV, bool MULTI>
 cudaError_t bwd_nv(const BwdArgs& a, const LnShape& sh, bool edge, int misaligned) {
   if (a.dw != nullptr)
-    return edge ? bwd_launch<BF16, NV, true, true>(a, sh, misaligned)
-                : bwd_launch<BF16, NV, false, true>(a, sh, 0);
-  return edge ? bwd_launch<BF16, NV, true, false>(a, sh, misaligned)
-              : bwd_launch<BF16, NV, false, false>(a, sh, 0);
+    return edge ? bwd_launch<BF16, NV, true, MULTI, true>(a, sh, misaligned)
+                : bwd_launch<BF16, NV, false, MULTI, true>(a, sh, 0);
+  return edge ? bwd_launch<BF16, NV, true, MULTI, false>(a, sh, misaligned)
+              : bwd_launch<BF16, NV, false, MULTI, false>(a, sh, 0);
 }
 
 template <bool BF16>
 cudaError_t bwd_any(const BwdArgs& a) {
-  constexpr int kSize = BF16 ? 2 : 4, VEC = 16 / kSize, BIG = BF16 ? 2 : 4;
+  constexpr int kSize = BF16 ? 2 : 4, VEC = 16 / kSize;
+  // at most 16 elements a thread: two sums for each stay in registers
+  constexpr int kBig = BF16 ? 2 : 4, kNv[3] = {1, kBig, kBig};
   LnShape sh;
   bool edge;
   int mis;
   const void* const ptrs[] = {a.x, a.dy, a.dx};
   const int64_t lds[] = {a.ldx, a.lddy, a.cols};
   if (a.cols <= kLnMaxCols && vector_rows(ptrs, lds, 3, a.cols, kSize, &edge, &mis) &&
-      ln_shape((a.cols + VEC - 1) / VEC + (edge ? 1 : 0), BIG, a.rows, 8, &sh))
-    return sh.nv == 1 ? bwd_nv<BF16, 1>(a, sh, edge, mis) : bwd_nv<BF16, BIG>(a, sh, edge, mis);
+      ln_shape((a.cols + VEC - 1) / VEC + (edge ? 1 : 0), kNv, a.rows, 8, &sh)) {
+    const bool multi = sh.split.W * sh.split.CS > 1;
+    if (sh.nv == 1)
+      return multi ? bwd_nv<BF16, 1, true>(a, sh, edge, mis)
+                   : bwd_nv<BF16, 1, false>(a, sh, edge, mis);
+    return multi ? bwd_nv<BF16, kBig, true>(a, sh, edge, mis)
+                 : bwd_nv<BF16, kBig, false>(a, sh, edge, mis);
+  }
   auto kern = k_ln_bwd_wide<BF16>;
   const int grid =
       persistent_grid(reinterpret_cast<const void*>(kern), kLnGenThreads, 0, a.rows);
