@@ -30,8 +30,8 @@
 //              scale tiles into a ring of stages;
 //   warp 1:    tensor memory; one thread issues per stage the two scale
 //              copies and four MMAs (M = 128, N = 2 T, K = 32);
-//   warps 2-5: split X into the stages (warp w takes stages w, w + 4, ...),
-//              then read the accumulator and store Y.
+//   warps 2-9: split X into the stages (one warp a stage), then read the
+//              accumulators and store Y.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -44,24 +44,40 @@ namespace mxfp4 {
 namespace {
 
 constexpr int kVM = 128;                 // weight rows of a CTA
-constexpr int kVWorkers = 4;
+constexpr int kVWorkers = 8;
 constexpr int kVThreads = 32 * (2 + kVWorkers);
 constexpr uint32_t kVNaN = 0x7FC00000u;
 
 template <int T>
 struct VLayout {
   static constexpr int kN = 2 * T;
-  static constexpr int kStages = T <= 16 ? 5 : (T == 32 ? 4 : 3);
+  // as many as let two CTAs share an SM (64 tokens: one CTA)
+  static constexpr int kStages = T == 8 ? 5 : (T == 16 ? 4 : (T == 32 ? 3 : 5));
+  // Warps that split X: no more than there are stages. A warp that is done
+  // with block i knows that block i - kStages has been consumed; it goes on
+  // to block i + kSplit, whose stage's barrier it can only read right once
+  // block i + kSplit - 2 kStages has been consumed (phases alternate).
+  static constexpr int kSplit = kVWorkers < kStages ? kVWorkers : kStages;
+  // Accumulators: consecutive MMAs on one wait for each other's result, which
+  // with few columns takes longer than the MMA itself, so the four K = 32
+  // steps of a stage go to accumulators of their own where they fit.
+  static constexpr int kAcc = T <= 16 ? 4 : (T == 32 ? 2 : 1);
   static constexpr uint32_t kA = kVM * 128, kB = kN * 128, kSf = 512;
   // per ring: codes, x planes, scales of both
   static constexpr uint32_t kAOff = 0;
   static constexpr uint32_t kBOff = kAOff + kStages * kA;
   static constexpr uint32_t kSfaOff = kBOff + kStages * kB;
   static constexpr uint32_t kSfbOff = kSfaOff + kStages * kSf;
-  static constexpr uint32_t kBarOff = kSfbOff + kStages * kSf;
+  // sums of this CTA's share of the tile, from every rank of its cluster
+  static constexpr uint32_t kPartOff = kSfbOff + kStages * kSf;
+  static constexpr uint32_t kBarOff = kPartOff + T * kVM * 4;
   static constexpr uint32_t kBytes = kBarOff + 256;
-  static constexpr uint32_t kTmemCols = kN + 8 <= 32 ? 32 : (kN + 8 <= 64 ? 64 : (kN + 8 <= 128 ? 128 : 256));
-  static constexpr uint32_t kSfaCol = kN, kSfbCol = kN + 4;
+  // tensor memory: accumulators, then per stage 4 columns of either scales
+  // (their own, so that copying a stage's scales waits for no MMA)
+  static constexpr uint32_t kSfCol = kAcc * kN;
+  static constexpr uint32_t kTmemUsed = kSfCol + 8 * kStages;
+  static constexpr uint32_t kTmemCols = kTmemUsed <= 128 ? 128 : 256;
+  static_assert(kTmemUsed <= 256, "two CTAs share an SM's 512 columns");
   // kind::mxf8f6f4: A E2M1 (5), B E4M3 (0), both K-major, N / 8, E8M0
   // scales, M / 16
   static constexpr uint32_t kIdesc =
@@ -119,16 +135,16 @@ __device__ __forceinline__ uint32_t v_cluster_rank() {
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ void v_cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
-               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+__device__ __forceinline__ void v_cluster_arrive() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
-__device__ __forceinline__ float v_peer_load(uint32_t a, uint32_t rank) {
+__device__ __forceinline__ void v_cluster_wait() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void v_peer_store(uint32_t a, uint32_t rank, float v) {
   uint32_t d;
-  float v;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(rank));
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(d) : "memory");
-  return v;
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(d), "f"(v) : "memory");
 }
 
 // E4M3 code pairs (nearest, saturating at 448) of two fp32 values, and back.
@@ -235,6 +251,17 @@ __global__ void __launch_bounds__(kVThreads)
   const int kb0 = int(int64_t(kblocks) * rank / split);
   const int kb1 = int(int64_t(kblocks) * (rank + 1) / split);
 
+  if (split > 1) v_cluster_arrive();  // waited for before the first store to a peer
+  const uint8_t* const sf = sfw + tile * kblocks * 512;
+  uint32_t issued = 0, last_ph = 0;  // loading thread: stages, last phases
+  auto load = [&](int kb, uint32_t s, uint32_t ph) {
+    issued |= 1u << s;
+    last_ph = (last_ph & ~(1u << s)) | (ph << s);
+    // the tile load counts the packed codes: half of the bytes it fills
+    expect_tx(&full[s], L::kA / 2 + L::kSf);
+    tma_load_2d(sm + L::kAOff + s * L::kA, &tm_w, kb * 128, int(n0), &full[s]);
+    v_bulk_load(sm + L::kSfaOff + s * L::kSf, sf + int64_t(kb) * 512, L::kSf, &full[s]);
+  };
   if (tid == 0) {
     for (int s = 0; s < L::kStages; ++s) {
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 2;" ::"r"(smem_u32(&full[s])));
@@ -242,7 +269,10 @@ __global__ void __launch_bounds__(kVThreads)
     }
     asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(acc_full)));
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     *failed = 0;
+    // the first stages are free: their loads need not wait for the others
+    for (int kb = kb0; kb < kb1 && kb < kb0 + L::kStages; ++kb) load(kb, uint32_t(kb - kb0), 0);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -250,7 +280,32 @@ __global__ void __launch_bounds__(kVThreads)
                  "r"(L::kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+
+  // Workers: X arrives in batches of 8 tokens x 128 k (a lane holds 8
+  // elements of a token, 16 lanes a token, two tokens a round), two batches
+  // ahead of the one being split; warp w takes every kSplit-th stage.
+  const int w = warp - 2, half = lane >> 4, l16 = lane & 15;
+  const int n_batch = (tokens + 7) / 8;  // of a stage
+  int f_kb = kb0 + w, f_b = 0;           // the next batch to fetch
+  struct Batch {
+    uint4 r[4];
+  };
+  auto fetch = [&](Batch& q) {
+    const uint16_t* xp = x + int64_t(f_kb) * 128 + l16 * 8;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int t = 8 * f_b + 2 * j + half;
+      if (f_kb < kb1 && t < tokens) q.r[j] = ld_l1(xp + int64_t(t0 + t) * ldx);
+    }
+    if (++f_b == n_batch) f_b = 0, f_kb += L::kSplit;
+  };
+  Batch b0, b1, b2;
+  if (w >= L::kSplit) f_kb = kb1;        // a warp without stages
   if (warp >= 2) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b0.r[j] = b1.r[j] = b2.r[j] = make_uint4(0, 0, 0, 0);
+    fetch(b0);
+    fetch(b1);
     // rows of absent tokens stay zero, and so do their scales
     uint4* b = reinterpret_cast<uint4*>(sm + L::kBOff);
     for (int i = tid - 64; i < int(L::kStages * L::kB / 16); i += 32 * kVWorkers)
@@ -267,19 +322,13 @@ __global__ void __launch_bounds__(kVThreads)
 
   if (warp == 0) {
     if (lane == 0) {
-      uint32_t s = 0, ph = 0, issued = 0, last_ph = 0;
-      const uint8_t* sf = sfw + tile * kblocks * 512;
-      for (int kb = kb0; kb < kb1; ++kb) {
+      uint32_t s = 0, ph = 1;
+      for (int kb = kb0 + L::kStages; kb < kb1; ++kb) {
         if (!v_wait(&empty[s], ph ^ 1u, failed)) {
           atomicExch(failed, 1);
           break;
         }
-        issued |= 1u << s;
-        last_ph = (last_ph & ~(1u << s)) | (ph << s);
-        // the load counts the packed codes: half of the bytes it fills
-        expect_tx(&full[s], L::kA / 2 + L::kSf);
-        tma_load_2d(sm + L::kAOff + s * L::kA, &tm_w, kb * 128, int(n0), &full[s]);
-        v_bulk_load(sm + L::kSfaOff + s * L::kSf, sf + int64_t(kb) * 512, L::kSf, &full[s]);
+        load(kb, s, ph);
         if (++s == L::kStages) s = 0, ph ^= 1u;
       }
       // every load has landed before the CTA can end (the workers' arrival
@@ -298,15 +347,16 @@ __global__ void __launch_bounds__(kVThreads)
           break;
         }
         asm volatile("tcgen05.fence::after_thread_sync;");
-        v_copy_scales(tmem + L::kSfaCol, sm + L::kSfaOff + s * L::kSf);
-        v_copy_scales(tmem + L::kSfbCol, sm + L::kSfbOff + s * L::kSf);
+        const uint32_t sfa = tmem + L::kSfCol + 8 * s, sfb = sfa + 4;
+        v_copy_scales(sfa, sm + L::kSfaOff + s * L::kSf);
+        v_copy_scales(sfb, sm + L::kSfbOff + s * L::kSf);
         const uint64_t ad = smem_desc_sw128(sm + L::kAOff + s * L::kA);
         const uint64_t bd = smem_desc_sw128(sm + L::kBOff + s * L::kB);
 #pragma unroll
         for (uint32_t g = 0; g < 4; ++g)
-          mma_mxf8f6f4(tmem, ad + 2 * g, bd + 2 * g, L::kIdesc | (g << 29) | (g << 4),
-                       (kb > kb0 || g > 0) ? 1u : 0u, (tmem + L::kSfaCol) | (g << 30),
-                       (tmem + L::kSfbCol) | (g << 30));
+          mma_mxf8f6f4(tmem + (g % L::kAcc) * L::kN, ad + 2 * g, bd + 2 * g,
+                       L::kIdesc | (g << 29) | (g << 4), (kb > kb0 || g >= L::kAcc) ? 1u : 0u,
+                       sfa | (g << 30), sfb | (g << 30));
         commit_to(&empty[s]);
         if (++s == L::kStages) s = 0, ph ^= 1u;
       }
@@ -317,48 +367,38 @@ __global__ void __launch_bounds__(kVThreads)
     }
     __syncwarp();
   } else {
-    // split X: warp w takes every fourth stage; a lane holds 8 elements of a
-    // token's 128 (16 lanes a token), two tokens a round
-    const int w = warp - 2;
-    const int half = lane >> 4, l16 = lane & 15;
-    constexpr int kRounds = T / 2;
-    constexpr int kBatch = kRounds < 4 ? kRounds : 4;  // loads in flight
-    uint4 raw[kBatch];
     bool ok = true;
-    for (int kb = kb0 + w; kb < kb1 && ok; kb += kVWorkers) {
+    for (int kb = w < L::kSplit ? kb0 + w : kb1; kb < kb1 && ok; kb += L::kSplit) {
       const int it = kb - kb0;
       const uint32_t s = uint32_t(it % L::kStages), ph = uint32_t(it / L::kStages) & 1u;
-      const uint16_t* xp = x + int64_t(kb) * 128 + l16 * 8;
-      for (int r0 = 0; r0 < kRounds && 2 * r0 < tokens; r0 += kBatch) {
-#pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int t = 2 * (r0 + j) + half;
-          raw[j] = t < tokens ? ld_l1(xp + int64_t(t0 + t) * ldx) : make_uint4(0, 0, 0, 0);
-        }
-        if (r0 == 0) {
+      uint8_t* const bt = sm + L::kBOff + s * L::kB;
+      uint8_t* const ft = sm + L::kSfbOff + s * L::kSf + (l16 >> 2);
+      for (int b = 0; b < n_batch; ++b) {
+        fetch(b2);
+        if (b == 0) {
           ok = __all_sync(0xFFFFFFFFu, v_wait(&empty[s], ph ^ 1u, failed));
           if (!ok) break;
         }
 #pragma unroll
-        for (int j = 0; j < kBatch; ++j) {
-          const int t = 2 * (r0 + j) + half;
-          if (2 * (r0 + j) >= tokens) break;
-          const Planes p = split8(raw[j]);
+        for (int j = 0; j < 4; ++j) {
+          const int t = 8 * b + 2 * j + half;
+          if (8 * b + 2 * j >= tokens) break;
+          const Planes p = split8(b0.r[j]);
           if (t < tokens) {
-            uint8_t* b = sm + L::kBOff + s * L::kB;
             // row r of the 128-byte swizzled K-major operand: 16-byte chunk
             // c at c ^ (r % 8); this lane's 8 codes are half a chunk
             const uint32_t c = uint32_t(l16 >> 1), o = uint32_t(l16 & 1) * 8;
             const uint32_t rl = uint32_t(T + t);
-            *reinterpret_cast<uint2*>(b + t * 128 + ((c ^ (t & 7)) << 4) + o) = p.hi;
-            *reinterpret_cast<uint2*>(b + rl * 128 + ((c ^ (rl & 7)) << 4) + o) = p.lo;
+            *reinterpret_cast<uint2*>(bt + t * 128 + ((c ^ (t & 7)) << 4) + o) = p.hi;
+            *reinterpret_cast<uint2*>(bt + rl * 128 + ((c ^ (rl & 7)) << 4) + o) = p.lo;
             if ((lane & 3) == 0) {
-              uint8_t* f = sm + L::kSfbOff + s * L::kSf + (l16 >> 2);
-              f[16 * (t & 31) + 4 * (t >> 5)] = uint8_t(p.s_hi);
-              f[16 * (rl & 31) + 4 * (rl >> 5)] = uint8_t(p.s_lo);
+              ft[16 * (t & 31) + 4 * (t >> 5)] = uint8_t(p.s_hi);
+              ft[16 * (rl & 31) + 4 * (rl >> 5)] = uint8_t(p.s_lo);
             }
           }
         }
+        b0 = b1;
+        b1 = b2;
       }
       if (!ok) {
         atomicExch(failed, 1);
@@ -373,52 +413,61 @@ __global__ void __launch_bounds__(kVThreads)
   }
   __syncthreads();
 
-  // epilogue: worker warp with lane quarter q holds rows 32 q + lane
-  float* part = reinterpret_cast<float*>(sm);  // [T][128], over the ring
+  // Epilogue: worker warps read the accumulator (lane quarter q = rows 32 q
+  // + lane; two warps a quarter, half of the tokens each). In a cluster the
+  // rows are shared out for the joining, 128 / split to a rank: every rank
+  // stores its sums for them at their owner, which adds them in rank order.
+  const int share = kVM / split;  // split is a power of two
+  if (split > 1) v_cluster_wait();  // every CTA of the cluster has started
   if (warp >= 2) {
     asm volatile("tcgen05.fence::after_thread_sync;");
     const bool bad = failed_flag(failed) || !v_wait(acc_full, 0, nullptr, kAccWaitLimit);
     if (bad) atomicExch(failed, 1);
-    const int q = warp & 3, row = 32 * q + lane;
+    const int q = warp & 3, row = 32 * q + lane, h = w >> 2;
     const uint32_t tb = tmem + (uint32_t(32 * q) << 16);
+    const int owner = row / share;
+    const uint32_t part = smem_u32(sm + L::kPartOff);
 #pragma unroll
-    for (int c = 0; c < T; c += 8) {
-      uint32_t a[8], b[8];
-      asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                   : "=r"(a[0]), "=r"(a[1]), "=r"(a[2]), "=r"(a[3]), "=r"(a[4]), "=r"(a[5]),
-                     "=r"(a[6]), "=r"(a[7])
-                   : "r"(tb + c));
-      asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                   : "=r"(b[0]), "=r"(b[1]), "=r"(b[2]), "=r"(b[3]), "=r"(b[4]), "=r"(b[5]),
-                     "=r"(b[6]), "=r"(b[7])
-                   : "r"(tb + T + c));
+    for (int c = h * (T / 2); c < (h + 1) * (T / 2); c += 4) {
+      uint32_t a[L::kAcc][2][4];
+#pragma unroll
+      for (int k = 0; k < L::kAcc; ++k)
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(a[k][i][0]), "=r"(a[k][i][1]), "=r"(a[k][i][2]), "=r"(a[k][i][3])
+                       : "r"(tb + k * L::kN + i * T + c));
       asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < 4; ++j) {
         const int t = c + j;
-        const float v = bad ? __uint_as_float(kVNaN)
-                            : __fadd_rn(__uint_as_float(a[j]), __uint_as_float(b[j]));
-        if (split > 1)
-          part[t * kVM + row] = v;
-        else if (t < tokens && n0 + row < n)
-          store_y<BF16>(y, int64_t(t0 + t) * n + n0 + row, v);
+        float v = 0.0f;
+#pragma unroll
+        for (int k = 0; k < L::kAcc; ++k)
+          v = __fadd_rn(v, __fadd_rn(__uint_as_float(a[k][0][j]), __uint_as_float(a[k][1][j])));
+        if (bad) v = __uint_as_float(kVNaN);
+        if (t < tokens) {
+          if (split > 1)  // [rank][token][row of the share]
+            v_peer_store(part + 4 * ((rank * T + t) * share + row - owner * share),
+                         uint32_t(owner), v);
+          else if (n0 + row < n)
+            store_y<BF16>(y, int64_t(t0 + t) * n + n0 + row, v);
+        }
       }
     }
     asm volatile("tcgen05.fence::before_thread_sync;");
   }
   if (split > 1) {
-    // each rank adds its share of the (token, row) sums over all ranks, in
-    // rank order, and keeps its own sums alive until every rank has read them
-    v_cluster_sync();
-    const uint32_t pa = smem_u32(part);
-    const int items = tokens * kVM;
-    for (int i = rank * kVThreads + tid; i < items; i += split * kVThreads) {
-      float v = v_peer_load(pa + 4 * i, 0);
-      for (int r = 1; r < split; ++r) v = __fadd_rn(v, v_peer_load(pa + 4 * i, uint32_t(r)));
-      const int t = i / kVM, row = i % kVM;
-      if (n0 + row < n) store_y<BF16>(y, int64_t(t0 + t) * n + n0 + row, v);
+    v_cluster_arrive();
+    v_cluster_wait();
+    const float* part = reinterpret_cast<const float*>(sm + L::kPartOff);
+    for (int i = tid; i < tokens * share; i += kVThreads) {
+      const int t = i / share, r = i % share;
+      float v = part[t * share + r];
+      for (int k = 1; k < split; ++k) v = __fadd_rn(v, part[(k * T + t) * share + r]);
+      const int64_t row = n0 + rank * share + r;
+      if (row < n) store_y<BF16>(y, int64_t(t0 + t) * n + row, v);
     }
-    v_cluster_sync();
   } else {
     __syncthreads();
   }
