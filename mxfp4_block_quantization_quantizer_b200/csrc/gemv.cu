@@ -95,8 +95,8 @@ __device__ __forceinline__ void mma_mxf8f6f4(uint32_t tmem_c, uint64_t adesc, ui
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(tsfa), "r"(tsfb));
 }
 
-__device__ __forceinline__ void v_copy_scales(uint32_t taddr, const void* tile) {
-  const uint64_t d = smem_desc(tile, 16, 128);
+// A 512-byte scale tile from shared memory (descriptor d) to 4 columns.
+__device__ __forceinline__ void v_copy_desc(uint32_t taddr, uint64_t d) {
   asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(d));
 }
 
@@ -339,26 +339,35 @@ __global__ void __launch_bounds__(kVThreads)
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
-      uint32_t s = 0, ph = 0;
+      // Issuing is what bounds this thread (about 70 ns a stage beside the
+      // MMAs where addresses are formed in the loop): the loop is unrolled
+      // over the ring, so that every operand is a base plus a constant.
+      const uint64_t a0 = smem_desc_sw128(sm + L::kAOff), b0d = smem_desc_sw128(sm + L::kBOff);
+      const uint64_t fa0 = smem_desc(sm + L::kSfaOff, 16, 128);
+      const uint64_t fb0 = smem_desc(sm + L::kSfbOff, 16, 128);
+      const uint32_t sf0 = tmem + L::kSfCol;
       bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!v_wait(&full[s], ph, failed)) {
-          ok = false;
-          break;
-        }
-        asm volatile("tcgen05.fence::after_thread_sync;");
-        const uint32_t sfa = tmem + L::kSfCol + 8 * s, sfb = sfa + 4;
-        v_copy_scales(sfa, sm + L::kSfaOff + s * L::kSf);
-        v_copy_scales(sfb, sm + L::kSfbOff + s * L::kSf);
-        const uint64_t ad = smem_desc_sw128(sm + L::kAOff + s * L::kA);
-        const uint64_t bd = smem_desc_sw128(sm + L::kBOff + s * L::kB);
+      uint32_t ph = 0;
+      for (int kb = kb0; kb < kb1 && ok; kb += L::kStages, ph ^= 1u) {
 #pragma unroll
-        for (uint32_t g = 0; g < 4; ++g)
-          mma_mxf8f6f4(tmem + (g % L::kAcc) * L::kN, ad + 2 * g, bd + 2 * g,
-                       L::kIdesc | (g << 29) | (g << 4), (kb > kb0 || g >= L::kAcc) ? 1u : 0u,
-                       sfa | (g << 30), sfb | (g << 30));
-        commit_to(&empty[s]);
-        if (++s == L::kStages) s = 0, ph ^= 1u;
+        for (int s = 0; s < L::kStages; ++s) {
+          if (kb + s >= kb1) break;
+          if (!v_wait(&full[s], ph, failed)) {
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;");
+          const uint32_t sfa = sf0 + 8 * s, sfb = sfa + 4;
+          v_copy_desc(sfa, fa0 + s * (L::kSf >> 4));
+          v_copy_desc(sfb, fb0 + s * (L::kSf >> 4));
+#pragma unroll
+          for (uint32_t g = 0; g < 4; ++g)
+            mma_mxf8f6f4(tmem + (g % L::kAcc) * L::kN, a0 + (s * (L::kA >> 4) + 2 * g),
+                         b0d + (s * (L::kB >> 4) + 2 * g), L::kIdesc | (g << 29) | (g << 4),
+                         (s > 0 || g >= L::kAcc || kb > kb0) ? 1u : 0u, sfa + (g << 30),
+                         sfb + (g << 30));
+          commit_to(&empty[s]);
+        }
       }
       if (!ok) atomicExch(failed, 1);
       commit_to(acc_full);
