@@ -53,11 +53,6 @@ struct VLayout {
   static constexpr int kN = 2 * T;
   // as many as let two CTAs share an SM (64 tokens: one CTA)
   static constexpr int kStages = T == 8 ? 5 : (T == 16 ? 4 : (T == 32 ? 3 : 5));
-  // Warps that split X: no more than there are stages. A warp that is done
-  // with block i knows that block i - kStages has been consumed; it goes on
-  // to block i + kSplit, whose stage's barrier it can only read right once
-  // block i + kSplit - 2 kStages has been consumed (phases alternate).
-  static constexpr int kSplit = kVWorkers < kStages ? kVWorkers : kStages;
   // Accumulators: consecutive MMAs on one wait for each other's result, which
   // with few columns takes longer than the MMA itself, so the four K = 32
   // steps of a stage go to accumulators of their own where they fit.
@@ -173,51 +168,65 @@ __device__ __forceinline__ uint32_t plane_scale(uint32_t amax_bits) {
   return amax_bits >= 0x7F800000u ? 0xFFu : (E > 7u ? E - 7u : 0u);
 }
 
-// Both planes of 8 values of a group that 4 adjacent lanes share.
+// Both planes of 8 values of a group that 4 adjacent lanes share, for R
+// independent groups at once (the shuffles and conversions of one hide behind
+// those of the others: one at a time took 4 times as long).
 struct Planes {
   uint2 hi, lo;
   uint32_t s_hi, s_lo;
 };
-__device__ __forceinline__ Planes split8(uint4 raw) {
-  Planes p;
-  uint32_t am = bf16x8_absmax(raw);
-  am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
-  am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-  p.s_hi = plane_scale(am);
-  const bool bad = p.s_hi == 0xFFu;
-  const float mul = inv_scale(p.s_hi);
-  const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-  float r[8];
-  uint32_t c[4];
+template <int R>
+__device__ __forceinline__ void split8(const uint4* raw, Planes* p) {
+  uint32_t am[R], rm[R];
+  float r[R][8];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float a = __fmul_rn(bf16_lo(w[j]), mul), b = __fmul_rn(bf16_hi(w[j]), mul);
-    c[j] = e4m3x2(a, b);
-    float d[2];
-    e4m3x2_decode(c[j], d);
-    r[2 * j] = __fsub_rn(a, d[0]);  // exact: in units of 2^s_hi
-    r[2 * j + 1] = __fsub_rn(b, d[1]);
+  for (int k = 0; k < R; ++k) am[k] = bf16x8_absmax(raw[k]);
+#pragma unroll
+  for (int o = 1; o <= 2; o *= 2)
+#pragma unroll
+    for (int k = 0; k < R; ++k) am[k] = max(am[k], __shfl_xor_sync(0xFFFFFFFFu, am[k], o));
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    p[k].s_hi = plane_scale(am[k]);
+    const bool bad = p[k].s_hi == 0xFFu;
+    const float mul = inv_scale(p[k].s_hi);
+    const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+    uint32_t c[4];
+    rm[k] = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float a = __fmul_rn(bf16_lo(w[j]), mul), b = __fmul_rn(bf16_hi(w[j]), mul);
+      c[j] = e4m3x2(a, b);
+      float d[2];
+      e4m3x2_decode(c[j], d);
+      r[k][2 * j] = __fsub_rn(a, d[0]);  // exact: in units of 2^s_hi
+      r[k][2 * j + 1] = __fsub_rn(b, d[1]);
+      rm[k] = max(rm[k], max(__float_as_uint(r[k][2 * j]) & 0x7FFFFFFFu,
+                             __float_as_uint(r[k][2 * j + 1]) & 0x7FFFFFFFu));
+    }
+    p[k].hi = bad ? make_uint2(0, 0) : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+    if (bad) rm[k] = 0;
   }
-  p.hi = bad ? make_uint2(0, 0) : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-  uint32_t rm = 0;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) rm = max(rm, __float_as_uint(r[j]) & 0x7FFFFFFFu);
-  if (bad) rm = 0;
-  rm = max(rm, __shfl_xor_sync(0xFFFFFFFFu, rm, 1));
-  rm = max(rm, __shfl_xor_sync(0xFFFFFFFFu, rm, 2));
-  // the remainders are at most 8 (half a step of 4 significant bits); the
-  // remainders get a scale of their own, relative to s_hi and never below
-  // 2^-127 (remainders below 2^-113 of s_hi, far under fp32's reach, shrink)
-  const uint32_t E = rm >> 23;
-  int rel = rm == 0 ? 0 : max(int(E) - 127 - 7, -120);
-  if (int(p.s_hi) + rel < 0) rel = -int(p.s_hi);
-  p.s_lo = bad ? 0u : uint32_t(int(p.s_hi) + rel);
-  const float mul2 = __uint_as_float(uint32_t(127 - rel) << 23);
+  for (int o = 1; o <= 2; o *= 2)
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    c[j] = e4m3x2(__fmul_rn(r[2 * j], mul2), __fmul_rn(r[2 * j + 1], mul2));
-  p.lo = bad ? make_uint2(0, 0) : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-  return p;
+    for (int k = 0; k < R; ++k) rm[k] = max(rm[k], __shfl_xor_sync(0xFFFFFFFFu, rm[k], o));
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    // the remainders are at most 8 (half a step of 4 significant bits); the
+    // remainders get a scale of their own, relative to s_hi and never below
+    // 2^-127 (remainders below 2^-113 of s_hi, far under fp32's reach, shrink)
+    const bool bad = p[k].s_hi == 0xFFu;
+    int rel = rm[k] == 0 ? 0 : max(int(rm[k] >> 23) - 127 - 7, -120);
+    if (int(p[k].s_hi) + rel < 0) rel = -int(p[k].s_hi);
+    p[k].s_lo = bad ? 0u : uint32_t(int(p[k].s_hi) + rel);
+    const float mul = __uint_as_float(uint32_t(127 - rel) << 23);
+    uint32_t c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      c[j] = e4m3x2(__fmul_rn(r[k][2 * j], mul), __fmul_rn(r[k][2 * j + 1], mul));
+    p[k].lo = bad ? make_uint2(0, 0) : make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  }
 }
 
 template <bool BF16>
@@ -229,7 +238,7 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
 }
 
 template <int T, bool BF16>
-__global__ void __launch_bounds__(kVThreads)
+__global__ void __launch_bounds__(kVThreads, 2)
     k_gemv(const __grid_constant__ CUtensorMap tm_w, const uint8_t* __restrict__ sfw,
            const uint16_t* __restrict__ x, int64_t ldx, int m, int64_t n, int kblocks, int split,
            void* __restrict__ y, int* __restrict__ status) {
@@ -264,7 +273,9 @@ __global__ void __launch_bounds__(kVThreads)
   };
   if (tid == 0) {
     for (int s = 0; s < L::kStages; ++s) {
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 2;" ::"r"(smem_u32(&full[s])));
+      // the loads' announcement and a split batch each
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&full[s])),
+                   "r"(1 + (tokens + 7) / 8));
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&empty[s])));
     }
     asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(acc_full)));
@@ -281,26 +292,35 @@ __global__ void __launch_bounds__(kVThreads)
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
 
-  // Workers: X arrives in batches of 8 tokens x 128 k (a lane holds 8
-  // elements of a token, 16 lanes a token, two tokens a round), two batches
-  // ahead of the one being split; warp w takes every kSplit-th stage.
+  // Workers: X is split in batches of 8 tokens x 128 k (a lane holds 8
+  // elements of a token, 16 lanes a token, two tokens a round), n_batch to a
+  // stage. Warp w takes batches w, w + active, ... of the CTA's sequence and
+  // loads two of its batches ahead. Warps take turns over at most kStages
+  // stages: one that is done with block i knows that block i - kStages has
+  // been consumed, and the barrier of a later block's stage reads right only
+  // if the block two rounds of the ring before it has been consumed (phases
+  // alternate), so it must not be more than kStages blocks ahead of that.
   const int w = warp - 2, half = lane >> 4, l16 = lane & 15;
-  const int n_batch = (tokens + 7) / 8;  // of a stage
-  int f_kb = kb0 + w, f_b = 0;           // the next batch to fetch
+  const int n_batch = (tokens + 7) / 8;
+  const int n_items = (kb1 - kb0) * n_batch;
+  const int active = min(kVWorkers, L::kStages * n_batch);
+  int f_i = w < active ? w : n_items;  // the next batch to fetch
   struct Batch {
     uint4 r[4];
   };
   auto fetch = [&](Batch& q) {
-    const uint16_t* xp = x + int64_t(f_kb) * 128 + l16 * 8;
+    if (f_i < n_items) {
+      const int blk = f_i / n_batch, b = f_i - blk * n_batch;
+      const uint16_t* xp = x + int64_t(kb0 + blk) * 128 + l16 * 8;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int t = 8 * f_b + 2 * j + half;
-      if (f_kb < kb1 && t < tokens) q.r[j] = ld_l1(xp + int64_t(t0 + t) * ldx);
+      for (int j = 0; j < 4; ++j) {
+        const int t = 8 * b + 2 * j + half;
+        if (t < tokens) q.r[j] = ld_l1(xp + int64_t(t0 + t) * ldx);
+      }
     }
-    if (++f_b == n_batch) f_b = 0, f_kb += L::kSplit;
+    f_i += active;
   };
   Batch b0, b1, b2;
-  if (w >= L::kSplit) f_kb = kb1;        // a warp without stages
   if (warp >= 2) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) b0.r[j] = b1.r[j] = b2.r[j] = make_uint4(0, 0, 0, 0);
@@ -376,43 +396,41 @@ __global__ void __launch_bounds__(kVThreads)
     }
     __syncwarp();
   } else {
-    bool ok = true;
-    for (int kb = w < L::kSplit ? kb0 + w : kb1; kb < kb1 && ok; kb += L::kSplit) {
-      const int it = kb - kb0;
-      const uint32_t s = uint32_t(it % L::kStages), ph = uint32_t(it / L::kStages) & 1u;
-      uint8_t* const bt = sm + L::kBOff + s * L::kB;
-      uint8_t* const ft = sm + L::kSfbOff + s * L::kSf + (l16 >> 2);
-      for (int b = 0; b < n_batch; ++b) {
-        fetch(b2);
-        if (b == 0) {
-          ok = __all_sync(0xFFFFFFFFu, v_wait(&empty[s], ph ^ 1u, failed));
-          if (!ok) break;
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int t = 8 * b + 2 * j + half;
-          if (8 * b + 2 * j >= tokens) break;
-          const Planes p = split8(b0.r[j]);
-          if (t < tokens) {
-            // row r of the 128-byte swizzled K-major operand: 16-byte chunk
-            // c at c ^ (r % 8); this lane's 8 codes are half a chunk
-            const uint32_t c = uint32_t(l16 >> 1), o = uint32_t(l16 & 1) * 8;
-            const uint32_t rl = uint32_t(T + t);
-            *reinterpret_cast<uint2*>(bt + t * 128 + ((c ^ (t & 7)) << 4) + o) = p.hi;
-            *reinterpret_cast<uint2*>(bt + rl * 128 + ((c ^ (rl & 7)) << 4) + o) = p.lo;
-            if ((lane & 3) == 0) {
-              ft[16 * (t & 31) + 4 * (t >> 5)] = uint8_t(p.s_hi);
-              ft[16 * (rl & 31) + 4 * (rl >> 5)] = uint8_t(p.s_lo);
-            }
-          }
-        }
-        b0 = b1;
-        b1 = b2;
-      }
-      if (!ok) {
+    for (int i = w < active ? w : n_items; i < n_items; i += active) {
+      const int blk = i / n_batch, b = i - blk * n_batch;
+      const uint32_t s = uint32_t(blk % L::kStages), ph = uint32_t(blk / L::kStages) & 1u;
+      fetch(b2);
+      if (!__all_sync(0xFFFFFFFFu, v_wait(&empty[s], ph ^ 1u, failed))) {
         atomicExch(failed, 1);
         break;
       }
+      uint8_t* const bt = sm + L::kBOff + s * L::kB;
+      uint8_t* const ft = sm + L::kSfbOff + s * L::kSf + (l16 >> 2);
+      auto put = [&](const Planes& p, int t) {
+        if (t >= tokens) return;
+        // row r of the 128-byte swizzled K-major operand: 16-byte chunk c at
+        // c ^ (r % 8); this lane's 8 codes are half a chunk
+        const uint32_t c = uint32_t(l16 >> 1), o = uint32_t(l16 & 1) * 8;
+        const uint32_t rl = uint32_t(T + t);
+        *reinterpret_cast<uint2*>(bt + t * 128 + ((c ^ (t & 7)) << 4) + o) = p.hi;
+        *reinterpret_cast<uint2*>(bt + rl * 128 + ((c ^ (rl & 7)) << 4) + o) = p.lo;
+        if ((lane & 3) == 0) {
+          ft[16 * (t & 31) + 4 * (t >> 5)] = uint8_t(p.s_hi);
+          ft[16 * (rl & 31) + 4 * (rl >> 5)] = uint8_t(p.s_lo);
+        }
+      };
+      if (tokens - 8 * b <= 2) {
+        Planes p[1];
+        split8<1>(b0.r, p);
+        put(p[0], 8 * b + half);
+      } else {
+        Planes p[4];
+        split8<4>(b0.r, p);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) put(p[j], 8 * b + 2 * j + half);
+      }
+      b0 = b1;
+      b1 = b2;
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
       __syncwarp();
       if (lane == 0)
