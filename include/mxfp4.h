@@ -392,6 +392,10 @@ mxfp4_status mxfp4_gemm_quantize_a(const void* x, int64_t m, int64_t n, int64_t 
                                    const uint8_t* b_scales, float* c, uint8_t* a_codes,
                                    uint8_t* a_scales, int* status, void* stream);
 
+/* Bytes of workspace mxfp4_gemv needs (0 where it needs none; a few MB at
+ * most for a few rows); -1 for a shape it refuses. */
+int64_t mxfp4_gemv_workspace(int64_t m, int64_t n, int64_t k);
+
 /*
  * Product of a few unquantized rows with an MXFP4 weight, the step a model
  * answers single tokens with (m = 1 to a few dozen):
@@ -411,6 +415,9 @@ mxfp4_status mxfp4_gemm_quantize_a(const void* x, int64_t m, int64_t n, int64_t 
  *   b_scales device, blocked order (rows = n, groups = k/32), 16-byte aligned
  *   y        device [m][n] of y_dtype, 16-byte aligned, written; must not
  *            overlap x
+ *   workspace  device, 16-byte aligned, workspace_bytes of scratch (at least
+ *            mxfp4_gemv_workspace; NULL where that is 0); calls that run at
+ *            the same time need workspaces of their own
  *   status   device int or NULL (MXFP4_STATUS_WAIT_TIMEOUT above); the tiles
  *            of a CTA whose wait ran out hold NaN
  * k must be a multiple of 32, m at most 2^19. A group of x that holds Inf or
@@ -422,7 +429,7 @@ mxfp4_status mxfp4_gemm_quantize_a(const void* x, int64_t m, int64_t n, int64_t 
  */
 mxfp4_status mxfp4_gemv(const void* x, int64_t m, int64_t n, int64_t k, int64_t ldx,
                         const uint8_t* b_codes, const uint8_t* b_scales, void* y, int y_dtype,
-                        int* status, void* stream);
+                        void* workspace, int64_t workspace_bytes, int* status, void* stream);
 
 /* Largest rows and cols of mxfp4_newton_schulz. */
 #define MXFP4_NS_MAX_DIM ((int64_t)1 << 20)

@@ -26,7 +26,7 @@ SYMBOLS = ("mxfp4_quantize", "mxfp4_quantize_oas", "mxfp4_dequantize",
            "mxfp4_rht_quantize", "mxfp4_rht_quantize_oas", "mxfp4_osc_step",
            "mxfp4_osc_synthetic_update", "mxfp4_qramp_step", "mxfp4_qema_quantize",
            "mxfp4_scales_to_blocked", "mxfp4_gemm", "mxfp4_gemm_quantize_a",
-           "mxfp4_gemv", "mxfp4_newton_schulz", "mxfp4_newton_schulz_workspace",
+           "mxfp4_gemv", "mxfp4_gemv_workspace", "mxfp4_newton_schulz", "mxfp4_newton_schulz_workspace",
            "mxfp4_layernorm", "mxfp4_layernorm_quantize", "mxfp4_layernorm_backward",
            "mxfp4_layernorm_backward_workspace", "mxfp4_status_string")
 
@@ -80,7 +80,7 @@ def lib():
         }
         f32 = ctypes.c_float
         sig.update({
-            "mxfp4_gemv": [vp, i64, i64, i64, i64, vp, vp, vp, i32, vp, vp],
+            "mxfp4_gemv": [vp, i64, i64, i64, i64, vp, vp, vp, i32, vp, i64, vp, vp],
             "mxfp4_newton_schulz": [vp, i32, i64, i64, i32, f32, f32, f32, f32, f32, vp, i32, vp,
                                     i64, vp, vp],
             "mxfp4_layernorm": [vp, i32, i64, i64, i64, vp, vp, f32, vp, vp, vp, vp],
@@ -94,6 +94,8 @@ def lib():
             f.argtypes, f.restype = args, i32
         for f in (L.mxfp4_layernorm_backward_workspace, L.mxfp4_newton_schulz_workspace):
             f.argtypes, f.restype = [i64, i64], i64
+        L.mxfp4_gemv_workspace.argtypes = [i64, i64, i64]
+        L.mxfp4_gemv_workspace.restype = i64
         L.mxfp4_status_string.argtypes = [i32]
         L.mxfp4_status_string.restype = ctypes.c_char_p
         _lib = L
@@ -468,12 +470,14 @@ def _apart(out, name, *inputs):
                 raise ValueError("%s overlaps an input" % name)
 
 
-def gemv(x, b_codes, b_blocked, out_dtype=torch.bfloat16, out=None, stream=None, status=None):
+def gemv(x, b_codes, b_blocked, out_dtype=torch.bfloat16, out=None, workspace=None, stream=None,
+         status=None):
     """mxfp4_gemv: Y = x B^T for a few bf16 rows x [m, k] (contiguous rows,
     any row stride that is a multiple of 8; not quantized) and an MXFP4
     weight B given as K-major codes [n, k/2] and blocked scales. Y is bf16 or
-    fp32 [m, n]. status: optional int32 CUDA tensor of one element, the
-    timeout status word."""
+    fp32 [m, n]. workspace: optional uint8 CUDA tensor of
+    mxfp4_gemv_workspace(m, n, k) bytes; status: optional int32 CUDA tensor
+    of one element, the timeout status word."""
     ldx = _rows2d(x, "x")
     if x.dtype != torch.bfloat16:
         raise TypeError("x must be bfloat16")
@@ -491,8 +495,10 @@ def gemv(x, b_codes, b_blocked, out_dtype=torch.bfloat16, out=None, stream=None,
         _buffer(out, "out", out.dtype, m * n, d)
         _apart(out, "out", x)
     st = None if status is None else _addr(_buffer(status, "status", torch.int32, 1, d))
+    need = lib().mxfp4_gemv_workspace(m, n, k)
+    ws = _workspace(workspace, need, d) if need > 0 else None
     _call("mxfp4_gemv", d, stream, x.data_ptr(), m, n, k, ldx, b_codes.data_ptr(),
-          b_blocked.data_ptr(), out.data_ptr(), _dtype_code(out), st)
+          b_blocked.data_ptr(), out.data_ptr(), _dtype_code(out), _addr(ws), max(need, 0), st)
     return out
 
 

@@ -23,15 +23,20 @@
 // rows of the B operand, their products two accumulator columns that the
 // epilogue adds.
 //
-// One CTA takes 128 weight rows, T tokens (N = 2 T columns) and a slab of k;
-// the CTAs of a cluster take the slabs of the same rows and add their sums
-// through distributed shared memory in the order of their ranks (no atomics).
+// Work: a tile is 128 weight rows x T tokens (N = 2 T columns), a unit 128 k
+// of it. The units of all tiles, k first, are dealt out in equal runs to two
+// CTAs an SM, so a run can end inside a tile: a tile that one run covers is
+// stored at once, the sums of the others go to the caller's workspace and a
+// second small kernel (launched ahead, waiting on the first) adds them in the
+// order of k. No atomics: the same bits every time. (Clusters that joined
+// their sums through distributed shared memory took 1.5 to 3 us to start: the
+// clusters of a GPC start one after another.)
 //   warp 0:    one thread issues the loads of codes (128 rows x 128 k) and
 //              scale tiles into a ring of stages;
 //   warp 1:    tensor memory; one thread issues per stage the two scale
 //              copies and four MMAs (M = 128, N = 2 T, K = 32);
-//   warps 2-9: split X into the stages (one warp a stage), then read the
-//              accumulators and store Y.
+//   warps 2-:  split X into the stages, and where a run leaves a tile, read
+//              the accumulators and store the sums.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -43,16 +48,18 @@ namespace mxfp4 {
 
 namespace {
 
-constexpr int kVM = 128;                 // weight rows of a CTA
-constexpr int kVWorkers = 8;
-constexpr int kVThreads = 32 * (2 + kVWorkers);
+constexpr int kVM = 128;                 // weight rows of a tile
+constexpr int kVCtas = 296;              // runs: two CTAs an SM of a B200
 constexpr uint32_t kVNaN = 0x7FC00000u;
 
 template <int T>
 struct VLayout {
   static constexpr int kN = 2 * T;
-  // as many as let two CTAs share an SM (64 tokens: one CTA)
-  static constexpr int kStages = T == 8 ? 5 : (T == 16 ? 4 : (T == 32 ? 3 : 5));
+  // a warp splits 8 tokens at a time
+  static constexpr int kWorkers = T == 8 ? 4 : 8;
+  static constexpr int kThreads = 32 * (2 + kWorkers);
+  // as many as let two CTAs share an SM
+  static constexpr int kStages = T == 8 ? 5 : (T == 16 ? 5 : (T == 32 ? 4 : 3));
   // Accumulators: consecutive MMAs on one wait for each other's result, which
   // with few columns takes longer than the MMA itself, so the four K = 32
   // steps of a stage go to accumulators of their own where they fit.
@@ -63,10 +70,9 @@ struct VLayout {
   static constexpr uint32_t kBOff = kAOff + kStages * kA;
   static constexpr uint32_t kSfaOff = kBOff + kStages * kB;
   static constexpr uint32_t kSfbOff = kSfaOff + kStages * kSf;
-  // sums of this CTA's share of the tile, from every rank of its cluster
-  static constexpr uint32_t kPartOff = kSfbOff + kStages * kSf;
-  static constexpr uint32_t kBarOff = kPartOff + T * kVM * 4;
+  static constexpr uint32_t kBarOff = kSfbOff + kStages * kSf;
   static constexpr uint32_t kBytes = kBarOff + 256;
+  static_assert(2 * (kBytes + 2048) <= 227 * 1024, "two CTAs an SM");
   // tensor memory: accumulators, then per stage 4 columns of either scales
   // (their own, so that copying a stage's scales waits for no MMA)
   static constexpr uint32_t kSfCol = kAcc * kN;
@@ -123,23 +129,6 @@ __device__ __forceinline__ bool v_wait(unsigned long long* bar, uint32_t parity,
     if (failed != nullptr && (i & 63) == 63 && failed_flag(failed)) return false;
   }
   return false;
-}
-
-__device__ __forceinline__ uint32_t v_cluster_rank() {
-  uint32_t r;
-  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
-__device__ __forceinline__ void v_cluster_arrive() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void v_cluster_wait() {
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void v_peer_store(uint32_t a, uint32_t rank, float v) {
-  uint32_t d;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(rank));
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(d), "f"(v) : "memory");
 }
 
 // E4M3 code pairs (nearest, saturating at 448) of two fp32 values, and back.
@@ -237,53 +226,69 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
     static_cast<float*>(y)[at] = v;
 }
 
+// The shape of one call. Tile t covers weight rows 128 (t / t_tiles) and tokens
+// T (t % t_tiles) on (token tiles of one weight tile run close together, so
+// they find its codes in L2).
+struct VShape {
+  int m, kblocks, t_tiles, run;  // run: units of a CTA
+  int64_t n, ldx, units;
+};
+
 template <int T, bool BF16>
-__global__ void __launch_bounds__(kVThreads, 2)
+__global__ void __launch_bounds__(VLayout<T>::kThreads, 2)
     k_gemv(const __grid_constant__ CUtensorMap tm_w, const uint8_t* __restrict__ sfw,
-           const uint16_t* __restrict__ x, int64_t ldx, int m, int64_t n, int kblocks, int split,
-           void* __restrict__ y, int* __restrict__ status) {
+           const uint16_t* __restrict__ x, const VShape sh, void* __restrict__ y,
+           float* __restrict__ partial, int* __restrict__ status) {
   using L = VLayout<T>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   unsigned long long* full = reinterpret_cast<unsigned long long*>(sm + L::kBarOff);
   unsigned long long* empty = full + L::kStages;
   unsigned long long* acc_full = empty + L::kStages;
-  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(acc_full + 1);
+  unsigned long long* acc_empty = acc_full + 1;
+  unsigned long long* drain = acc_full + 2;
+  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(acc_full + 3);
   int* failed = reinterpret_cast<int*>(tmem_base + 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int rank = split > 1 ? int(v_cluster_rank()) : 0;
-  const int64_t tile = blockIdx.x / split;
-  const int64_t n0 = tile * kVM;
-  const int t0 = int(blockIdx.y) * T;
-  const int tokens = min(T, m - t0);
-  // this CTA's slab of 128-element k blocks
-  const int kb0 = int(int64_t(kblocks) * rank / split);
-  const int kb1 = int(int64_t(kblocks) * (rank + 1) / split);
+  const int kblocks = sh.kblocks;
+  // this CTA's run of units: `blocks` of them from k block kb_first of tile0
+  const int64_t u0 = int64_t(blockIdx.x) * sh.run;
+  const int blocks = int(sh.units - u0 < sh.run ? sh.units - u0 : sh.run);
+  const int64_t tile0 = u0 / kblocks;
+  const int kb_first = int(u0 - tile0 * kblocks);
+  // split batches of a stage: the same number for every tile of the call
+  const int n_batch = (min(sh.m, T) + 7) / 8;
 
-  if (split > 1) v_cluster_arrive();  // waited for before the first store to a peer
-  const uint8_t* const sf = sfw + tile * kblocks * 512;
   uint32_t issued = 0, last_ph = 0;  // loading thread: stages, last phases
-  auto load = [&](int kb, uint32_t s, uint32_t ph) {
+  int l_kb = kb_first;               // ... and its next unit
+  int64_t l_tile = tile0;
+  auto load = [&](uint32_t s, uint32_t ph) {
     issued |= 1u << s;
     last_ph = (last_ph & ~(1u << s)) | (ph << s);
+    const int64_t nt = sh.t_tiles == 1 ? l_tile : l_tile / sh.t_tiles;
     // the tile load counts the packed codes: half of the bytes it fills
     expect_tx(&full[s], L::kA / 2 + L::kSf);
-    tma_load_2d(sm + L::kAOff + s * L::kA, &tm_w, kb * 128, int(n0), &full[s]);
-    v_bulk_load(sm + L::kSfaOff + s * L::kSf, sf + int64_t(kb) * 512, L::kSf, &full[s]);
+    tma_load_2d(sm + L::kAOff + s * L::kA, &tm_w, l_kb * 128, int(nt * kVM), &full[s]);
+    v_bulk_load(sm + L::kSfaOff + s * L::kSf, sfw + (nt * kblocks + l_kb) * 512, L::kSf,
+                &full[s]);
+    if (++l_kb == kblocks) l_kb = 0, ++l_tile;
   };
   if (tid == 0) {
     for (int s = 0; s < L::kStages; ++s) {
       // the loads' announcement and a split batch each
       asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&full[s])),
-                   "r"(1 + (tokens + 7) / 8));
+                   "r"(1 + n_batch));
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&empty[s])));
     }
     asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(acc_full)));
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(acc_empty)),
+                 "r"(L::kWorkers));
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(drain)));
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     *failed = 0;
     // the first stages are free: their loads need not wait for the others
-    for (int kb = kb0; kb < kb1 && kb < kb0 + L::kStages; ++kb) load(kb, uint32_t(kb - kb0), 0);
+    for (int i = 0; i < blocks && i < L::kStages; ++i) load(uint32_t(i), 0);
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -300,22 +305,33 @@ __global__ void __launch_bounds__(kVThreads, 2)
   // been consumed, and the barrier of a later block's stage reads right only
   // if the block two rounds of the ring before it has been consumed (phases
   // alternate), so it must not be more than kStages blocks ahead of that.
+  // The planes of tokens that a tile lacks hold whatever was there: an MMA
+  // column depends on its own row of the operand alone, and theirs are not
+  // stored.
   const int w = warp - 2, half = lane >> 4, l16 = lane & 15;
-  const int n_batch = (tokens + 7) / 8;
-  const int n_items = (kb1 - kb0) * n_batch;
-  const int active = min(kVWorkers, L::kStages * n_batch);
+  const int n_items = blocks * n_batch;
+  const int active = min(L::kWorkers, L::kStages * n_batch);
+  // unit of item i: its tile relative to tile0, k block and token base
+  auto locate = [&](int i, int& blk, int& b, int& rel, int& kb, int& t0) {
+    blk = n_batch == 1 ? i : i / n_batch;
+    b = i - blk * n_batch;
+    rel = (kb_first + blk) / kblocks;
+    kb = kb_first + blk - rel * kblocks;
+    t0 = sh.t_tiles == 1 ? 0 : int((tile0 + rel) % sh.t_tiles) * T;
+  };
   int f_i = w < active ? w : n_items;  // the next batch to fetch
   struct Batch {
     uint4 r[4];
   };
   auto fetch = [&](Batch& q) {
     if (f_i < n_items) {
-      const int blk = f_i / n_batch, b = f_i - blk * n_batch;
-      const uint16_t* xp = x + int64_t(kb0 + blk) * 128 + l16 * 8;
+      int blk, b, rel, kb, t0;
+      locate(f_i, blk, b, rel, kb, t0);
+      const uint16_t* xp = x + int64_t(kb) * 128 + l16 * 8;
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int t = 8 * b + 2 * j + half;
-        if (t < tokens) q.r[j] = ld_l1(xp + int64_t(t0 + t) * ldx);
+        const int t = t0 + 8 * b + 2 * j + half;
+        if (t < sh.m && 8 * b < T) q.r[j] = ld_l1(xp + int64_t(t) * sh.ldx);
       }
     }
     f_i += active;
@@ -326,29 +342,22 @@ __global__ void __launch_bounds__(kVThreads, 2)
     for (int j = 0; j < 4; ++j) b0.r[j] = b1.r[j] = b2.r[j] = make_uint4(0, 0, 0, 0);
     fetch(b0);
     fetch(b1);
-    // rows of absent tokens stay zero, and so do their scales
-    uint4* b = reinterpret_cast<uint4*>(sm + L::kBOff);
-    for (int i = tid - 64; i < int(L::kStages * L::kB / 16); i += 32 * kVWorkers)
-      b[i] = make_uint4(0, 0, 0, 0);
-    uint4* f = reinterpret_cast<uint4*>(sm + L::kSfbOff);
-    for (int i = tid - 64; i < int(L::kStages * L::kSf / 16); i += 32 * kVWorkers)
-      f[i] = make_uint4(0, 0, 0, 0);
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   }
   asm volatile("tcgen05.fence::before_thread_sync;");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;");
   const uint32_t tmem = *tmem_base;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
   if (warp == 0) {
     if (lane == 0) {
       uint32_t s = 0, ph = 1;
-      for (int kb = kb0 + L::kStages; kb < kb1; ++kb) {
+      for (int i = L::kStages; i < blocks; ++i) {
         if (!v_wait(&empty[s], ph ^ 1u, failed)) {
           atomicExch(failed, 1);
           break;
         }
-        load(kb, s, ph);
+        load(s, ph);
         if (++s == L::kStages) s = 0, ph ^= 1u;
       }
       // every load has landed before the CTA can end (the workers' arrival
@@ -367,12 +376,16 @@ __global__ void __launch_bounds__(kVThreads, 2)
       const uint64_t fb0 = smem_desc(sm + L::kSfbOff, 16, 128);
       const uint32_t sf0 = tmem + L::kSfCol;
       bool ok = true;
-      uint32_t ph = 0;
-      for (int kb = kb0; kb < kb1 && ok; kb += L::kStages, ph ^= 1u) {
+      uint32_t ph = 0, seg = 0;
+      int kb = kb_first;
+      uint32_t fresh = 1;  // the next MMAs start their accumulators
+      for (int i = 0; i < blocks && ok; i += L::kStages, ph ^= 1u) {
 #pragma unroll
         for (int s = 0; s < L::kStages; ++s) {
-          if (kb + s >= kb1) break;
-          if (!v_wait(&full[s], ph, failed)) {
+          if (i + s >= blocks) break;
+          // a new tile: its accumulators have been read
+          if ((fresh && seg > 0 && !v_wait(acc_empty, (seg - 1) & 1u, failed)) ||
+              !v_wait(&full[s], ph, failed)) {
             ok = false;
             break;
           }
@@ -384,124 +397,153 @@ __global__ void __launch_bounds__(kVThreads, 2)
           for (uint32_t g = 0; g < 4; ++g)
             mma_mxf8f6f4(tmem + (g % L::kAcc) * L::kN, a0 + (s * (L::kA >> 4) + 2 * g),
                          b0d + (s * (L::kB >> 4) + 2 * g), L::kIdesc | (g << 29) | (g << 4),
-                         (s > 0 || g >= L::kAcc || kb > kb0) ? 1u : 0u, sfa + (g << 30),
-                         sfb + (g << 30));
+                         g >= L::kAcc ? 1u : fresh ^ 1u, sfa + (g << 30), sfb + (g << 30));
           commit_to(&empty[s]);
+          fresh = 0;
+          if (++kb == kblocks || i + s + 1 == blocks) {
+            commit_to(acc_full);
+            ++seg;
+            fresh = 1;
+            kb = 0;
+          }
         }
       }
       if (!ok) atomicExch(failed, 1);
-      commit_to(acc_full);
       // the MMAs issued have completed before shared or tensor memory goes
-      if (!v_wait(acc_full, 0, nullptr)) atomicExch(failed, 1);
+      commit_to(drain);
+      if (!v_wait(drain, 0, nullptr)) atomicExch(failed, 1);
     }
     __syncwarp();
   } else {
-    for (int i = w < active ? w : n_items; i < n_items; i += active) {
-      const int blk = i / n_batch, b = i - blk * n_batch;
-      const uint32_t s = uint32_t(blk % L::kStages), ph = uint32_t(blk / L::kStages) & 1u;
-      fetch(b2);
-      if (!__all_sync(0xFFFFFFFFu, v_wait(&empty[s], ph ^ 1u, failed))) {
-        atomicExch(failed, 1);
-        break;
-      }
-      uint8_t* const bt = sm + L::kBOff + s * L::kB;
-      uint8_t* const ft = sm + L::kSfbOff + s * L::kSf + (l16 >> 2);
-      auto put = [&](const Planes& p, int t) {
-        if (t >= tokens) return;
-        // row r of the 128-byte swizzled K-major operand: 16-byte chunk c at
-        // c ^ (r % 8); this lane's 8 codes are half a chunk
-        const uint32_t c = uint32_t(l16 >> 1), o = uint32_t(l16 & 1) * 8;
-        const uint32_t rl = uint32_t(T + t);
-        *reinterpret_cast<uint2*>(bt + t * 128 + ((c ^ (t & 7)) << 4) + o) = p.hi;
-        *reinterpret_cast<uint2*>(bt + rl * 128 + ((c ^ (rl & 7)) << 4) + o) = p.lo;
-        if ((lane & 3) == 0) {
-          ft[16 * (t & 31) + 4 * (t >> 5)] = uint8_t(p.s_hi);
-          ft[16 * (rl & 31) + 4 * (rl >> 5)] = uint8_t(p.s_lo);
+    const int segs = (kb_first + blocks + kblocks - 1) / kblocks;
+    int i = w < active ? w : n_items;
+    for (int seg = 0; seg < segs; ++seg) {
+      // the batches of this tile
+      for (; i < n_items; i += active) {
+        int blk, b, rel, kb, t0;
+        locate(i, blk, b, rel, kb, t0);
+        if (rel != seg) break;
+        const uint32_t s = uint32_t(blk % L::kStages), ph = uint32_t(blk / L::kStages) & 1u;
+        fetch(b2);
+        if (!__all_sync(0xFFFFFFFFu, v_wait(&empty[s], ph ^ 1u, failed))) {
+          atomicExch(failed, 1);
+          break;
         }
-      };
-      if (tokens - 8 * b <= 2) {
-        Planes p[1];
-        split8<1>(b0.r, p);
-        put(p[0], 8 * b + half);
-      } else {
-        Planes p[4];
-        split8<4>(b0.r, p);
+        uint8_t* const bt = sm + L::kBOff + s * L::kB;
+        uint8_t* const ft = sm + L::kSfbOff + s * L::kSf + (l16 >> 2);
+        auto put = [&](const Planes& p, int t) {
+          // row r of the 128-byte swizzled K-major operand: 16-byte chunk c
+          // at c ^ (r % 8); this lane's 8 codes are half a chunk
+          const uint32_t c = uint32_t(l16 >> 1), o = uint32_t(l16 & 1) * 8;
+          const uint32_t rl = uint32_t(T + t);
+          *reinterpret_cast<uint2*>(bt + t * 128 + ((c ^ (t & 7)) << 4) + o) = p.hi;
+          *reinterpret_cast<uint2*>(bt + rl * 128 + ((c ^ (rl & 7)) << 4) + o) = p.lo;
+          if ((lane & 3) == 0) {
+            ft[16 * (t & 31) + 4 * (t >> 5)] = uint8_t(p.s_hi);
+            ft[16 * (rl & 31) + 4 * (rl >> 5)] = uint8_t(p.s_lo);
+          }
+        };
+        if (sh.m - t0 - 8 * b <= 2) {
+          Planes p[1];
+          split8<1>(b0.r, p);
+          put(p[0], 8 * b + half);
+        } else {
+          Planes p[4];
+          split8<4>(b0.r, p);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) put(p[j], 8 * b + 2 * j + half);
+          for (int j = 0; j < 4; ++j) put(p[j], 8 * b + 2 * j + half);
+        }
+        b0 = b1;
+        b1 = b2;
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        __syncwarp();
+        if (lane == 0)
+          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&full[s]))
+                       : "memory");
       }
-      b0 = b1;
-      b1 = b2;
-      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      // the tile's sums: lane quarter q of tensor memory holds rows 32 q +
+      // lane; with 8 workers two warps a quarter, half of the tokens each
+      const int64_t tile = tile0 + seg;
+      const int64_t nt = sh.t_tiles == 1 ? tile : tile / sh.t_tiles;
+      const int t0 = int(tile - nt * sh.t_tiles) * T;
+      const int tokens = min(T, sh.m - t0);
+      const bool whole = (seg > 0 || kb_first == 0) && (seg + 1) * kblocks <= kb_first + blocks;
+      const bool got = __all_sync(
+          0xFFFFFFFFu, !failed_flag(failed) && v_wait(acc_full, uint32_t(seg) & 1u, failed,
+                                                      kAccWaitLimit < kVWaitLimit ? kAccWaitLimit
+                                                                                  : kVWaitLimit));
+      if (!got) atomicExch(failed, 1);
+      asm volatile("tcgen05.fence::after_thread_sync;");
+      constexpr int kSpan = T * 4 / L::kWorkers;  // tokens of a warp
+      const int q = warp & 3, row = 32 * q + lane, h = w >> 2;
+      const uint32_t tb = tmem + (uint32_t(32 * q) << 16);
+      float* const part = partial + (int64_t(blockIdx.x) + tile) * (T * kVM) + row;
+#pragma unroll
+      for (int c = h * kSpan; c < (h + 1) * kSpan; c += 4) {
+        uint32_t a[L::kAcc][2][4];
+#pragma unroll
+        for (int k = 0; k < L::kAcc; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(a[k][e][0]), "=r"(a[k][e][1]), "=r"(a[k][e][2]), "=r"(a[k][e][3])
+                         : "r"(tb + k * L::kN + e * T + c));
+        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float v = 0.0f;
+#pragma unroll
+          for (int k = 0; k < L::kAcc; ++k)
+            v = __fadd_rn(v, __fadd_rn(__uint_as_float(a[k][0][j]), __uint_as_float(a[k][1][j])));
+          if (!got) v = __uint_as_float(kVNaN);
+          if (c + j >= tokens) continue;
+          if (!whole)
+            part[(c + j) * kVM] = v;
+          else if (nt * kVM + row < sh.n)
+            store_y<BF16>(y, int64_t(t0 + c + j) * sh.n + nt * kVM + row, v);
+        }
+      }
+      asm volatile("tcgen05.fence::before_thread_sync;");
       __syncwarp();
       if (lane == 0)
-        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&full[s]))
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(acc_empty))
                      : "memory");
     }
   }
+  asm volatile("tcgen05.fence::before_thread_sync;");
   __syncthreads();
-
-  // Epilogue: worker warps read the accumulator (lane quarter q = rows 32 q
-  // + lane; two warps a quarter, half of the tokens each). In a cluster the
-  // rows are shared out for the joining, 128 / split to a rank: every rank
-  // stores its sums for them at their owner, which adds them in rank order.
-  const int share = kVM / split;  // split is a power of two
-  if (split > 1) v_cluster_wait();  // every CTA of the cluster has started
-  if (warp >= 2) {
-    asm volatile("tcgen05.fence::after_thread_sync;");
-    const bool bad = failed_flag(failed) || !v_wait(acc_full, 0, nullptr, kAccWaitLimit);
-    if (bad) atomicExch(failed, 1);
-    const int q = warp & 3, row = 32 * q + lane, h = w >> 2;
-    const uint32_t tb = tmem + (uint32_t(32 * q) << 16);
-    const int owner = row / share;
-    const uint32_t part = smem_u32(sm + L::kPartOff);
-#pragma unroll
-    for (int c = h * (T / 2); c < (h + 1) * (T / 2); c += 4) {
-      uint32_t a[L::kAcc][2][4];
-#pragma unroll
-      for (int k = 0; k < L::kAcc; ++k)
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(a[k][i][0]), "=r"(a[k][i][1]), "=r"(a[k][i][2]), "=r"(a[k][i][3])
-                       : "r"(tb + k * L::kN + i * T + c));
-      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int t = c + j;
-        float v = 0.0f;
-#pragma unroll
-        for (int k = 0; k < L::kAcc; ++k)
-          v = __fadd_rn(v, __fadd_rn(__uint_as_float(a[k][0][j]), __uint_as_float(a[k][1][j])));
-        if (bad) v = __uint_as_float(kVNaN);
-        if (t < tokens) {
-          if (split > 1)  // [rank][token][row of the share]
-            v_peer_store(part + 4 * ((rank * T + t) * share + row - owner * share),
-                         uint32_t(owner), v);
-          else if (n0 + row < n)
-            store_y<BF16>(y, int64_t(t0 + t) * n + n0 + row, v);
-        }
-      }
-    }
-    asm volatile("tcgen05.fence::before_thread_sync;");
-  }
-  if (split > 1) {
-    v_cluster_arrive();
-    v_cluster_wait();
-    const float* part = reinterpret_cast<const float*>(sm + L::kPartOff);
-    for (int i = tid; i < tokens * share; i += kVThreads) {
-      const int t = i / share, r = i % share;
-      float v = part[t * share + r];
-      for (int k = 1; k < split; ++k) v = __fadd_rn(v, part[(k * T + t) * share + r]);
-      const int64_t row = n0 + rank * share + r;
-      if (row < n) store_y<BF16>(y, int64_t(t0 + t) * n + row, v);
-    }
-  } else {
-    __syncthreads();
-  }
   report_failure(status, failed);
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(L::kTmemCols));
+}
+
+// Tiles that several runs share: run i's sums of tile t are at i + t (runs
+// and tiles only ever go up together, so no two pairs share a place).
+template <int T, bool BF16>
+__global__ void __launch_bounds__(256)
+    k_gemv_join(const float* __restrict__ partial, const VShape sh, void* __restrict__ y) {
+  constexpr int kPer = T * kVM / 256;  // CTAs a tile
+  const int64_t tile = blockIdx.x / kPer;
+  const int e = int(blockIdx.x % kPer) * 256 + threadIdx.x;
+  const int64_t first = tile * sh.kblocks / sh.run;
+  const int64_t last = ((tile + 1) * sh.kblocks - 1) / sh.run;
+  const int64_t nt = tile / sh.t_tiles;
+  const int64_t t = (tile - nt * sh.t_tiles) * T + e / kVM, row = nt * kVM + e % kVM;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (first == last || t >= sh.m || row >= sh.n) return;
+  const float* p = partial + (first + tile) * (T * kVM) + e;
+  float v = __ldcg(p);
+  int64_t i = first + 1;
+  for (; i + 3 <= last; i += 4) {
+    float q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) q[k] = __ldcg(p += T * kVM);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v = __fadd_rn(v, q[k]);
+  }
+  for (; i <= last; ++i) v = __fadd_rn(v, __ldcg(p += T * kVM));
+  store_y<BF16>(y, t * sh.n + row, v);
 }
 
 // Any k that is a multiple of 32 (the tensor-core kernel takes multiples of
@@ -578,17 +620,31 @@ struct GemvArgs {
   int64_t m, n, k, ldx;
   const uint8_t *codes, *scales;
   void* y;
+  void* workspace;
   int* status;
   cudaStream_t s;
 };
 
-// Slabs of k: enough CTAs to give every SM about two (the loads of two CTAs
-// keep an SM's share of the memory bandwidth busy), at least two k blocks a
-// slab, powers of two up to the portable cluster size.
-int gemv_split(int64_t tiles, int64_t kblocks) {
-  int split = 1;
-  while (split < 8 && tiles * split * 2 <= 296 && kblocks / (split * 2) >= 2) split *= 2;
-  return split;
+int gemv_tokens(int64_t m) { return m <= 8 ? 8 : (m <= 16 ? 16 : (m <= 32 ? 32 : 64)); }
+
+// How the units are dealt out. Runs of at least two units; runs that hold
+// several tiles anyway are rounded up to whole tiles, which saves the joining
+// (about 2 us) for at most a quarter more work in the longest run.
+VShape gemv_shape(int64_t m, int64_t n, int64_t k, int64_t ldx) {
+  const int T = gemv_tokens(m);
+  VShape sh;
+  sh.m = int(m);
+  sh.kblocks = int(k / 128);
+  sh.t_tiles = int((m + T - 1) / T);
+  sh.n = n;
+  sh.ldx = ldx;
+  sh.units = (n + kVM - 1) / kVM * sh.t_tiles * sh.kblocks;
+  int64_t run = (sh.units + kVCtas - 1) / kVCtas;
+  if (run < 2) run = 2;
+  if (run >= 4 * int64_t(sh.kblocks) || sh.kblocks == 1)
+    run = (run + sh.kblocks - 1) / sh.kblocks * sh.kblocks;
+  sh.run = int(run);
+  return sh;
 }
 
 template <int T, bool BF16>
@@ -600,32 +656,34 @@ cudaError_t gemv_tc(const GemvArgs& a) {
   constexpr size_t smem = L::kBytes + 1024;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (a.n + kVM - 1) / kVM, t_tiles = (a.m + T - 1) / T;
-  const int64_t kblocks = a.k / 128;
-  const int split = gemv_split(tiles * t_tiles, kblocks);
+  const VShape sh = gemv_shape(a.m, a.n, a.k, a.ldx);
+  const unsigned grid = unsigned((sh.units + sh.run - 1) / sh.run);
+  float* partial = static_cast<float*>(a.workspace);
+  kern<<<grid, L::kThreads, smem, a.s>>>(tm, a.scales, a.x, sh, a.y, partial, a.status);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || sh.run % sh.kblocks == 0) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(tiles * split), unsigned(t_tiles));
-  cfg.blockDim = dim3(kVThreads);
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3(unsigned(sh.units / sh.kblocks * (T * kVM / 256)));
+  cfg.blockDim = dim3(256);
   cfg.stream = a.s;
   cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = unsigned(split);
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, tm, a.scales, a.x, a.ldx, int(a.m), a.n, int(kblocks),
-                            split, a.y, a.status);
+  return cudaLaunchKernelEx(&cfg, k_gemv_join<T, BF16>, static_cast<const float*>(partial), sh,
+                            a.y);
 }
 
 template <bool BF16>
 cudaError_t gemv_any(const GemvArgs& a) {
   if (a.k % 128 == 0 && (reinterpret_cast<uintptr_t>(a.codes) & 31u) == 0) {
-    if (a.m <= 8) return gemv_tc<8, BF16>(a);
-    if (a.m <= 16) return gemv_tc<16, BF16>(a);
-    if (a.m <= 32) return gemv_tc<32, BF16>(a);
-    return gemv_tc<64, BF16>(a);
+    switch (gemv_tokens(a.m)) {
+      case 8: return gemv_tc<8, BF16>(a);
+      case 16: return gemv_tc<16, BF16>(a);
+      case 32: return gemv_tc<32, BF16>(a);
+      default: return gemv_tc<64, BF16>(a);
+    }
   }
   const dim3 grid(unsigned((a.n + 7) / 8), unsigned(a.m == 1 ? 1 : (a.m + 7) / 8));
   if (a.m == 1)
@@ -639,10 +697,19 @@ cudaError_t gemv_any(const GemvArgs& a) {
 
 }  // namespace
 
+int64_t gemv_workspace(int64_t m, int64_t n, int64_t k) {
+  if (k % 128 != 0) return 0;
+  const VShape sh = gemv_shape(m, n, k, k);
+  if (sh.run % sh.kblocks == 0) return 0;
+  const int64_t runs = (sh.units + sh.run - 1) / sh.run;
+  return (runs + sh.units / sh.kblocks) * gemv_tokens(m) * kVM * int64_t(sizeof(float));
+}
+
 cudaError_t launch_gemv(const void* x, int64_t m, int64_t n, int64_t k, int64_t ldx,
                         const uint8_t* codes, const uint8_t* scales, void* y, bool bf16_out,
-                        int* status, cudaStream_t s) {
-  const GemvArgs a = {static_cast<const uint16_t*>(x), m, n, k, ldx, codes, scales, y, status, s};
+                        void* workspace, int* status, cudaStream_t s) {
+  const GemvArgs a = {static_cast<const uint16_t*>(x), m, n, k, ldx, codes, scales, y, workspace,
+                      status, s};
   return bf16_out ? gemv_any<true>(a) : gemv_any<false>(a);
 }
 

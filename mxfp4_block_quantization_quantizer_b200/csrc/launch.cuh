@@ -90,9 +90,10 @@ cudaError_t launch_gemm_qa(const void* x, int64_t m, int64_t n, int64_t k, bool 
 // Y[m][n] = X W^T with bf16 X (row stride ldx) left unquantized and W as MXFP4
 // codes and blocked scales; bf16_out: Y bf16, else fp32; status as for
 // launch_rht_quant.
+int64_t gemv_workspace(int64_t m, int64_t n, int64_t k);
 cudaError_t launch_gemv(const void* x, int64_t m, int64_t n, int64_t k, int64_t ldx,
                         const uint8_t* codes, const uint8_t* scales, void* y, bool bf16_out,
-                        int* status, cudaStream_t s);
+                        void* workspace, int* status, cudaStream_t s);
 
 // Newton-Schulz orthogonalization of g [rows][cols] into out (see
 // mxfp4_newton_schulz), and the bytes of workspace it takes.

@@ -218,15 +218,17 @@ def test_timeout_sets_status_and_poisons(tmp_path):
     B.build_variant(path, ["MXFP4_ACC_WAIT_POLLS=0"])
     L = ctypes.CDLL(path)
     vp, i64 = ctypes.c_void_p, ctypes.c_int64
-    L.mxfp4_gemv.argtypes = [vp, i64, i64, i64, i64, vp, vp, vp, ctypes.c_int, vp, vp]
+    L.mxfp4_gemv.argtypes = [vp, i64, i64, i64, i64, vp, vp, vp, ctypes.c_int, vp, i64, vp, vp]
     for rows, n, k in ((2, 256, 1024), (9, 20000, 128)):
         codes, scales = weight(n, k, 22)
         blocked = m.scales_to_blocked(scales)
         x = torch.randn(rows, k, generator=gen(23), device="cuda").to(BF)
         y = torch.zeros(rows, n, device="cuda")
         st = torch.zeros(1, dtype=torch.int32, device="cuda")
+        need = m.lib().mxfp4_gemv_workspace(rows, n, k)
+        ws = torch.zeros(need + 16, dtype=torch.uint8, device="cuda")
         assert L.mxfp4_gemv(x.data_ptr(), rows, n, k, k, codes.data_ptr(), blocked.data_ptr(),
-                            y.data_ptr(), m.F32, st.data_ptr(),
+                            y.data_ptr(), m.F32, ws.data_ptr(), need, st.data_ptr(),
                             torch.cuda.current_stream().cuda_stream) == 0
         torch.cuda.synchronize()
         assert int(st.item()) == m.STATUS_WAIT_TIMEOUT and torch.isnan(y).all()
