@@ -392,8 +392,8 @@ mxfp4_status mxfp4_gemm_quantize_a(const void* x, int64_t m, int64_t n, int64_t 
                                    const uint8_t* b_scales, float* c, uint8_t* a_codes,
                                    uint8_t* a_scales, int* status, void* stream);
 
-/* Bytes of workspace mxfp4_gemv needs (0 where it needs none; a few MB at
- * most for a few rows); -1 for a shape it refuses. */
+/* Bytes of workspace mxfp4_gemv needs (about 4 m k, m rounded up to 2, 8, 16
+ * or a multiple of 32); -1 for a shape it refuses. */
 int64_t mxfp4_gemv_workspace(int64_t m, int64_t n, int64_t k);
 
 /*
@@ -401,27 +401,25 @@ int64_t mxfp4_gemv_workspace(int64_t m, int64_t n, int64_t k);
  * answers single tokens with (m = 1 to a few dozen):
  *   Y[m][n] = sum_k X[m][k] * B[n][k]         (fp32 accumulate)
  * X is bf16 and is not quantized; B is given as in mxfp4_gemm. The products
- * run on the block-scaled tensor cores: each x enters as the sum of two E4M3
- * values with a power-of-two scale per 32 elements each, which is x exactly
- * unless |x| is below 2^-13 of the largest magnitude of its group of 32, and
- * off by at most 2^-21 of that magnitude then. Sums are fp32; Y is rounded
- * once. The sums of one call do not depend on anything but its arguments
- * (the same bits every time).
+ * run on the block-scaled tensor cores: each x enters as eight base-8 digits
+ * (E2M1 values with a power-of-two scale per 32 elements), which add up to x
+ * exactly where |x| is at least 2^-16 of the largest magnitude of its group
+ * of 32, and are off by at most 2^-23 of that magnitude otherwise (by 2^-128
+ * in groups whose largest magnitude is below 2^-104). Sums are fp32; Y is
+ * rounded once. The same arguments give the same bits every time.
  *   x        device bf16, row i at x + i * ldx elements; 16-byte aligned,
  *            ldx >= k a multiple of 8
- *   b_codes  device [n][k/2], 16-byte aligned (32-byte aligned codes with k
- *            a multiple of 128 take the tensor cores, other ones the
- *            slower CUDA cores, which take x as it is)
+ *   b_codes  device [n][k/2], 16-byte aligned
  *   b_scales device, blocked order (rows = n, groups = k/32), 16-byte aligned
  *   y        device [m][n] of y_dtype, 16-byte aligned, written; must not
  *            overlap x
  *   workspace  device, 16-byte aligned, workspace_bytes of scratch (at least
- *            mxfp4_gemv_workspace; NULL where that is 0); calls that run at
- *            the same time need workspaces of their own
+ *            mxfp4_gemv_workspace); calls that run at the same time need
+ *            workspaces of their own
  *   status   device int or NULL (MXFP4_STATUS_WAIT_TIMEOUT above); the tiles
  *            of a CTA whose wait ran out hold NaN
- * k must be a multiple of 32, m at most 2^19. A group of x that holds Inf or
- * NaN gives NaN in its row of Y, a scale byte of 0xFF in its column.
+ * k must be a multiple of 32, m at most 2^19, k at most 2^30. A group of x that holds Inf or
+ * NaN makes its row of Y NaN, a scale byte of 0xFF its column.
  * Any m works; from about a hundred rows on, quantizing X (mxfp4_gemm) or
  * decoding B (mxfp4_dequantize) and a dense product are faster.
  * Source: "Microscaling FP4 Quantization: MR-GPTQ Achieves 6x Speedup"

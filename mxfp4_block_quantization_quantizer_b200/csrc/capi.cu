@@ -289,7 +289,7 @@ mxfp4_status layernorm_args(const void* x, int dtype, int64_t rows, int64_t cols
 namespace {
 bool gemv_dims_ok(int64_t m, int64_t n, int64_t k) {
   return dims_ok(m, k) && dims_ok(n, k) && dims_ok(m, n) && k % 32 == 0 &&
-         m <= (int64_t(1) << 19);  // grid y
+         m <= (int64_t(1) << 19) && k <= (int64_t(1) << 30);  // grids, 32-bit k counts
 }
 }  // namespace
 
@@ -301,14 +301,12 @@ mxfp4_status mxfp4_gemv(const void* x, int64_t m, int64_t n, int64_t k, int64_t 
                         const uint8_t* b_codes, const uint8_t* b_scales, void* y, int y_dtype,
                         void* workspace, int64_t workspace_bytes, int* status, void* stream) {
   if (!dtype_ok(y_dtype)) return MXFP4_ERR_ENUM;
-  if (!x || !b_codes || !b_scales || !y) return MXFP4_ERR_NULL;
+  if (!x || !b_codes || !b_scales || !y || !workspace) return MXFP4_ERR_NULL;
   if (!gemv_dims_ok(m, n, k) || !stride_ok(m, k, ldx) || ldx % 8) return MXFP4_ERR_SHAPE;
   if (!aligned16(x) || !aligned16(b_codes) || !aligned16(b_scales) || !aligned16(y) ||
       !aligned16(workspace) || !aligned4(status))
     return MXFP4_ERR_ALIGN;
-  const int64_t need = mxfp4::gemv_workspace(m, n, k);
-  if (need > 0 && workspace == nullptr) return MXFP4_ERR_NULL;
-  if (workspace_bytes < need) return MXFP4_ERR_WORKSPACE;
+  if (workspace_bytes < mxfp4::gemv_workspace(m, n, k)) return MXFP4_ERR_WORKSPACE;
   return from_cuda(mxfp4::launch_gemv(x, m, n, k, ldx, b_codes, b_scales, y,
                                       y_dtype == MXFP4_BF16, workspace, status,
                                       as_stream(stream)));
