@@ -392,8 +392,8 @@ mxfp4_status mxfp4_gemm_quantize_a(const void* x, int64_t m, int64_t n, int64_t 
                                    const uint8_t* b_scales, float* c, uint8_t* a_codes,
                                    uint8_t* a_scales, int* status, void* stream);
 
-/* Bytes of workspace mxfp4_gemv needs (about 4 m k, m rounded up to 2, 8, 16
- * or a multiple of 32); -1 for a shape it refuses. */
+/* Bytes of workspace mxfp4_gemv needs (0 for m <= 2; about 4 m k else, m
+ * rounded up to 8, 16 or a multiple of 32); -1 for a shape it refuses. */
 int64_t mxfp4_gemv_workspace(int64_t m, int64_t n, int64_t k);
 
 /*
@@ -414,8 +414,8 @@ int64_t mxfp4_gemv_workspace(int64_t m, int64_t n, int64_t k);
  *   y        device [m][n] of y_dtype, 16-byte aligned, written; must not
  *            overlap x
  *   workspace  device, 16-byte aligned, workspace_bytes of scratch (at least
- *            mxfp4_gemv_workspace); calls that run at the same time need
- *            workspaces of their own
+ *            mxfp4_gemv_workspace; NULL where that is 0); calls that run at
+ *            the same time need workspaces of their own
  *   status   device int or NULL (MXFP4_STATUS_WAIT_TIMEOUT above); the tiles
  *            of a CTA whose wait ran out hold NaN
  * k must be a multiple of 32, m at most 2^19, k at most 2^30. A group of x that holds Inf or

@@ -495,10 +495,11 @@ def gemv(x, b_codes, b_blocked, out_dtype=torch.bfloat16, out=None, workspace=No
         _buffer(out, "out", out.dtype, m * n, d)
         _apart(out, "out", x)
     st = None if status is None else _addr(_buffer(status, "status", torch.int32, 1, d))
-    workspace = _workspace(workspace, lib().mxfp4_gemv_workspace(m, n, k), d)
+    need = lib().mxfp4_gemv_workspace(m, n, k)
+    workspace = _workspace(workspace, need, d) if need > 0 else None
     _call("mxfp4_gemv", d, stream, x.data_ptr(), m, n, k, ldx, b_codes.data_ptr(),
-          b_blocked.data_ptr(), out.data_ptr(), _dtype_code(out), workspace.data_ptr(),
-          workspace.numel(), st)
+          b_blocked.data_ptr(), out.data_ptr(), _dtype_code(out), _addr(workspace), max(need, 0),
+          st)
     return out
 
 

@@ -301,12 +301,14 @@ mxfp4_status mxfp4_gemv(const void* x, int64_t m, int64_t n, int64_t k, int64_t 
                         const uint8_t* b_codes, const uint8_t* b_scales, void* y, int y_dtype,
                         void* workspace, int64_t workspace_bytes, int* status, void* stream) {
   if (!dtype_ok(y_dtype)) return MXFP4_ERR_ENUM;
-  if (!x || !b_codes || !b_scales || !y || !workspace) return MXFP4_ERR_NULL;
+  if (!x || !b_codes || !b_scales || !y) return MXFP4_ERR_NULL;
   if (!gemv_dims_ok(m, n, k) || !stride_ok(m, k, ldx) || ldx % 8) return MXFP4_ERR_SHAPE;
   if (!aligned16(x) || !aligned16(b_codes) || !aligned16(b_scales) || !aligned16(y) ||
       !aligned16(workspace) || !aligned4(status))
     return MXFP4_ERR_ALIGN;
-  if (workspace_bytes < mxfp4::gemv_workspace(m, n, k)) return MXFP4_ERR_WORKSPACE;
+  const int64_t need = mxfp4::gemv_workspace(m, n, k);
+  if (need > 0 && workspace == nullptr) return MXFP4_ERR_NULL;
+  if (workspace_bytes < need) return MXFP4_ERR_WORKSPACE;
   return from_cuda(mxfp4::launch_gemv(x, m, n, k, ldx, b_codes, b_scales, y,
                                       y_dtype == MXFP4_BF16, workspace, status,
                                       as_stream(stream)));

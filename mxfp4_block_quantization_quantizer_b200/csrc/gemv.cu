@@ -26,17 +26,19 @@
 // kind::mxf8f6f4, whose MMAs take 32 k instead of 64 and 16 bytes of shared
 // memory for 8 of codes: the issue of its MMAs bound the kernel at 4.7 TB/s.)
 //
-// Two launches. k_gemv_digits writes the operand of X once, in the order in
-// which a stage of the product reads it. k_gemv, launched over it (it sets
-// up and loads weights meanwhile and waits before it reads digits):
-// one CTA takes 128 weight rows, T tokens (N = 8 T columns) and a slab of k;
+// One CTA takes 128 weight rows, T tokens (N = 8 T columns) and a slab of k;
 // the CTAs of a cluster take the slabs of the same rows and add their sums
 // through distributed shared memory in the order of their ranks (no atomics).
 //   warp 0:    one thread issues the loads of a stage (256 k: codes, scale
 //              tiles, digits) into a ring;
 //   warp 1:    tensor memory; one thread issues per stage the scale copies
 //              and four MMAs (M = 128, N = 8 T, K = 64);
-//   warps 2-5: epilogue.
+//   warps 2-5: for one or two tokens, write their digits into the stages
+//              (every CTA for itself: one launch, no workspace); epilogue.
+// For more tokens the digits cost more instructions than a stage leaves time
+// for, so k_gemv_digits writes them once, in the order in which a stage reads
+// them, and k_gemv is launched over it: it sets up and loads weights
+// meanwhile and waits before it reads digits.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -157,28 +159,14 @@ __device__ __forceinline__ void store_y(void* y, int64_t at, float v) {
     static_cast<float*>(y)[at] = v;
 }
 
-// The digits of X: for token tile tt and stage kb (256 k), block
-// tt * stages + kb holds the B operand (row p T + t, 128 bytes of codes, 16-byte
-// chunk c at c ^ (row % 8): the 128-byte swizzle) and behind it its scale
-// tiles [128-k half][row block]. A thread takes 8 elements, 4 threads a
-// group; groups from k on (up to whole MMAs of 64) get zeros. A group with
-// Inf or NaN gets scale byte 0xFF (NaN) for every digit.
-template <int T>
-__global__ void __launch_bounds__(256)
-    k_gemv_digits(const uint16_t* __restrict__ x, int64_t ldx, int m, int64_t k, int64_t k64,
-                  int stages, uint8_t* __restrict__ digits) {
-  using L = VLayout<T>;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int64_t per = k64 / 8;  // threads a token
-  const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
-  const int64_t token = id / per, e = (id - token * per) * 8;
-  const bool in = token < m;    // whole groups: 4 threads agree
-  uint4 raw = make_uint4(0, 0, 0, 0);
-  if (in && e < k) raw = ld_l1(x + token * ldx + e);
+// Digits of 8 elements of a group that 4 adjacent lanes share, in packed
+// codes: put(p, word, byte) for each digit p, byte its scale byte. A group
+// with Inf or NaN gets scale byte 0xFF (NaN) for every digit.
+template <typename Put>
+__device__ __forceinline__ void digits8(uint4 raw, Put put) {
   uint32_t am = bf16x8_absmax(raw);
   am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 1));
   am = max(am, __shfl_xor_sync(0xFFFFFFFFu, am, 2));
-  if (!in) return;
   // byte of 2^s (s = exponent - 1, no lower than what digit 7 can reach)
   const bool bad = am >= 0x7F800000u;
   const uint32_t s0 = bad ? 0xFFu : max(am >> 23, 3u * (kVDigits - 1) + 1) - 1;
@@ -190,31 +178,61 @@ __global__ void __launch_bounds__(256)
     v[2 * j] = bad ? 0.0f : __fmul_rn(bf16_lo(w[j]), mul);
     v[2 * j + 1] = bad ? 0.0f : __fmul_rn(bf16_hi(w[j]), mul);
   }
-  const int t = int(token % T), g = int(e % 256) / 32;
-  uint8_t* const block = digits + ((token / T) * stages + e / 256) * int64_t(L::kX);
 #pragma unroll
   for (int p = 0; p < kVDigits; ++p) {
-    const int r = p * T + t;
-    *reinterpret_cast<uint32_t*>(block + r * 128 + ((g ^ (r & 7)) << 4) + int(e % 32) / 2) =
-        e2m1x8_rn(v);
-    if (e % 32 == 0)
-      block[L::kB + (g / 4 * L::kRowBlocks + r / 128) * 512 + 16 * (r % 32) + 4 * (r % 128 / 32) +
-            g % 4] = uint8_t(bad ? 0xFFu : s0 - 3 * p);
+    put(p, e2m1x8_rn(v), bad ? 0xFFu : s0 - 3 * p);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fsub_rn(v[j], e2m1_rn_value(v[j])), 8.0f);
   }
 }
 
+// A stage's B operand: row p T + t holds digit p of token t, 128 bytes of
+// codes (256 k), 16-byte chunk c (a group) at c ^ (row % 8): the 128-byte
+// swizzle; behind the kN rows the scale tiles [128-k half][row block].
+template <int T>
+__device__ __forceinline__ void put_digit(uint8_t* block, int p, int t, int g, int sub,
+                                          uint32_t word, uint32_t byte) {
+  using L = VLayout<T>;
+  const int r = p * T + t;
+  *reinterpret_cast<uint32_t*>(block + r * 128 + ((g ^ (r & 7)) << 4) + sub * 4) = word;
+  if (sub == 0)
+    block[L::kB + (g / 4 * L::kRowBlocks + r / 128) * 512 + 16 * (r % 32) + 4 * (r % 128 / 32) +
+          g % 4] = uint8_t(byte);
+}
+
+// The digits of X: block tt * stages + kb holds the operand of token tile tt
+// and stage kb. A thread takes 8 elements; groups from k on (up to whole MMAs
+// of 64) get zeros.
+template <int T>
+__global__ void __launch_bounds__(256)
+    k_gemv_digits(const uint16_t* __restrict__ x, int64_t ldx, int m, int64_t k, int64_t k64,
+                  int stages, uint8_t* __restrict__ digits) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int64_t per = k64 / 8;  // threads a token
+  const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
+  const int64_t token = id / per, e = (id - token * per) * 8;
+  const bool in = token < m;    // whole groups: 4 threads agree
+  uint4 raw = make_uint4(0, 0, 0, 0);
+  if (in && e < k) raw = ld_l1(x + token * ldx + e);
+  uint8_t* const block =
+      digits + ((token / T) * stages + e / 256) * int64_t(VLayout<T>::kX);
+  digits8(raw, [&](int p, uint32_t word, uint32_t byte) {
+    if (in)
+      put_digit<T>(block, p, int(token % T), int(e % 256) / 32, int(e % 32) / 8, word, byte);
+  });
+}
+
 struct VShape {
   int m, steps, stages, split;  // steps: MMAs of 64 k; stages: of 256
-  int64_t n, k_tiles;           // k_tiles: scale tiles of 128 k
+  int64_t n, k, k_tiles, ldx;   // k_tiles: scale tiles of 128 k
 };
 
-template <int T, bool BF16>
+// OWN: the CTA writes the digits of x itself; else `digits` holds them.
+template <int T, bool OWN, bool BF16>
 __global__ void __launch_bounds__(kVThreads)
     k_gemv(const __grid_constant__ CUtensorMap tm_w, const uint8_t* __restrict__ sfw,
-           const uint8_t* __restrict__ digits, const VShape sh, void* __restrict__ y,
-           int* __restrict__ status) {
+           const uint16_t* __restrict__ x, const uint8_t* __restrict__ digits, const VShape sh,
+           void* __restrict__ y, int* __restrict__ status) {
   using L = VLayout<T>;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -241,19 +259,22 @@ __global__ void __launch_bounds__(kVThreads)
     last_ph = (last_ph & ~(1u << s)) | (ph << s);
     // (the last stage may have one scale tile)
     const uint32_t sf = 2 * kb + 1 < sh.k_tiles ? 1024u : 512u;
-    expect_tx(&full[s], L::kA + sf + L::kX);
+    expect_tx(&full[s], L::kA + sf + (OWN ? 0 : L::kX));
     tma_load_2d(sm + s * L::kA, &tm_w, kb * 128, int(n0), &full[s]);
     v_bulk_load(sm + L::kSfaOff + s * L::kSfa, sfw + (tile * sh.k_tiles + 2 * kb) * 512, sf,
                 &full[s]);
   };
   auto load_x = [&](int kb, uint32_t s) {
+    if (OWN) return;
     v_bulk_load(sm + L::kXOff + s * L::kX,
                 digits + (int64_t(blockIdx.y) * sh.stages + kb) * int64_t(L::kX), L::kX,
                 &full[s]);
   };
   if (tid == 0) {
     for (int s = 0; s < L::kStages; ++s) {
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&full[s])));
+      // the loads' announcement, and each token's digits where written here
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&full[s])),
+                   "r"(OWN ? 1 + tokens : 1));
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&empty[s])));
     }
     asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(acc_full)));
@@ -269,6 +290,25 @@ __global__ void __launch_bounds__(kVThreads)
                  "r"(L::kTmemCols));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
+  // OWN: item i of this CTA is token i % tokens of stage i / tokens; warp w
+  // takes items w, w + active, ... (a lane 8 of the token's 256 elements) and
+  // loads one ahead. Warps take turns over at most kStages stages: one that
+  // is done with stage i knows that stage i - kStages has been consumed, and
+  // the barrier of a later stage reads right only if the stage two rounds of
+  // the ring before it has been consumed (phases alternate), so it must not
+  // be more than kStages stages ahead of that. (Tokens that are absent leave
+  // their rows as they are: an MMA column depends on its own row alone.)
+  const int w = warp - 2;
+  const int n_items = OWN ? (kb1 - kb0) * tokens : 0;
+  const int active = OWN ? min(4, L::kStages * tokens) : 1;
+  auto fetch = [&](int i) {
+    const int st = i / tokens;
+    const int64_t e = int64_t(kb0 + st) * 256 + 8 * lane;
+    return i < n_items && e < sh.k ? ld_l1(x + (t0 + i - st * tokens) * sh.ldx + e)
+                                   : make_uint4(0, 0, 0, 0);
+  };
+  uint4 next = make_uint4(0, 0, 0, 0);
+  if (OWN && warp >= 2 && w < active) next = fetch(w);
   asm volatile("tcgen05.fence::before_thread_sync;");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;");
@@ -276,7 +316,7 @@ __global__ void __launch_bounds__(kVThreads)
 
   if (warp == 0) {
     if (lane == 0) {
-      asm volatile("griddepcontrol.wait;" ::: "memory");
+      if (!OWN) asm volatile("griddepcontrol.wait;" ::: "memory");
       for (int i = 0; i < L::kStages && kb0 + i < kb1; ++i) load_x(kb0 + i, uint32_t(i));
       uint32_t s = 0, ph = 1;
       for (int kb = kb0 + L::kStages; kb < kb1; ++kb) {
@@ -342,6 +382,26 @@ __global__ void __launch_bounds__(kVThreads)
       if (!v_wait(acc_full, 0, nullptr)) atomicExch(failed, 1);
     }
     __syncwarp();
+  } else if (OWN) {
+    for (int i = w < active ? w : n_items; i < n_items; i += active) {
+      const int st = i / tokens, t = i - st * tokens;
+      const uint32_t s = uint32_t(st % L::kStages), ph = uint32_t(st / L::kStages) & 1u;
+      const uint4 raw = next;
+      next = fetch(i + active);
+      if (!__all_sync(0xFFFFFFFFu, v_wait(&empty[s], ph ^ 1u, failed))) {
+        atomicExch(failed, 1);
+        break;
+      }
+      uint8_t* const block = sm + L::kXOff + s * L::kX;
+      digits8(raw, [&](int p, uint32_t word, uint32_t byte) {
+        put_digit<T>(block, p, t, lane >> 2, lane & 3, word, byte);
+      });
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+      __syncwarp();
+      if (lane == 0)
+        asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&full[s]))
+                     : "memory");
+    }
   }
   // accumulators that had an MMA (a short slab may not reach all of them)
   const int used = min(L::kAcc, sh.steps - 4 * kb0);
@@ -435,55 +495,64 @@ struct GemvArgs {
 
 int gemv_tokens(int64_t m) { return m <= 2 ? 2 : (m <= 8 ? 8 : (m <= 16 ? 16 : 32)); }
 
-// Slabs of k: as many as still fit the GPU at once (`per_sm` CTAs on 148 SMs:
-// the loads of two CTAs keep an SM's share of the memory bandwidth busy), a
-// power of two up to the portable cluster size, one stage each at least.
+// Slabs of k (a power of two up to the portable cluster size): up to one CTA
+// an SM in any case, up to `per_sm` CTAs an SM (whose loads together keep an
+// SM's share of the memory bandwidth busy) where that leaves a slab four
+// stages. 8192 x 28672 (2 CTAs an SM / 1): 25.4 / 30.8 us; 4096 x 4096, with
+// slabs of 2 / 4 stages: 9.3 / 7.6 us (clusters start one after another).
 int gemv_split(int64_t tiles, int64_t stages, int per_sm) {
   int split = 1;
-  while (split < 8 && tiles * split * 2 <= 148 * per_sm && stages / (split * 2) >= 1) split *= 2;
+  while (split < 8 && stages >= 2 * split &&
+         (tiles * split * 2 <= 148 ||
+          (tiles * split * 2 <= 148 * per_sm && stages >= 8 * split)))
+    split *= 2;
   return split;
 }
 
 template <int T, bool BF16>
 cudaError_t gemv_t(const GemvArgs& a) {
   using L = VLayout<T>;
+  constexpr bool kOwn = T == 2;
   VShape sh;
   sh.m = int(a.m);
   sh.steps = int((a.k + 63) / 64);
   sh.stages = int((a.k + 255) / 256);
   sh.n = a.n;
+  sh.k = a.k;
   sh.k_tiles = (a.k + 127) / 128;
+  sh.ldx = a.ldx;
   const int64_t tiles = (a.n + kVM - 1) / kVM, t_tiles = (a.m + T - 1) / T;
   sh.split = gemv_split(tiles * t_tiles, sh.stages, L::kPerSm);
 
   CUtensorMap tm;
   if (!encode_rows_sw128(&tm, a.codes, a.n, a.k / 2, kVM)) return cudaErrorInvalidValue;
-  auto kern = k_gemv<T, BF16>;
+  auto kern = k_gemv<T, kOwn, BF16>;
   constexpr size_t smem = L::kBytes + 1024;
   cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-
-  const int64_t k64 = int64_t(sh.steps) * 64, threads = a.m * (k64 / 8);
-  k_gemv_digits<T><<<unsigned((threads + 255) / 256), 256, 0, a.s>>>(
-      a.x, a.ldx, int(a.m), a.k, k64, sh.stages, a.digits);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (!kOwn) {
+    const int64_t k64 = int64_t(sh.steps) * 64, threads = a.m * (k64 / 8);
+    k_gemv_digits<T><<<unsigned((threads + 255) / 256), 256, 0, a.s>>>(
+        a.x, a.ldx, int(a.m), a.k, k64, sh.stages, a.digits);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(tiles * sh.split), unsigned(t_tiles));
   cfg.blockDim = dim3(kVThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = a.s;
   cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = unsigned(sh.split);
-  at[1].val.clusterDim.y = 1;
-  at[1].val.clusterDim.z = 1;
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(sh.split);
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kern, tm, a.scales, static_cast<const uint8_t*>(a.digits), sh,
-                            a.y, a.status);
+  cfg.numAttrs = kOwn ? 1 : 2;
+  return cudaLaunchKernelEx(&cfg, kern, tm, a.scales, a.x,
+                            static_cast<const uint8_t*>(a.digits), sh, a.y, a.status);
 }
 
 template <bool BF16>
@@ -500,10 +569,9 @@ cudaError_t gemv_any(const GemvArgs& a) {
 
 int64_t gemv_workspace(int64_t m, int64_t, int64_t k) {
   const int T = gemv_tokens(m);
-  const int64_t block = T == 2    ? VLayout<2>::kX
-                        : T == 8  ? VLayout<8>::kX
-                        : T == 16 ? VLayout<16>::kX
-                                  : VLayout<32>::kX;
+  if (T == 2) return 0;
+  const int64_t block =
+      T == 8 ? VLayout<8>::kX : (T == 16 ? VLayout<16>::kX : VLayout<32>::kX);
   return (m + T - 1) / T * ((k + 255) / 256) * block;
 }
 
