@@ -50,7 +50,7 @@ struct NsArgs {
   const __half *c_hi, *c_lo;
   __half *d_hi, *d_lo;
   void* out;            // kLast: [m][n] of the caller's type
-  int out_bf16;
+  int out_bf16, out_vec;  // out_vec: rows of out are whole 16-byte vectors of 8
   float out_scale;
   int* status;
 };
@@ -295,67 +295,93 @@ __global__ void __launch_bounds__(kSThreads, 1)
     __syncwarp();
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
-    constexpr int kCols = BN / 2;  // columns of a warp
+    constexpr int kCols = BN / 2;  // columns of a warp, read 32 at a time
+    constexpr bool kHasC = MODE != kGram, kHasLo = MODE == kStep || MODE == kLast;
+    // C's share of 32 columns, loaded a round ahead (the first one before the
+    // products are done): one dependent load after the other took longer than
+    // the main loop of a narrow tile
+    struct Chunk {
+      uint4 hi[4], lo[4];
+    };
+    auto fetch = [&](Chunk& f, int64_t row, int64_t c0) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        // rows are padded to whole 16-byte chunks
+        const bool in = row < p.m && c0 + 8 * g < p.n;
+        if (kHasC && in) f.hi[g] = *reinterpret_cast<const uint4*>(p.c_hi + row * p.ldd + c0 + 8 * g);
+        if (kHasLo && in) f.lo[g] = *reinterpret_cast<const uint4*>(p.c_lo + row * p.ldd + c0 + 8 * g);
+      }
+    };
     int64_t ti = 0;
     for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x, ++ti) {
       int64_t m0, n0;
       ns_tile<BN, kSym>(t, mt, nt, m0, n0);
+      const int64_t row = m0 + 32 * q + lane;
+      Chunk cur, next;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) cur.hi[g] = cur.lo[g] = make_uint4(0, 0, 0, 0);
+      next = cur;
+      if constexpr (kHasC) fetch(cur, row, n0 + kCols * half);
       const uint32_t buf = uint32_t(ti & 1), bph = uint32_t(ti >> 1) & 1u;
       const bool ok = __all_sync(0xFFFFFFFFu, !failed_flag(failed) &&
                                                   wait_parity(&acc_full[buf], bph, kAccWaitLimit));
       if (!ok) atomicExch(failed, 1);
       asm volatile("tcgen05.fence::after_thread_sync;");
-      const int64_t row = m0 + 32 * q + lane;
       const uint32_t tb = tmem + buf * BN + (uint32_t(32 * q) << 16) + uint32_t(kCols * half);
 #pragma unroll 1
       for (int cb = 0; cb < kCols; cb += 32) {
         uint32_t v[32];
         MXFP4_TMEM_LD32(v, tb + cb);
+        const int64_t c0 = n0 + kCols * half + cb;
+        if constexpr (kHasC)
+          if (cb + 32 < kCols) fetch(next, row, c0 + 32);
         asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
         if (!ok || failed_flag(failed)) {
 #pragma unroll
           for (int j = 0; j < 32; ++j) v[j] = 0x7FC00000u;
         }
-        const int64_t c0 = n0 + kCols * half + cb;
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           const int64_t c = c0 + 8 * g;
-          if (row >= p.m || c >= p.n) break;
+          if (row >= p.m || c >= p.n) continue;
           float o[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) o[j] = __fmul_rn(p.alpha, __uint_as_float(v[8 * g + j]));
-          if constexpr (MODE != kGram) {
-            // rows are padded to whole 16-byte chunks
-            const uint4 h = *reinterpret_cast<const uint4*>(p.c_hi + row * p.ldd + c);
-            const uint32_t hw[4] = {h.x, h.y, h.z, h.w};
-            float cv[8];
+          if constexpr (kHasC) {
+            const uint32_t hw[4] = {cur.hi[g].x, cur.hi[g].y, cur.hi[g].z, cur.hi[g].w};
+            const uint32_t lw[4] = {cur.lo[g].x, cur.lo[g].y, cur.lo[g].z, cur.lo[g].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float2 f = unpack_h2(hw[j]);
-              cv[2 * j] = f.x, cv[2 * j + 1] = f.y;
-            }
-            if constexpr (MODE == kStep || MODE == kLast) {
-              const uint4 l = *reinterpret_cast<const uint4*>(p.c_lo + row * p.ldd + c);
-              const uint32_t lw[4] = {l.x, l.y, l.z, l.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float2 f = unpack_h2(lw[j]);
-                cv[2 * j] = __fadd_rn(cv[2 * j], f.x);
-                cv[2 * j + 1] = __fadd_rn(cv[2 * j + 1], f.y);
+              float2 f = unpack_h2(hw[j]);
+              if constexpr (kHasLo) {
+                const float2 l = unpack_h2(lw[j]);
+                f.x = __fadd_rn(f.x, l.x), f.y = __fadd_rn(f.y, l.y);
               }
+              o[2 * j] = __fmaf_rn(p.beta, f.x, o[2 * j]);
+              o[2 * j + 1] = __fmaf_rn(p.beta, f.y, o[2 * j + 1]);
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = __fmaf_rn(p.beta, cv[j], o[j]);
           }
           if constexpr (MODE == kLast) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              if (c + j >= p.n) break;
-              const float y = __fmul_rn(o[j], p.out_scale);
-              if (p.out_bf16)
-                static_cast<uint16_t*>(p.out)[row * p.n + c + j] = uint16_t(pack_bf16x2(y, 0.0f));
-              else
-                static_cast<float*>(p.out)[row * p.n + c + j] = y;
+            for (int j = 0; j < 8; ++j) o[j] = __fmul_rn(o[j], p.out_scale);
+            if (p.out_vec && p.out_bf16) {
+              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.n + c) =
+                  make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
+                             pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
+            } else if (p.out_vec) {
+              float4* to = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * p.n + c);
+              to[0] = make_float4(o[0], o[1], o[2], o[3]);
+              to[1] = make_float4(o[4], o[5], o[6], o[7]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                if (c + j >= p.n) break;
+                if (p.out_bf16)
+                  static_cast<uint16_t*>(p.out)[row * p.n + c + j] =
+                      uint16_t(pack_bf16x2(o[j], 0.0f));
+                else
+                  static_cast<float*>(p.out)[row * p.n + c + j] = o[j];
+              }
             }
           } else {
             uint32_t w[4];
@@ -389,6 +415,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
             }
           }
         }
+        cur = next;
         __syncwarp();
       }
       asm volatile("tcgen05.fence::before_thread_sync;");
@@ -476,12 +503,29 @@ __global__ void __launch_bounds__(256)
   __syncthreads();
   const float p = f[0], r = f[1];
   const int64_t chunks = (cols + 7) / 8;
+  const bool vec = cols % 8 == 0;  // g is 16-byte aligned
   for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < rows * chunks;
        i += int64_t(gridDim.x) * 256) {
     const int64_t row = i / chunks, c = i % chunks * 8;
     float v[8];
+    if (vec) {
+      if constexpr (BF16) {
+        const uint4 q = ld_stream(static_cast<const uint16_t*>(g) + row * cols + c);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = c + j < cols ? ns_load<BF16>(g, row * cols + c + j) : 0.0f;
+        for (int j = 0; j < 4; ++j) v[2 * j] = bf16_lo(w[j]), v[2 * j + 1] = bf16_hi(w[j]);
+      } else {
+        const float* at = static_cast<const float*>(g) + row * cols + c;
+        const uint4 q0 = ld_l1(at), q1 = ld_l1(at + 4);
+        const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        v[j] = c + j < cols ? ns_load<BF16>(g, row * cols + c + j) : 0.0f;
+    }
     uint32_t hw[4], lw[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -631,7 +675,7 @@ cudaError_t launch_newton_schulz(const void* g, bool bf16, int64_t rows, int64_t
     // X = a X + B X (a X + X B)
     p.m = rows, p.n = cols, p.k = s, p.ldd = ldx;
     p.alpha = kNsInv, p.beta = a, p.c_hi = xi, p.c_lo = xl, p.d_hi = x[(i + 1) & 1], p.d_lo = xl;
-    p.out = out, p.out_bf16 = out_bf16, p.out_scale = scale * kNsInv;
+    p.out = out, p.out_bf16 = out_bf16, p.out_vec = cols % 8 == 0, p.out_scale = scale * kNsInv;
     ox.mn = !tall;
     if (i + 1 < steps)
       e = tall ? ns_gemm<false, false, kStep>(ox, ob, p, st) : ns_gemm<false, true, kStep>(ob, ox, p, st);
