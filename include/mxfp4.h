@@ -459,8 +459,8 @@ int64_t mxfp4_newton_schulz_workspace(int64_t rows, int64_t cols);
  *   workspace  device, 256-byte aligned, workspace_bytes of scratch (at
  *            least mxfp4_newton_schulz_workspace); calls that run at the same
  *            time need workspaces of their own
- *   status   device int or NULL (MXFP4_STATUS_WAIT_TIMEOUT above); OUT holds
- *            NaN when it is set
+ *   status   device int or NULL (MXFP4_STATUS_WAIT_TIMEOUT above); when it is
+ *            set, the tiles of OUT that were not completed hold NaN
  * Any rows, cols up to MXFP4_NS_MAX_DIM. G of zeros gives zeros (eps > 0);
  * Inf or NaN in G gives NaN.
  */

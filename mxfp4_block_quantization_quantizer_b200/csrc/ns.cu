@@ -7,8 +7,8 @@
 //
 // Bound by the tensor cores: with s <= l the sides, a step costs s s l flops
 // for A (half of a symmetric product), s^3 for A A (half) and 2 s s l for
-// B X. Three launches a step, each a persistent tcgen05 GEMM with a fused
-// epilogue; only the tiles on and above the diagonal of A and B are computed
+// B X. Three products a step, each a persistent tcgen05 GEMM with a fused
+// epilogue (a launch each, or all in one launch for small matrices); only the tiles on and above the diagonal of A and B are computed
 // and written to both sides.
 //
 // Numbers: operands are fp16, not bf16, at the same tensor rate and with
@@ -37,7 +37,8 @@ constexpr float kNsScale = 4096.0f, kNsInv = 1.0f / 4096.0f;
 constexpr int kSM = 128;            // tile rows
 constexpr int kSK = 64;             // K elements of a stage: one swizzle row
 constexpr int kSEpiWarps = 8;
-constexpr int kSThreads = 32 * (2 + kSEpiWarps);
+constexpr int kSThreads = 32 * (3 + kSEpiWarps);  // A loads, MMA, epilogue, B loads
+constexpr int kSLoadB = 2 + kSEpiWarps;           // the warp of the B loads
 constexpr int kNsPartials = 592;    // partial sums of the norm
 
 // What a product's epilogue does.
@@ -62,7 +63,11 @@ struct NsLayout {
   static constexpr uint32_t kBOff = kStages * kA;
   static constexpr uint32_t kBarOff = kBOff + kStages * kB;
   static constexpr uint32_t kBytes = kBarOff + 256;
-  static constexpr uint32_t kTmemCols = 2 * BN;
+  // Accumulators of a tile: consecutive MMAs on one wait for each other, about
+  // 150 clocks, which 128 x 256 products cover and narrower ones do not; the
+  // four MMAs of a stage take turns, and the epilogue adds. Two tiles' worth.
+  static constexpr int kAcc = 256 / BN;
+  static constexpr uint32_t kTmemCols = 512;
   // kind::f16: fp32 accumulator, fp16 operands (0), majorness bits 15, 16
   __host__ __device__ static constexpr uint32_t idesc(bool a_mn, bool b_mn) {
     return (1u << 4) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
@@ -164,6 +169,274 @@ __device__ __forceinline__ float2 unpack_h2(uint32_t w) {
         "=r"(d[31])                                                                            \
       : "r"(addr))
 
+// Lane l of a warp holds row l of a 32 x 32 tile in v[0..31]; afterwards it
+// holds column l.
+__device__ __forceinline__ void transpose32(float* v, int lane) {
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) {
+    const bool up = (lane & s) != 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+      if (j & s) continue;
+      const float give = up ? v[j] : v[j + s];
+      const float got = __shfl_xor_sync(0xFFFFFFFFu, give, s);
+      if (up)
+        v[j] = got;
+      else
+        v[j + s] = got;
+    }
+  }
+}
+
+// The epilogue of one warp for its row (lane) and the BN / 2 columns from n0
+// on, in rounds of 32: waits for the products, reads them from tensor memory
+// at `tb` and stores D. Returns false (and stores NaN) if the wait ran out.
+template <int BN, int MODE>
+__device__ __forceinline__ bool ns_epilogue(const NsArgs& p, int64_t row, int64_t n0, uint32_t tb,
+                                            unsigned long long* acc_full, uint32_t phase,
+                                            int* failed) {
+  constexpr bool kSym = MODE == kGram || MODE == kSquare;
+  constexpr int kCols = BN / 2;
+  constexpr bool kHasC = MODE != kGram, kHasLo = MODE == kStep || MODE == kLast;
+  // C's share of 32 columns, loaded a round ahead (the first one before the
+  // products are done): one dependent load after the other took longer than
+  // the main loop of a narrow tile
+  struct Chunk {
+    uint4 hi[4], lo[4];
+  };
+  // (from L2: in the fused kernel other SMs rewrite these buffers)
+  auto fetch = [&](Chunk& f, int64_t c0) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      // rows are padded to whole 16-byte chunks
+      const bool in = row < p.m && c0 + 8 * g < p.n;
+      if (kHasC && in) f.hi[g] = __ldcg(reinterpret_cast<const uint4*>(p.c_hi + row * p.ldd + c0 + 8 * g));
+      if (kHasLo && in) f.lo[g] = __ldcg(reinterpret_cast<const uint4*>(p.c_lo + row * p.ldd + c0 + 8 * g));
+    }
+  };
+  Chunk cur, next;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) cur.hi[g] = cur.lo[g] = make_uint4(0, 0, 0, 0);
+  next = cur;
+  if constexpr (kHasC) fetch(cur, n0);
+  const bool ok = __all_sync(0xFFFFFFFFu, !failed_flag(failed) &&
+                                              wait_parity(acc_full, phase, kAccWaitLimit));
+  if (!ok) atomicExch(failed, 1);
+  asm volatile("tcgen05.fence::after_thread_sync;");
+#pragma unroll 1
+  for (int cb = 0; cb < kCols; cb += 32) {
+    uint32_t v[32];
+    MXFP4_TMEM_LD32(v, tb + cb);
+    const int64_t c0 = n0 + cb;
+    if constexpr (kHasC)
+      if (cb + 32 < kCols) fetch(next, c0 + 32);
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int a = 1; a < NsLayout<BN>::kAcc; ++a) {
+      uint32_t u[32];
+      MXFP4_TMEM_LD32(u, tb + cb + a * BN);
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        v[j] = __float_as_uint(__fadd_rn(__uint_as_float(v[j]), __uint_as_float(u[j])));
+    }
+    if (!ok || failed_flag(failed)) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = 0x7FC00000u;
+    }
+    float o[32];
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        o[8 * g + j] = __fmul_rn(p.alpha, __uint_as_float(v[8 * g + j]));
+      if constexpr (kHasC) {
+        const uint32_t hw[4] = {cur.hi[g].x, cur.hi[g].y, cur.hi[g].z, cur.hi[g].w};
+        const uint32_t lw[4] = {cur.lo[g].x, cur.lo[g].y, cur.lo[g].z, cur.lo[g].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float2 f = unpack_h2(hw[j]);
+          if constexpr (kHasLo) {
+            const float2 l = unpack_h2(lw[j]);
+            f.x = __fadd_rn(f.x, l.x), f.y = __fadd_rn(f.y, l.y);
+          }
+          o[8 * g + 2 * j] = __fmaf_rn(p.beta, f.x, o[8 * g + 2 * j]);
+          o[8 * g + 2 * j + 1] = __fmaf_rn(p.beta, f.y, o[8 * g + 2 * j + 1]);
+        }
+      }
+    }
+    if constexpr (MODE == kLast) {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = __fmul_rn(o[j], p.out_scale);
+      if (p.out_vec) {
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int64_t c = c0 + 8 * g;
+          const float* e = o + 8 * g;
+          if (row >= p.m || c >= p.n) continue;
+          if (p.out_bf16) {
+            *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.n + c) =
+                make_uint4(pack_bf16x2(e[0], e[1]), pack_bf16x2(e[2], e[3]),
+                           pack_bf16x2(e[4], e[5]), pack_bf16x2(e[6], e[7]));
+          } else {
+            float4* to = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * p.n + c);
+            to[0] = make_float4(e[0], e[1], e[2], e[3]);
+            to[1] = make_float4(e[4], e[5], e[6], e[7]);
+          }
+        }
+      } else {
+        // rows off a 16-byte boundary: a lane takes a column, so that a warp
+        // stores 32 neighbours at a time
+        const int lane = threadIdx.x & 31;
+        transpose32(o, lane);
+        const int64_t c = c0 + lane, r0 = row - lane;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+          if (r0 + j >= p.m || c >= p.n) continue;
+          if (p.out_bf16)
+            static_cast<uint16_t*>(p.out)[(r0 + j) * p.n + c] = uint16_t(pack_bf16x2(o[j], 0.0f));
+          else
+            static_cast<float*>(p.out)[(r0 + j) * p.n + c] = o[j];
+        }
+      }
+    } else {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int64_t c = c0 + 8 * g;
+        const float* e = o + 8 * g;
+        if (row >= p.m || c >= p.n) continue;
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = pack_h2(e[2 * j], e[2 * j + 1]);
+        if constexpr (kSym) {
+          // each entry of the symmetric result has one writer: the element on
+          // or above the diagonal, for both sides
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const __half hv = __ushort_as_half(uint16_t(w[j / 2] >> (16 * (j & 1))));
+            if (c + j >= row && c + j < p.n) {
+              p.d_hi[(c + j) * p.ldd + row] = hv;
+              if (c < row) p.d_hi[row * p.ldd + c + j] = hv;
+            }
+          }
+          if (c >= row)
+            *reinterpret_cast<uint4*>(p.d_hi + row * p.ldd + c) =
+                make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+          *reinterpret_cast<uint4*>(p.d_hi + row * p.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
+          uint32_t lw[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 f = unpack_h2(w[j]);
+            lw[j] = pack_h2(__fsub_rn(e[2 * j], f.x), __fsub_rn(e[2 * j + 1], f.y));
+          }
+          *reinterpret_cast<uint4*>(p.d_lo + row * p.ldd + c) =
+              make_uint4(lw[0], lw[1], lw[2], lw[3]);
+        }
+      }
+    }
+    cur = next;
+    __syncwarp();
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;");
+  __syncwarp();
+  return ok;
+}
+
+// The thread that loads one operand (A: 128 rows, B: BN) into the ring, tile
+// after tile. A box holds 64 columns; K-major operands come as one box of all
+// rows, MN-major ones as a box of 64 k rows for every 64 of the tile's rows.
+// (One thread for both operands took 0.3 us a stage of narrow tiles, twice
+// what their MMAs take.)
+template <int BN>
+struct NsLoader {
+  using L = NsLayout<BN>;
+  uint8_t* base;
+  unsigned long long *full, *empty;
+  const int* failed;
+  uint32_t bytes, s = 0, ph = 0, issued = 0, last_ph = 0;
+  __device__ NsLoader(uint8_t* sm, unsigned long long* full_, unsigned long long* empty_, bool a,
+                      const int* failed_)
+      : base(a ? sm : sm + L::kBOff), full(full_), empty(empty_), failed(failed_),
+        bytes(a ? L::kA : L::kB) {}
+  __device__ bool tile(const CUtensorMap* map, bool mn, int row0, int64_t n_kb) {
+    const int boxes = mn ? int(bytes / 8192) : 1;
+    for (int64_t kb = 0; kb < n_kb; ++kb) {
+      if (!wait_parity_or_failed<false>(&empty[s], ph ^ 1u, failed)) {
+        atomicExch(const_cast<int*>(failed), 1);
+        return false;
+      }
+      issued |= 1u << s;
+      last_ph = (last_ph & ~(1u << s)) | (ph << s);
+      uint8_t* to = base + s * bytes;
+      const int k0 = int(kb) * kSK;
+      expect_tx(&full[s], bytes);
+      if (mn) {
+        for (int j = 0; j < boxes; ++j)
+          tma_load_2d(to + j * 8192, map, row0 + 64 * j, k0, &full[s]);
+      } else {
+        tma_load_2d(to, map, k0, row0, &full[s]);
+      }
+      if (++s == L::kStages) s = 0, ph ^= 1u;
+    }
+    return !failed_flag(failed);
+  }
+  // every load has landed (both operands': the phase completes with them)
+  __device__ void drain() {
+    for (uint32_t st = 0; st < L::kStages; ++st)
+      if ((issued >> st) & 1u) wait_parity(&full[st], (last_ph >> st) & 1u);
+  }
+};
+
+// The thread that issues the MMAs, tile after tile into the two accumulators
+// in turn. Its work per stage is kept small: descriptors advance by additions.
+template <int BN>
+struct NsIssuer {
+  using L = NsLayout<BN>;
+  uint8_t* sm;
+  unsigned long long *full, *empty;
+  uint32_t tmem;
+  const int* failed;
+  uint64_t a0, b0, ad, bd;
+  uint32_t ka, kb_, idesc, s = 0, ph = 0, ti = 0;
+  __device__ NsIssuer(uint8_t* sm_, unsigned long long* full_, unsigned long long* empty_,
+                      uint32_t tmem_, const int* failed_)
+      : sm(sm_), full(full_), empty(empty_), tmem(tmem_), failed(failed_) {}
+  // majorness of the operands of the tiles that follow
+  __device__ void operands(bool a_mn, bool b_mn) {
+    a0 = a_mn ? smem_desc_mn(sm) : smem_desc_sw128(sm);
+    b0 = b_mn ? smem_desc_mn(sm + L::kBOff) : smem_desc_sw128(sm + L::kBOff);
+    ad = a0 + s * (L::kA >> 4), bd = b0 + s * (L::kB >> 4);
+    ka = a_mn ? 128u : 2u, kb_ = b_mn ? 128u : 2u;
+    idesc = L::idesc(a_mn, b_mn);
+  }
+  __device__ bool tile(int64_t n_kb, unsigned long long* acc_full, unsigned long long* acc_empty) {
+    const uint32_t buf = ti & 1, bph = (ti >> 1) & 1u;
+    if (!wait_parity_or_failed<false>(&acc_empty[buf], bph ^ 1u, failed) || failed_flag(failed))
+      return false;
+    asm volatile("tcgen05.fence::after_thread_sync;");
+    const uint32_t acc = tmem + buf * 256;
+    bool ok = true;
+    for (int64_t kb = 0; kb < n_kb; ++kb) {
+      if (!wait_parity_or_failed<false>(&full[s], ph, failed)) {
+        ok = false;
+        break;
+      }
+      asm volatile("tcgen05.fence::after_thread_sync;");
+#pragma unroll
+      for (uint32_t j = 0; j < kSK / 16; ++j)
+        mma_f16(acc + (j % L::kAcc) * BN, ad + j * ka, bd + j * kb_, idesc,
+                (kb > 0 || j >= L::kAcc) ? 1u : 0u);
+      commit_to(&empty[s]);
+      ad += L::kA >> 4, bd += L::kB >> 4;
+      if (++s == L::kStages) s = 0, ph ^= 1u, ad = a0, bd = b0;
+    }
+    commit_to(&acc_full[buf]);
+    ++ti;
+    return ok;
+  }
+};
+
 template <int BN, bool A_MN, bool B_MN, int MODE>
 __global__ void __launch_bounds__(kSThreads, 1)
     k_ns_gemm(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
@@ -186,7 +459,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
 
   if (tid == 0) {
     for (int s = 0; s < L::kStages; ++s) {
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&full[s])));
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 2;" ::"r"(smem_u32(&full[s])));
       asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&empty[s])));
     }
     for (int s = 0; s < 2; ++s) {
@@ -213,213 +486,41 @@ __global__ void __launch_bounds__(kSThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  if (warp == 0) {
+  if (warp == 0 || warp == kSLoadB) {
     if (lane == 0) {
-      uint32_t s = 0, ph = 0, issued = 0, last_ph = 0;
+      NsLoader<BN> ld(sm, full, empty, warp == 0, failed);
+      const bool mn = warp == 0 ? A_MN : B_MN;
       for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x) {
         int64_t m0, n0;
         ns_tile<BN, kSym>(t, mt, nt, m0, n0);
-        bool stop = false;
-        for (int64_t kb = 0; kb < n_kb; ++kb) {
-          if (!wait_parity_or_failed<false>(&empty[s], ph ^ 1u, failed)) {
-            atomicExch(failed, 1);
-            stop = true;
-            break;
-          }
-          issued |= 1u << s;
-          last_ph = (last_ph & ~(1u << s)) | (ph << s);
-          uint8_t* a = sm + s * L::kA;
-          uint8_t* b = sm + L::kBOff + s * L::kB;
-          const int k0 = int(kb) * kSK;
-          expect_tx(&full[s], L::kA + L::kB);
-          if constexpr (A_MN) {
-#pragma unroll
-            for (int j = 0; j < kSM / 64; ++j)
-              tma_load_2d(a + j * 8192, &tm_a, int(m0) + 64 * j, k0, &full[s]);
-          } else {
-            tma_load_2d(a, &tm_a, k0, int(m0), &full[s]);
-          }
-          if constexpr (B_MN) {
-#pragma unroll
-            for (int j = 0; j < BN / 64; ++j)
-              tma_load_2d(b + j * 8192, &tm_b, int(n0) + 64 * j, k0, &full[s]);
-          } else {
-            tma_load_2d(b, &tm_b, k0, int(n0), &full[s]);
-          }
-          if (++s == L::kStages) s = 0, ph ^= 1u;
-        }
-        if (stop || failed_flag(failed)) break;
+        if (!ld.tile(warp == 0 ? &tm_a : &tm_b, mn, int(warp == 0 ? m0 : n0), n_kb)) break;
       }
-      for (uint32_t st = 0; st < L::kStages; ++st)
-        if ((issued >> st) & 1u) wait_parity(&full[st], (last_ph >> st) & 1u);
+      ld.drain();
     }
     __syncwarp();
   } else if (warp == 1) {
     if (lane == 0) {
-      uint32_t s = 0, ph = 0;
-      int64_t ti = 0;
-      for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x, ++ti) {
-        const uint32_t buf = uint32_t(ti & 1), bph = uint32_t(ti >> 1) & 1u;
-        if (!wait_parity_or_failed<false>(&acc_empty[buf], bph ^ 1u, failed) ||
-            failed_flag(failed)) {
-          atomicExch(failed, 1);
-          break;
-        }
-        asm volatile("tcgen05.fence::after_thread_sync;");
-        const uint32_t acc = tmem + buf * BN;
-        bool ok = true;
-        for (int64_t kb = 0; kb < n_kb; ++kb) {
-          if (!wait_parity_or_failed<false>(&full[s], ph, failed)) {
-            ok = false;
-            break;
-          }
-          asm volatile("tcgen05.fence::after_thread_sync;");
-          const uint8_t* a = sm + s * L::kA;
-          const uint8_t* b = sm + L::kBOff + s * L::kB;
-          const uint64_t ad = A_MN ? smem_desc_mn(a) : smem_desc_sw128(a);
-          const uint64_t bd = B_MN ? smem_desc_mn(b) : smem_desc_sw128(b);
-#pragma unroll
-          for (uint32_t j = 0; j < kSK / 16; ++j)
-            mma_f16(acc, ad + j * (A_MN ? 128u : 2u), bd + j * (B_MN ? 128u : 2u),
-                    L::idesc(A_MN, B_MN), (kb > 0 || j > 0) ? 1u : 0u);
-          commit_to(&empty[s]);
-          if (++s == L::kStages) s = 0, ph ^= 1u;
-        }
-        if (!ok) atomicExch(failed, 1);
-        commit_to(&acc_full[buf]);
-        if (!ok) break;
-      }
+      NsIssuer<BN> mma(sm, full, empty, tmem, failed);
+      mma.operands(A_MN, B_MN);
+      bool ok = true;
+      for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x)
+        ok = mma.tile(n_kb, acc_full, acc_empty);
+      if (!ok) atomicExch(failed, 1);
       commit_to(drain);
       if (!wait_parity(drain, 0)) atomicExch(failed, 1);
     }
     __syncwarp();
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
-    constexpr int kCols = BN / 2;  // columns of a warp, read 32 at a time
-    constexpr bool kHasC = MODE != kGram, kHasLo = MODE == kStep || MODE == kLast;
-    // C's share of 32 columns, loaded a round ahead (the first one before the
-    // products are done): one dependent load after the other took longer than
-    // the main loop of a narrow tile
-    struct Chunk {
-      uint4 hi[4], lo[4];
-    };
-    auto fetch = [&](Chunk& f, int64_t row, int64_t c0) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        // rows are padded to whole 16-byte chunks
-        const bool in = row < p.m && c0 + 8 * g < p.n;
-        if (kHasC && in) f.hi[g] = *reinterpret_cast<const uint4*>(p.c_hi + row * p.ldd + c0 + 8 * g);
-        if (kHasLo && in) f.lo[g] = *reinterpret_cast<const uint4*>(p.c_lo + row * p.ldd + c0 + 8 * g);
-      }
-    };
     int64_t ti = 0;
     for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x, ++ti) {
       int64_t m0, n0;
       ns_tile<BN, kSym>(t, mt, nt, m0, n0);
-      const int64_t row = m0 + 32 * q + lane;
-      Chunk cur, next;
-#pragma unroll
-      for (int g = 0; g < 4; ++g) cur.hi[g] = cur.lo[g] = make_uint4(0, 0, 0, 0);
-      next = cur;
-      if constexpr (kHasC) fetch(cur, row, n0 + kCols * half);
       const uint32_t buf = uint32_t(ti & 1), bph = uint32_t(ti >> 1) & 1u;
-      const bool ok = __all_sync(0xFFFFFFFFu, !failed_flag(failed) &&
-                                                  wait_parity(&acc_full[buf], bph, kAccWaitLimit));
-      if (!ok) atomicExch(failed, 1);
-      asm volatile("tcgen05.fence::after_thread_sync;");
-      const uint32_t tb = tmem + buf * BN + (uint32_t(32 * q) << 16) + uint32_t(kCols * half);
-#pragma unroll 1
-      for (int cb = 0; cb < kCols; cb += 32) {
-        uint32_t v[32];
-        MXFP4_TMEM_LD32(v, tb + cb);
-        const int64_t c0 = n0 + kCols * half + cb;
-        if constexpr (kHasC)
-          if (cb + 32 < kCols) fetch(next, row, c0 + 32);
-        asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-        if (!ok || failed_flag(failed)) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = 0x7FC00000u;
-        }
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int64_t c = c0 + 8 * g;
-          if (row >= p.m || c >= p.n) continue;
-          float o[8];
-#pragma unroll
-          for (int j = 0; j < 8; ++j) o[j] = __fmul_rn(p.alpha, __uint_as_float(v[8 * g + j]));
-          if constexpr (kHasC) {
-            const uint32_t hw[4] = {cur.hi[g].x, cur.hi[g].y, cur.hi[g].z, cur.hi[g].w};
-            const uint32_t lw[4] = {cur.lo[g].x, cur.lo[g].y, cur.lo[g].z, cur.lo[g].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              float2 f = unpack_h2(hw[j]);
-              if constexpr (kHasLo) {
-                const float2 l = unpack_h2(lw[j]);
-                f.x = __fadd_rn(f.x, l.x), f.y = __fadd_rn(f.y, l.y);
-              }
-              o[2 * j] = __fmaf_rn(p.beta, f.x, o[2 * j]);
-              o[2 * j + 1] = __fmaf_rn(p.beta, f.y, o[2 * j + 1]);
-            }
-          }
-          if constexpr (MODE == kLast) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) o[j] = __fmul_rn(o[j], p.out_scale);
-            if (p.out_vec && p.out_bf16) {
-              *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) + row * p.n + c) =
-                  make_uint4(pack_bf16x2(o[0], o[1]), pack_bf16x2(o[2], o[3]),
-                             pack_bf16x2(o[4], o[5]), pack_bf16x2(o[6], o[7]));
-            } else if (p.out_vec) {
-              float4* to = reinterpret_cast<float4*>(static_cast<float*>(p.out) + row * p.n + c);
-              to[0] = make_float4(o[0], o[1], o[2], o[3]);
-              to[1] = make_float4(o[4], o[5], o[6], o[7]);
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                if (c + j >= p.n) break;
-                if (p.out_bf16)
-                  static_cast<uint16_t*>(p.out)[row * p.n + c + j] =
-                      uint16_t(pack_bf16x2(o[j], 0.0f));
-                else
-                  static_cast<float*>(p.out)[row * p.n + c + j] = o[j];
-              }
-            }
-          } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) w[j] = pack_h2(o[2 * j], o[2 * j + 1]);
-            if constexpr (kSym) {
-              // each entry of the symmetric result has one writer: the
-              // element on or above the diagonal, for both sides
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const __half hv = __ushort_as_half(uint16_t(w[j / 2] >> (16 * (j & 1))));
-                if (c + j >= row && c + j < p.n) {
-                  p.d_hi[(c + j) * p.ldd + row] = hv;
-                  if (c < row) p.d_hi[row * p.ldd + c + j] = hv;
-                }
-              }
-              if (c >= row)
-                *reinterpret_cast<uint4*>(p.d_hi + row * p.ldd + c) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-              *reinterpret_cast<uint4*>(p.d_hi + row * p.ldd + c) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-              uint32_t lw[4];
-#pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                const float2 f = unpack_h2(w[j]);
-                lw[j] = pack_h2(__fsub_rn(o[2 * j], f.x), __fsub_rn(o[2 * j + 1], f.y));
-              }
-              *reinterpret_cast<uint4*>(p.d_lo + row * p.ldd + c) =
-                  make_uint4(lw[0], lw[1], lw[2], lw[3]);
-            }
-          }
-        }
-        cur = next;
-        __syncwarp();
-      }
-      asm volatile("tcgen05.fence::before_thread_sync;");
-      __syncwarp();
+      const bool ok = ns_epilogue<BN, MODE>(p, m0 + 32 * q + lane, n0 + (BN / 2) * half,
+                                            tmem + buf * 256 + (uint32_t(32 * q) << 16) +
+                                                uint32_t((BN / 2) * half),
+                                            &acc_full[buf], bph, failed);
       if (ok && lane == 0)
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&acc_empty[buf]))
                      : "memory");
@@ -441,7 +542,9 @@ __device__ __forceinline__ float ns_load(const void* g, int64_t i) {
 }
 template <bool BF16>
 __global__ void __launch_bounds__(256)
-    k_ns_norm(const void* __restrict__ g, int64_t n, double* __restrict__ partial) {
+    k_ns_norm(const void* __restrict__ g, int64_t n, double* __restrict__ partial,
+              unsigned* __restrict__ counter) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
   constexpr int VEC = BF16 ? 8 : 4;
   __shared__ double sh[8];
   double s = 0.0;
@@ -475,16 +578,15 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// X = 2^12 G / (|G|_F + eps) as hi + lo, pitch ld. Every CTA adds the
-// partial sums itself, in one order.
+// X = 2^12 G / (|G|_F + eps) as hi + lo, pitch ld, by all threads of the
+// grid. Every CTA adds the partial sums itself, in one order; f: two floats
+// of shared memory.
 template <bool BF16>
-__global__ void __launch_bounds__(256)
-    k_ns_start(const void* __restrict__ g, int64_t rows, int64_t cols, int64_t ld, float eps,
-               const double* __restrict__ partial, int n_partial, __half* __restrict__ hi,
-               __half* __restrict__ lo) {
-  __shared__ float f[2];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+__device__ __forceinline__ void ns_start(const void* __restrict__ g, int64_t rows, int64_t cols,
+                                         int64_t ld, float eps,
+                                         const double* __restrict__ partial, int n_partial,
+                                         __half* __restrict__ hi, __half* __restrict__ lo,
+                                         float* f) {
   if (threadIdx.x < 32) {
     double s = 0.0;
     for (int i = threadIdx.x; i < n_partial; i += 32) s += partial[i];
@@ -504,8 +606,8 @@ __global__ void __launch_bounds__(256)
   const float p = f[0], r = f[1];
   const int64_t chunks = (cols + 7) / 8;
   const bool vec = cols % 8 == 0;  // g is 16-byte aligned
-  for (int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x; i < rows * chunks;
-       i += int64_t(gridDim.x) * 256) {
+  for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < rows * chunks;
+       i += int64_t(gridDim.x) * blockDim.x) {
     const int64_t row = i / chunks, c = i % chunks * 8;
     float v[8];
     if (vec) {
@@ -538,6 +640,255 @@ __global__ void __launch_bounds__(256)
     *reinterpret_cast<uint4*>(hi + row * ld + c) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
     *reinterpret_cast<uint4*>(lo + row * ld + c) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
   }
+}
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+    k_ns_start(const void* __restrict__ g, int64_t rows, int64_t cols, int64_t ld, float eps,
+               const double* __restrict__ partial, int n_partial, __half* __restrict__ hi,
+               __half* __restrict__ lo) {
+  __shared__ float f[2];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  ns_start<BF16>(g, rows, cols, ld, eps, partial, n_partial, hi, lo, f);
+}
+
+// ---------------------------------------------------------------------------
+// All steps in one cooperative launch, for matrices whose products are too
+// short for a launch each: the same roles and tiles as k_ns_gemm, but the
+// pipeline runs on from product to product, with a barrier over the grid
+// between them (a counter in the workspace, zeroed by k_ns_norm) in place of
+// the end of one launch and the start of the next. The thread that loads and
+// the epilogue warps wait at it; what other CTAs stored is then read through
+// the asynchronous proxy, hence the fence on both sides.
+// ---------------------------------------------------------------------------
+
+// Tensor maps with boxes of 64 columns x 64 rows, kSM rows (K-major A) and BN
+// rows (K-major B).
+struct NsMaps {
+  CUtensorMap x_mn[2], x_a[2], ga_a, ga_b, gb_a, gb_b, x_b[2];
+};
+struct NsRun {
+  const void* g;
+  int64_t rows, cols, ldx, lds;
+  int steps, n_partial;
+  float a, b, c, eps;
+  const double* partial;
+  unsigned* counter;
+  __half *x[2], *xl, *ga, *gb;
+  void* out;
+  int out_bf16, out_vec;
+  float out_scale;
+  int* status;
+};
+
+// Product `i` of step i / 3: its shape, epilogue arguments and operands.
+struct NsPhase {
+  NsArgs p;
+  const CUtensorMap *ta, *tb;
+  bool a_mn, b_mn, sym;
+  int mode;
+};
+__device__ __forceinline__ NsPhase ns_phase(const NsRun& r, const NsMaps& maps, int i) {
+  const bool tall = r.rows > r.cols;
+  const int64_t s = tall ? r.cols : r.rows;
+  const int step = i / 3, cur = step & 1;
+  NsPhase f = {};
+  f.p.status = r.status;
+  f.mode = i % 3;
+  f.sym = f.mode != 2;
+  if (f.mode == 0) {
+    f.p.m = f.p.n = s, f.p.k = tall ? r.rows : r.cols, f.p.ldd = r.lds;
+    f.p.alpha = kNsInv, f.p.d_hi = r.ga;
+    f.ta = tall ? &maps.x_mn[cur] : &maps.x_a[cur];
+    f.tb = tall ? &maps.x_mn[cur] : &maps.x_b[cur];
+    f.a_mn = f.b_mn = tall;
+  } else if (f.mode == 1) {
+    f.p.m = f.p.n = f.p.k = s, f.p.ldd = r.lds;
+    f.p.alpha = __fmul_rn(r.c, kNsInv), f.p.beta = r.b, f.p.c_hi = r.ga, f.p.d_hi = r.gb;
+    f.ta = &maps.ga_a, f.tb = &maps.ga_b;
+  } else {
+    f.p.m = r.rows, f.p.n = r.cols, f.p.k = s, f.p.ldd = r.ldx;
+    f.p.alpha = kNsInv, f.p.beta = r.a, f.p.c_hi = r.x[cur], f.p.c_lo = r.xl;
+    f.p.d_hi = r.x[cur ^ 1], f.p.d_lo = r.xl;
+    f.p.out = r.out, f.p.out_bf16 = r.out_bf16, f.p.out_vec = r.out_vec;
+    f.p.out_scale = r.out_scale;
+    f.ta = tall ? &maps.x_a[cur] : &maps.gb_a;
+    f.tb = tall ? &maps.gb_b : &maps.x_mn[cur];
+    f.b_mn = !tall;
+    if (step + 1 == r.steps) f.mode = 3;
+  }
+  return f;
+}
+
+// Waits until `target` CTA arrivals are counted (bounded). A CTA that gave up
+// sets the counter's bit 30: every later wait of every CTA then fails too, so
+// nothing is computed from what that CTA did not finish.
+constexpr unsigned kNsGaveUp = 1u << 30;
+__device__ __forceinline__ bool ns_grid_wait(const unsigned* counter, unsigned target,
+                                             const int* failed) {
+  for (int i = 0; i < (1 << 21); ++i) {
+    unsigned v;
+    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
+    if (v >= target) return (v & kNsGaveUp) == 0;
+    if ((i & 255) == 255) {
+      if (failed_flag(failed)) return false;
+      __nanosleep(64);
+    }
+  }
+  return false;
+}
+__device__ __forceinline__ void ns_grid_arrive(unsigned* counter) {
+  __threadfence();
+  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(counter) : "memory");
+}
+
+template <int BN, bool BF16>
+__global__ void __launch_bounds__(kSThreads, 1)
+    k_ns_fused(const __grid_constant__ NsMaps maps, const __grid_constant__ NsRun r) {
+  using L = NsLayout<BN>;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned long long* full = reinterpret_cast<unsigned long long*>(sm + L::kBarOff);
+  unsigned long long* empty = full + L::kStages;
+  unsigned long long* acc_full = empty + L::kStages;  // two accumulators
+  unsigned long long* acc_empty = acc_full + 2;
+  unsigned long long* drain = acc_empty + 2;
+  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drain + 1);
+  int* failed = reinterpret_cast<int*>(tmem_base + 1);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int phases = 3 * r.steps;
+  auto tiles_of = [&](const NsPhase& f, int64_t& mt, int64_t& nt) {
+    mt = (f.p.m + kSM - 1) / kSM, nt = (f.p.n + BN - 1) / BN;
+    return ns_tiles<BN>(f.sym, mt, nt);
+  };
+  auto tile_of = [&](const NsPhase& f, int64_t t, int64_t mt, int64_t nt, int64_t& m0,
+                     int64_t& n0) {
+    if (f.sym)
+      ns_tile<BN, true>(t, mt, nt, m0, n0);
+    else
+      ns_tile<BN, false>(t, mt, nt, m0, n0);
+  };
+
+  if (tid == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 2;" ::"r"(smem_u32(&full[s])));
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&empty[s])));
+    }
+    for (int s = 0; s < 2; ++s) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&acc_full[s])));
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&acc_empty[s])),
+                   "r"(kSEpiWarps));
+    }
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(drain)));
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    *failed = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_base)),
+                 "r"(L::kTmemCols));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  ns_start<BF16>(r.g, r.rows, r.cols, r.ldx, r.eps, r.partial, r.n_partial, r.x[0], r.xl,
+                 reinterpret_cast<float*>(sm));
+  asm volatile("tcgen05.fence::before_thread_sync;");
+  asm volatile("fence.proxy.async;" ::: "memory");
+  __syncthreads();
+  asm volatile("tcgen05.fence::after_thread_sync;");
+  const uint32_t tmem = *tmem_base;
+  if (tid == 0) ns_grid_arrive(r.counter);
+
+  if (warp == 0 || warp == kSLoadB) {
+    if (lane == 0) {
+      NsLoader<BN> ld(sm, full, empty, warp == 0, failed);
+      bool ok = true;
+      for (int i = 0; i < phases && ok; ++i) {
+        const NsPhase f = ns_phase(r, maps, i);
+        int64_t mt, nt;
+        const int64_t n_tiles = tiles_of(f, mt, nt), n_kb = (f.p.k + kSK - 1) / kSK;
+        if (!ns_grid_wait(r.counter, gridDim.x * unsigned(i + 1), failed)) {
+          atomicExch(failed, 1);
+          break;
+        }
+        asm volatile("fence.proxy.async;" ::: "memory");
+        for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
+          int64_t m0, n0;
+          tile_of(f, t, mt, nt, m0, n0);
+          ok = ld.tile(warp == 0 ? f.ta : f.tb, warp == 0 ? f.a_mn : f.b_mn,
+                       int(warp == 0 ? m0 : n0), n_kb);
+        }
+      }
+      ld.drain();
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (lane == 0) {
+      NsIssuer<BN> mma(sm, full, empty, tmem, failed);
+      bool ok = true;
+      for (int i = 0; i < phases && ok; ++i) {
+        const NsPhase f = ns_phase(r, maps, i);
+        int64_t mt, nt;
+        const int64_t n_tiles = tiles_of(f, mt, nt), n_kb = (f.p.k + kSK - 1) / kSK;
+        mma.operands(f.a_mn, f.b_mn);
+        for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x)
+          ok = mma.tile(n_kb, acc_full, acc_empty);
+      }
+      if (!ok) atomicExch(failed, 1);
+      commit_to(drain);
+      if (!wait_parity(drain, 0)) atomicExch(failed, 1);
+    }
+    __syncwarp();
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    int64_t ti = 0;
+    for (int i = 0; i < phases; ++i) {
+      const NsPhase f = ns_phase(r, maps, i);
+      int64_t mt, nt;
+      const int64_t n_tiles = tiles_of(f, mt, nt);
+      // (after a failure nothing is waited for: NaN is stored and the others
+      // are not held up)
+      if (lane == 0 && !failed_flag(failed) &&
+          !ns_grid_wait(r.counter, gridDim.x * unsigned(i + 1), failed))
+        atomicExch(failed, 1);
+      __syncwarp();
+      for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x, ++ti) {
+        int64_t m0, n0;
+        tile_of(f, t, mt, nt, m0, n0);
+        const uint32_t buf = uint32_t(ti & 1), bph = uint32_t(ti >> 1) & 1u;
+        const int64_t row = m0 + 32 * q + lane, c0 = n0 + (BN / 2) * half;
+        const uint32_t tb =
+            tmem + buf * 256 + (uint32_t(32 * q) << 16) + uint32_t((BN / 2) * half);
+        bool ok;
+        if (f.mode == kGram)
+          ok = ns_epilogue<BN, kGram>(f.p, row, c0, tb, &acc_full[buf], bph, failed);
+        else if (f.mode == kSquare)
+          ok = ns_epilogue<BN, kSquare>(f.p, row, c0, tb, &acc_full[buf], bph, failed);
+        else if (f.mode == kStep)
+          ok = ns_epilogue<BN, kStep>(f.p, row, c0, tb, &acc_full[buf], bph, failed);
+        else
+          ok = ns_epilogue<BN, kLast>(f.p, row, c0, tb, &acc_full[buf], bph, failed);
+        if (ok && lane == 0)
+          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(
+                           smem_u32(&acc_empty[buf]))
+                       : "memory");
+      }
+      // this CTA's share is stored: one arrival for its 8 warps
+      asm volatile("fence.proxy.async;" ::: "memory");
+      asm volatile("bar.sync 1, %0;" ::"r"(32 * kSEpiWarps) : "memory");
+      if (warp == 2 && lane == 0) {
+        if (failed_flag(failed))
+          atomicOr(r.counter, kNsGaveUp);
+        else
+          ns_grid_arrive(r.counter);
+      }
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;");
+  __syncthreads();
+  report_failure(r.status, failed);
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                 "r"(L::kTmemCols));
 }
 
 // Tensor map over fp16 [rows][cols] with pitch ld: boxes of 64 columns (one
@@ -619,6 +970,41 @@ cudaError_t ns_gemm(const NsOperand& a, const NsOperand& b, const NsArgs& args, 
   return ns_gemm_bn<64, A_MN, B_MN, MODE>(a, b, args, s);
 }
 
+// All steps in one launch. BN: 128 columns a tile where that fills the GPU.
+template <int BN, bool BF16>
+cudaError_t ns_fused(const NsRun& r, cudaStream_t s) {
+  using L = NsLayout<BN>;
+  NsMaps maps;
+  const int64_t side = r.rows < r.cols ? r.rows : r.cols;
+  for (int i = 0; i < 2; ++i)
+    if (!encode_half(&maps.x_mn[i], r.x[i], r.rows, r.cols, r.ldx, kSK) ||
+        !encode_half(&maps.x_a[i], r.x[i], r.rows, r.cols, r.ldx, kSM) ||
+        !encode_half(&maps.x_b[i], r.x[i], r.rows, r.cols, r.ldx, BN))
+      return cudaErrorInvalidValue;
+  if (!encode_half(&maps.ga_a, r.ga, side, side, r.lds, kSM) ||
+      !encode_half(&maps.ga_b, r.ga, side, side, r.lds, BN) ||
+      !encode_half(&maps.gb_a, r.gb, side, side, r.lds, kSM) ||
+      !encode_half(&maps.gb_b, r.gb, side, side, r.lds, BN))
+    return cudaErrorInvalidValue;
+  auto kern = k_ns_fused<BN, BF16>;
+  constexpr size_t smem = L::kBytes + 1024;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (r.rows + kSM - 1) / kSM * ((r.cols + BN - 1) / BN);
+  const int sms = ns_sms();
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(tiles < sms ? tiles : sms));
+  cfg.blockDim = dim3(kSThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeCooperative;
+  at[0].val.cooperative = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, maps, r);
+}
+
 int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
 int64_t pad256(int64_t v) { return (v + 255) / 256 * 256; }
 
@@ -626,7 +1012,7 @@ int64_t pad256(int64_t v) { return (v + 255) / 256 * 256; }
 
 int64_t newton_schulz_workspace(int64_t rows, int64_t cols) {
   const int64_t s = rows < cols ? rows : cols;
-  return 3 * pad256(rows * pad64(cols) * 2) + 2 * pad256(s * pad64(s) * 2) + kNsPartials * 8;
+  return 3 * pad256(rows * pad64(cols) * 2) + 2 * pad256(s * pad64(s) * 2) + kNsPartials * 8 + 256;
 }
 
 cudaError_t launch_newton_schulz(const void* g, bool bf16, int64_t rows, int64_t cols, int steps,
@@ -645,12 +1031,28 @@ cudaError_t launch_newton_schulz(const void* g, bool bf16, int64_t rows, int64_t
   const int64_t n = rows * cols;
   const int64_t want = (n / 8 + 255) / 256;
   const int n_partial = int(want < 1 ? 1 : (want < kNsPartials ? want : kNsPartials));
+  unsigned* counter = reinterpret_cast<unsigned*>(partial + kNsPartials);
   if (bf16)
-    k_ns_norm<true><<<n_partial, 256, 0, st>>>(g, n, partial);
+    k_ns_norm<true><<<n_partial, 256, 0, st>>>(g, n, partial, counter);
   else
-    k_ns_norm<false><<<n_partial, 256, 0, st>>>(g, n, partial);
+    k_ns_norm<false><<<n_partial, 256, 0, st>>>(g, n, partial, counter);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
+  // One launch for all products where 256-column tiles would not fill the GPU
+  const int64_t mt = (rows + kSM - 1) / kSM;
+  if (mt * ((cols + 255) / 256) < 148) {
+    NsRun r = {};
+    r.g = g, r.rows = rows, r.cols = cols, r.ldx = ldx, r.lds = lds;
+    r.steps = steps, r.n_partial = n_partial;
+    r.a = a, r.b = b, r.c = c, r.eps = eps;
+    r.partial = partial, r.counter = counter;
+    r.x[0] = x[0], r.x[1] = x[1], r.xl = xl, r.ga = ga, r.gb = gb;
+    r.out = out, r.out_bf16 = out_bf16, r.out_vec = cols % 8 == 0;
+    r.out_scale = scale * kNsInv, r.status = status;
+    if (mt * ((cols + 127) / 128) >= 148)
+      return bf16 ? ns_fused<128, true>(r, st) : ns_fused<128, false>(r, st);
+    return bf16 ? ns_fused<64, true>(r, st) : ns_fused<64, false>(r, st);
+  }
   const int64_t chunk_blocks = (rows * ((cols + 7) / 8) + 255) / 256;
   const int start_grid = int(chunk_blocks < 148 * 8 ? chunk_blocks : 148 * 8);
   e = bf16 ? ns_launch(k_ns_start<true>, start_grid, 256, 0, st, g, rows, cols, ldx, eps,
