@@ -343,97 +343,132 @@ __device__ __forceinline__ bool ns_epilogue(const NsArgs& p, int64_t row, int64_
   return ok;
 }
 
-// The thread that loads one operand (A: 128 rows, B: BN) into the ring, tile
+// The two issuing roles run with their whole warp, on values that are the
+// same in every lane, and one elected lane issues: the operands of tensor-core
+// and TMA instructions are then formed in uniform registers. From a branch
+// that one lane takes alone, four MMAs and a commit took 370 clocks to issue
+// and a load 410, more than a 128 x 64 stage needs.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ bool warp_wait(unsigned long long* bar, uint32_t parity,
+                                          const int* failed) {
+  return __all_sync(0xFFFFFFFFu, wait_parity_or_failed<false>(bar, parity, failed));
+}
+
+// The warp that loads one operand (A: 128 rows, B: BN) into the ring, tile
 // after tile. A box holds 64 columns; K-major operands come as one box of all
 // rows, MN-major ones as a box of 64 k rows for every 64 of the tile's rows.
-// (One thread for both operands took 0.3 us a stage of narrow tiles, twice
-// what their MMAs take.)
-template <int BN>
+template <int BN, bool A>
 struct NsLoader {
   using L = NsLayout<BN>;
+  static constexpr uint32_t kOp = A ? L::kA : L::kB;
   uint8_t* base;
   unsigned long long *full, *empty;
-  const int* failed;
-  uint32_t bytes, s = 0, ph = 0, issued = 0, last_ph = 0;
-  __device__ NsLoader(uint8_t* sm, unsigned long long* full_, unsigned long long* empty_, bool a,
-                      const int* failed_)
-      : base(a ? sm : sm + L::kBOff), full(full_), empty(empty_), failed(failed_),
-        bytes(a ? L::kA : L::kB) {}
-  __device__ bool tile(const CUtensorMap* map, bool mn, int row0, int64_t n_kb) {
-    const int boxes = mn ? int(bytes / 8192) : 1;
-    for (int64_t kb = 0; kb < n_kb; ++kb) {
-      if (!wait_parity_or_failed<false>(&empty[s], ph ^ 1u, failed)) {
-        atomicExch(const_cast<int*>(failed), 1);
+  int* failed;
+  const bool lead;
+  uint32_t s = 0, ph = 0, issued = 0, last_ph = 0;
+  __device__ NsLoader(uint8_t* sm, unsigned long long* full_, unsigned long long* empty_,
+                      int* failed_)
+      : base(A ? sm : sm + L::kBOff), full(full_), empty(empty_), failed(failed_),
+        lead(elect_one()) {}
+  __device__ __forceinline__ bool tile(const CUtensorMap* map, bool mn, int row0, int n_kb) {
+    for (int kb = 0; kb < n_kb; ++kb) {
+      if (!warp_wait(&empty[s], ph ^ 1u, failed)) {
+        atomicExch(failed, 1);
         return false;
       }
       issued |= 1u << s;
       last_ph = (last_ph & ~(1u << s)) | (ph << s);
-      uint8_t* to = base + s * bytes;
-      const int k0 = int(kb) * kSK;
-      expect_tx(&full[s], bytes);
-      if (mn) {
-        for (int j = 0; j < boxes; ++j)
-          tma_load_2d(to + j * 8192, map, row0 + 64 * j, k0, &full[s]);
-      } else {
-        tma_load_2d(to, map, k0, row0, &full[s]);
+      uint8_t* const to = base + s * kOp;
+      unsigned long long* const bar = &full[s];
+      const int k0 = kb * kSK;
+      if (lead) {
+        expect_tx(bar, kOp);
+        if (mn) {
+#pragma unroll
+          for (int j = 0; j < int(kOp / 8192); ++j)
+            tma_load_2d(to + j * 8192, map, row0 + 64 * j, k0, bar);
+        } else {
+          tma_load_2d(to, map, k0, row0, bar);
+        }
       }
       if (++s == L::kStages) s = 0, ph ^= 1u;
     }
-    return !failed_flag(failed);
+    return __all_sync(0xFFFFFFFFu, !failed_flag(failed));
   }
   // every load has landed (both operands': the phase completes with them)
-  __device__ void drain() {
+  __device__ __forceinline__ void drain() {
     for (uint32_t st = 0; st < L::kStages; ++st)
       if ((issued >> st) & 1u) wait_parity(&full[st], (last_ph >> st) & 1u);
+    __syncwarp();
   }
 };
 
-// The thread that issues the MMAs, tile after tile into the two accumulators
-// in turn. Its work per stage is kept small: descriptors advance by additions.
+// The warp that issues the MMAs, tile after tile into the two accumulators in
+// turn.
 template <int BN>
 struct NsIssuer {
   using L = NsLayout<BN>;
   uint8_t* sm;
   unsigned long long *full, *empty;
   uint32_t tmem;
-  const int* failed;
-  uint64_t a0, b0, ad, bd;
+  int* failed;
+  const bool lead;
+  uint64_t a0, b0;
   uint32_t ka, kb_, idesc, s = 0, ph = 0, ti = 0;
   __device__ NsIssuer(uint8_t* sm_, unsigned long long* full_, unsigned long long* empty_,
-                      uint32_t tmem_, const int* failed_)
-      : sm(sm_), full(full_), empty(empty_), tmem(tmem_), failed(failed_) {}
+                      uint32_t tmem_, int* failed_)
+      : sm(sm_), full(full_), empty(empty_), tmem(tmem_), failed(failed_), lead(elect_one()) {}
   // majorness of the operands of the tiles that follow
-  __device__ void operands(bool a_mn, bool b_mn) {
+  __device__ __forceinline__ void operands(bool a_mn, bool b_mn) {
     a0 = a_mn ? smem_desc_mn(sm) : smem_desc_sw128(sm);
     b0 = b_mn ? smem_desc_mn(sm + L::kBOff) : smem_desc_sw128(sm + L::kBOff);
-    ad = a0 + s * (L::kA >> 4), bd = b0 + s * (L::kB >> 4);
     ka = a_mn ? 128u : 2u, kb_ = b_mn ? 128u : 2u;
     idesc = L::idesc(a_mn, b_mn);
   }
-  __device__ bool tile(int64_t n_kb, unsigned long long* acc_full, unsigned long long* acc_empty) {
+  __device__ __forceinline__ bool tile(int n_kb, unsigned long long* acc_full,
+                                       unsigned long long* acc_empty) {
     const uint32_t buf = ti & 1, bph = (ti >> 1) & 1u;
-    if (!wait_parity_or_failed<false>(&acc_empty[buf], bph ^ 1u, failed) || failed_flag(failed))
-      return false;
+    if (!warp_wait(&acc_empty[buf], bph ^ 1u, failed)) return false;
     asm volatile("tcgen05.fence::after_thread_sync;");
     const uint32_t acc = tmem + buf * 256;
     bool ok = true;
-    for (int64_t kb = 0; kb < n_kb; ++kb) {
-      if (!wait_parity_or_failed<false>(&full[s], ph, failed)) {
+    for (int kb = 0; kb < n_kb; ++kb) {
+      if (!warp_wait(&full[s], ph, failed)) {
         ok = false;
         break;
       }
       asm volatile("tcgen05.fence::after_thread_sync;");
+      const uint64_t ad = a0 + s * (L::kA >> 4), bd = b0 + s * (L::kB >> 4);
+      unsigned long long* const bar = &empty[s];
+      if (lead) {
 #pragma unroll
-      for (uint32_t j = 0; j < kSK / 16; ++j)
-        mma_f16(acc + (j % L::kAcc) * BN, ad + j * ka, bd + j * kb_, idesc,
-                (kb > 0 || j >= L::kAcc) ? 1u : 0u);
-      commit_to(&empty[s]);
-      ad += L::kA >> 4, bd += L::kB >> 4;
-      if (++s == L::kStages) s = 0, ph ^= 1u, ad = a0, bd = b0;
+        for (uint32_t j = 0; j < kSK / 16; ++j)
+          mma_f16(acc + (j % L::kAcc) * BN, ad + j * ka, bd + j * kb_, idesc,
+                  (kb > 0 || j >= L::kAcc) ? 1u : 0u);
+        commit_to(bar);
+      }
+      if (++s == L::kStages) s = 0, ph ^= 1u;
     }
-    commit_to(&acc_full[buf]);
+    if (lead) commit_to(&acc_full[buf]);
+    __syncwarp();
     ++ti;
     return ok;
+  }
+  // every MMA issued has completed
+  __device__ __forceinline__ void finish(bool ok, unsigned long long* drain) {
+    if (!ok) atomicExch(failed, 1);
+    if (lead) commit_to(drain);
+    __syncwarp();
+    if (!wait_parity(drain, 0)) atomicExch(failed, 1);
+    __syncwarp();
   }
 };
 
@@ -452,10 +487,11 @@ __global__ void __launch_bounds__(kSThreads, 1)
   unsigned long long* drain = acc_empty + 2;
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drain + 1);
   int* failed = reinterpret_cast<int*>(tmem_base + 1);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const int64_t mt = (p.m + kSM - 1) / kSM, nt = (p.n + BN - 1) / BN;
   const int64_t n_tiles = ns_tiles<BN>(kSym, mt, nt);
-  const int64_t n_kb = (p.k + kSK - 1) / kSK;
+  const int n_kb = int((p.k + kSK - 1) / kSK);
 
   if (tid == 0) {
     for (int s = 0; s < L::kStages; ++s) {
@@ -486,30 +522,29 @@ __global__ void __launch_bounds__(kSThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  if (warp == 0 || warp == kSLoadB) {
-    if (lane == 0) {
-      NsLoader<BN> ld(sm, full, empty, warp == 0, failed);
-      const bool mn = warp == 0 ? A_MN : B_MN;
-      for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x) {
-        int64_t m0, n0;
-        ns_tile<BN, kSym>(t, mt, nt, m0, n0);
-        if (!ld.tile(warp == 0 ? &tm_a : &tm_b, mn, int(warp == 0 ? m0 : n0), n_kb)) break;
-      }
-      ld.drain();
+  if (warp == 0) {
+    NsLoader<BN, true> ld(sm, full, empty, failed);
+    for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x) {
+      int64_t m0, n0;
+      ns_tile<BN, kSym>(t, mt, nt, m0, n0);
+      if (!ld.tile(&tm_a, A_MN, int(m0), n_kb)) break;
     }
-    __syncwarp();
+    ld.drain();
+  } else if (warp == kSLoadB) {
+    NsLoader<BN, false> ld(sm, full, empty, failed);
+    for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x) {
+      int64_t m0, n0;
+      ns_tile<BN, kSym>(t, mt, nt, m0, n0);
+      if (!ld.tile(&tm_b, B_MN, int(n0), n_kb)) break;
+    }
+    ld.drain();
   } else if (warp == 1) {
-    if (lane == 0) {
-      NsIssuer<BN> mma(sm, full, empty, tmem, failed);
-      mma.operands(A_MN, B_MN);
-      bool ok = true;
-      for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x)
-        ok = mma.tile(n_kb, acc_full, acc_empty);
-      if (!ok) atomicExch(failed, 1);
-      commit_to(drain);
-      if (!wait_parity(drain, 0)) atomicExch(failed, 1);
-    }
-    __syncwarp();
+    NsIssuer<BN> mma(sm, full, empty, tmem, failed);
+    mma.operands(A_MN, B_MN);
+    bool ok = true;
+    for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x)
+      ok = mma.tile(n_kb, acc_full, acc_empty);
+    mma.finish(ok, drain);
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
     int64_t ti = 0;
@@ -755,7 +790,8 @@ __global__ void __launch_bounds__(kSThreads, 1)
   unsigned long long* drain = acc_empty + 2;
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drain + 1);
   int* failed = reinterpret_cast<int*>(tmem_base + 1);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const int phases = 3 * r.steps;
   auto tiles_of = [&](const NsPhase& f, int64_t& mt, int64_t& nt) {
     mt = (f.p.m + kSM - 1) / kSM, nt = (f.p.n + BN - 1) / BN;
@@ -798,46 +834,43 @@ __global__ void __launch_bounds__(kSThreads, 1)
   const uint32_t tmem = *tmem_base;
   if (tid == 0) ns_grid_arrive(r.counter);
 
-  if (warp == 0 || warp == kSLoadB) {
-    if (lane == 0) {
-      NsLoader<BN> ld(sm, full, empty, warp == 0, failed);
-      bool ok = true;
-      for (int i = 0; i < phases && ok; ++i) {
-        const NsPhase f = ns_phase(r, maps, i);
-        int64_t mt, nt;
-        const int64_t n_tiles = tiles_of(f, mt, nt), n_kb = (f.p.k + kSK - 1) / kSK;
-        if (!ns_grid_wait(r.counter, gridDim.x * unsigned(i + 1), failed)) {
-          atomicExch(failed, 1);
-          break;
-        }
-        asm volatile("fence.proxy.async;" ::: "memory");
-        for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
-          int64_t m0, n0;
-          tile_of(f, t, mt, nt, m0, n0);
-          ok = ld.tile(warp == 0 ? f.ta : f.tb, warp == 0 ? f.a_mn : f.b_mn,
-                       int(warp == 0 ? m0 : n0), n_kb);
-        }
+  auto load_all = [&](auto ld, bool is_a) {
+    bool ok = true;
+    for (int i = 0; i < phases && ok; ++i) {
+      const NsPhase f = ns_phase(r, maps, i);
+      int64_t mt, nt;
+      const int64_t n_tiles = tiles_of(f, mt, nt);
+      const int n_kb = int((f.p.k + kSK - 1) / kSK);
+      if (!__all_sync(0xFFFFFFFFu,
+                      ns_grid_wait(r.counter, gridDim.x * unsigned(i + 1), failed))) {
+        atomicExch(failed, 1);
+        break;
       }
-      ld.drain();
+      asm volatile("fence.proxy.async;" ::: "memory");
+      for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
+        int64_t m0, n0;
+        tile_of(f, t, mt, nt, m0, n0);
+        ok = ld.tile(is_a ? f.ta : f.tb, is_a ? f.a_mn : f.b_mn, int(is_a ? m0 : n0), n_kb);
+      }
     }
-    __syncwarp();
+    ld.drain();
+  };
+  if (warp == 0) {
+    load_all(NsLoader<BN, true>(sm, full, empty, failed), true);
+  } else if (warp == kSLoadB) {
+    load_all(NsLoader<BN, false>(sm, full, empty, failed), false);
   } else if (warp == 1) {
-    if (lane == 0) {
-      NsIssuer<BN> mma(sm, full, empty, tmem, failed);
-      bool ok = true;
-      for (int i = 0; i < phases && ok; ++i) {
-        const NsPhase f = ns_phase(r, maps, i);
-        int64_t mt, nt;
-        const int64_t n_tiles = tiles_of(f, mt, nt), n_kb = (f.p.k + kSK - 1) / kSK;
-        mma.operands(f.a_mn, f.b_mn);
-        for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x)
-          ok = mma.tile(n_kb, acc_full, acc_empty);
-      }
-      if (!ok) atomicExch(failed, 1);
-      commit_to(drain);
-      if (!wait_parity(drain, 0)) atomicExch(failed, 1);
+    NsIssuer<BN> mma(sm, full, empty, tmem, failed);
+    bool ok = true;
+    for (int i = 0; i < phases && ok; ++i) {
+      const NsPhase f = ns_phase(r, maps, i);
+      int64_t mt, nt;
+      const int64_t n_tiles = tiles_of(f, mt, nt);
+      mma.operands(f.a_mn, f.b_mn);
+      for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x)
+        ok = mma.tile(int((f.p.k + kSK - 1) / kSK), acc_full, acc_empty);
     }
-    __syncwarp();
+    mma.finish(ok, drain);
   } else {
     const int q = warp & 3, half = (warp - 2) >> 2;
     int64_t ti = 0;
