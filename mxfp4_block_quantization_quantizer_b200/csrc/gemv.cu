@@ -134,6 +134,24 @@ __device__ __forceinline__ bool v_wait(unsigned long long* bar, uint32_t parity,
   return false;
 }
 
+// The issuing warps run together on values that are the same in every lane,
+// and one elected lane issues: the operands of tensor-core and TMA
+// instructions are then formed in uniform registers (from a branch that one
+// lane takes alone each of them takes 70 to 90 clocks to issue).
+__device__ __forceinline__ bool v_elect() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
+__device__ __forceinline__ bool v_warp_wait(unsigned long long* bar, uint32_t parity,
+                                            const int* failed) {
+  return __all_sync(0xFFFFFFFFu, v_wait(bar, parity, failed));
+}
+
 __device__ __forceinline__ uint32_t v_cluster_rank() {
   uint32_t r;
   asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
@@ -241,7 +259,8 @@ __global__ void __launch_bounds__(kVThreads)
   unsigned long long* acc_full = empty + L::kStages;
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(acc_full + 1);
   int* failed = reinterpret_cast<int*>(tmem_base + 1);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const int split = sh.split;
   const int rank = split > 1 ? int(v_cluster_rank()) : 0;
   const int64_t tile = blockIdx.x / split;
@@ -253,10 +272,8 @@ __global__ void __launch_bounds__(kVThreads)
   const int kb1 = int(int64_t(sh.stages) * (rank + 1) / split);
 
   if (split > 1) v_cluster_arrive();  // waited for before the first store to a peer
-  uint32_t issued = 0, last_ph = 0;   // loading thread: stages, last phases
-  auto load_w = [&](int kb, uint32_t s, uint32_t ph) {
-    issued |= 1u << s;
-    last_ph = (last_ph & ~(1u << s)) | (ph << s);
+  // the loads of a stage, by one thread
+  auto load_w = [&](int kb, uint32_t s) {
     // (the last stage may have one scale tile)
     const uint32_t sf = 2 * kb + 1 < sh.k_tiles ? 1024u : 512u;
     expect_tx(&full[s], L::kA + sf + (OWN ? 0 : L::kX));
@@ -282,7 +299,7 @@ __global__ void __launch_bounds__(kVThreads)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     *failed = 0;
     // the first stages are free, and their weights need not wait for digits
-    for (int i = 0; i < L::kStages && kb0 + i < kb1; ++i) load_w(kb0 + i, uint32_t(i), 0);
+    for (int i = 0; i < L::kStages && kb0 + i < kb1; ++i) load_w(kb0 + i, uint32_t(i));
   }
   if (warp == 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -315,45 +332,50 @@ __global__ void __launch_bounds__(kVThreads)
   const uint32_t tmem = *tmem_base;
 
   if (warp == 0) {
-    if (lane == 0) {
-      if (!OWN) asm volatile("griddepcontrol.wait;" ::: "memory");
-      for (int i = 0; i < L::kStages && kb0 + i < kb1; ++i) load_x(kb0 + i, uint32_t(i));
-      uint32_t s = 0, ph = 1;
-      for (int kb = kb0 + L::kStages; kb < kb1; ++kb) {
-        if (!v_wait(&empty[s], ph ^ 1u, failed)) {
-          atomicExch(failed, 1);
-          break;
-        }
-        load_w(kb, s, ph);
-        load_x(kb, s);
-        if (++s == L::kStages) s = 0, ph ^= 1u;
-      }
-      // every load has landed before the CTA can end
-      for (uint32_t st = 0; st < L::kStages; ++st)
-        if ((issued >> st) & 1u) v_wait(&full[st], (last_ph >> st) & 1u, nullptr);
+    const bool lead = v_elect();
+    if (!OWN) {
+      asm volatile("griddepcontrol.wait;" ::: "memory");
+      if (lead)
+        for (int i = 0; i < L::kStages && kb0 + i < kb1; ++i) load_x(kb0 + i, uint32_t(i));
     }
+    // stages with a load, and the phase of each one's last
+    uint32_t s = 0, ph = 1, issued = (1u << min(L::kStages, kb1 - kb0)) - 1, last_ph = 0;
+    for (int kb = kb0 + L::kStages; kb < kb1; ++kb) {
+      if (!v_warp_wait(&empty[s], ph ^ 1u, failed)) {
+        atomicExch(failed, 1);
+        break;
+      }
+      last_ph = (last_ph & ~(1u << s)) | (ph << s);
+      if (lead) {
+        load_w(kb, s);
+        load_x(kb, s);
+      }
+      if (++s == L::kStages) s = 0, ph ^= 1u;
+    }
+    // every load has landed before the CTA can end
+    for (uint32_t st = 0; st < L::kStages; ++st)
+      if ((issued >> st) & 1u) v_wait(&full[st], (last_ph >> st) & 1u, nullptr);
     __syncwarp();
   } else if (warp == 1) {
-    if (lane == 0) {
-      // issuing bounds this thread: the loop is unrolled over the ring, so
-      // that every operand is a base plus a constant
-      const uint64_t a0 = smem_desc_sw128(sm), x0 = smem_desc_sw128(sm + L::kXOff);
-      const uint64_t fa0 = smem_desc(sm + L::kSfaOff, 16, 128);
-      const uint64_t fb0 = smem_desc(sm + L::kXOff + L::kB, 16, 128);
-      const uint32_t sf0 = tmem + L::kSfCol;
-      bool ok = true;
-      uint32_t ph = 0;
-      for (int kb = kb0; kb < kb1 && ok; kb += L::kStages, ph ^= 1u) {
+    const bool lead = v_elect();
+    const uint64_t a0 = smem_desc_sw128(sm), x0 = smem_desc_sw128(sm + L::kXOff);
+    const uint64_t fa0 = smem_desc(sm + L::kSfaOff, 16, 128);
+    const uint64_t fb0 = smem_desc(sm + L::kXOff + L::kB, 16, 128);
+    const uint32_t sf0 = tmem + L::kSfCol;
+    bool ok = true;
+    uint32_t ph = 0;
+    for (int kb = kb0; kb < kb1 && ok; kb += L::kStages, ph ^= 1u) {
 #pragma unroll
-        for (int s = 0; s < L::kStages; ++s) {
-          if (kb + s >= kb1) break;
-          if (!v_wait(&full[s], ph, failed)) {
-            ok = false;
-            break;
-          }
-          asm volatile("tcgen05.fence::after_thread_sync;");
-          const int left = sh.steps - 4 * (kb + s);  // MMAs of this stage, up to 4
-          const uint32_t sfa = sf0 + L::kSfStage * s, sfb = sfa + 8;
+      for (int s = 0; s < L::kStages; ++s) {
+        if (kb + s >= kb1) break;
+        if (!v_warp_wait(&full[s], ph, failed)) {
+          ok = false;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;");
+        const int left = sh.steps - 4 * (kb + s);  // MMAs of this stage, up to 4
+        const uint32_t sfa = sf0 + L::kSfStage * s, sfb = sfa + 8;
+        if (lead) {
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
             if (2 * j >= left) break;
@@ -376,11 +398,12 @@ __global__ void __launch_bounds__(kVThreads)
           commit_to(&empty[s]);
         }
       }
-      if (!ok) atomicExch(failed, 1);
-      commit_to(acc_full);
-      // the MMAs issued have completed before shared or tensor memory goes
-      if (!v_wait(acc_full, 0, nullptr)) atomicExch(failed, 1);
     }
+    if (!ok) atomicExch(failed, 1);
+    if (lead) commit_to(acc_full);
+    __syncwarp();
+    // the MMAs issued have completed before shared or tensor memory goes
+    if (!v_wait(acc_full, 0, nullptr)) atomicExch(failed, 1);
     __syncwarp();
   } else if (OWN) {
     for (int i = w < active ? w : n_items; i < n_items; i += active) {

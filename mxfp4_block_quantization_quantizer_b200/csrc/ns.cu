@@ -191,11 +191,10 @@ __device__ __forceinline__ void transpose32(float* v, int lane) {
 // The epilogue of one warp for its row (lane) and the BN / 2 columns from n0
 // on, in rounds of 32: waits for the products, reads them from tensor memory
 // at `tb` and stores D. Returns false (and stores NaN) if the wait ran out.
-template <int BN, int MODE>
+template <int BN, int MODE, bool SYM>
 __device__ __forceinline__ bool ns_epilogue(const NsArgs& p, int64_t row, int64_t n0, uint32_t tb,
                                             unsigned long long* acc_full, uint32_t phase,
                                             int* failed) {
-  constexpr bool kSym = MODE == kGram || MODE == kSquare;
   constexpr int kCols = BN / 2;
   constexpr bool kHasC = MODE != kGram, kHasLo = MODE == kStep || MODE == kLast;
   // C's share of 32 columns, loaded a round ahead (the first one before the
@@ -308,7 +307,7 @@ __device__ __forceinline__ bool ns_epilogue(const NsArgs& p, int64_t row, int64_
         uint32_t w[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) w[j] = pack_h2(e[2 * j], e[2 * j + 1]);
-        if constexpr (kSym) {
+        if constexpr (SYM) {
           // each entry of the symmetric result has one writer: the element on
           // or above the diagonal, for both sides
 #pragma unroll
@@ -324,14 +323,16 @@ __device__ __forceinline__ bool ns_epilogue(const NsArgs& p, int64_t row, int64_
                 make_uint4(w[0], w[1], w[2], w[3]);
         } else {
           *reinterpret_cast<uint4*>(p.d_hi + row * p.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
-          uint32_t lw[4];
+          if constexpr (kHasLo) {
+            uint32_t lw[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float2 f = unpack_h2(w[j]);
-            lw[j] = pack_h2(__fsub_rn(e[2 * j], f.x), __fsub_rn(e[2 * j + 1], f.y));
+            for (int j = 0; j < 4; ++j) {
+              const float2 f = unpack_h2(w[j]);
+              lw[j] = pack_h2(__fsub_rn(e[2 * j], f.x), __fsub_rn(e[2 * j + 1], f.y));
+            }
+            *reinterpret_cast<uint4*>(p.d_lo + row * p.ldd + c) =
+                make_uint4(lw[0], lw[1], lw[2], lw[3]);
           }
-          *reinterpret_cast<uint4*>(p.d_lo + row * p.ldd + c) =
-              make_uint4(lw[0], lw[1], lw[2], lw[3]);
         }
       }
     }
@@ -552,7 +553,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
       int64_t m0, n0;
       ns_tile<BN, kSym>(t, mt, nt, m0, n0);
       const uint32_t buf = uint32_t(ti & 1), bph = uint32_t(ti >> 1) & 1u;
-      const bool ok = ns_epilogue<BN, MODE>(p, m0 + 32 * q + lane, n0 + (BN / 2) * half,
+      const bool ok = ns_epilogue<BN, MODE, kSym>(p, m0 + 32 * q + lane, n0 + (BN / 2) * half,
                                             tmem + buf * 256 + (uint32_t(32 * q) << 16) +
                                                 uint32_t((BN / 2) * half),
                                             &acc_full[buf], bph, failed);
@@ -705,7 +706,7 @@ struct NsMaps {
 struct NsRun {
   const void* g;
   int64_t rows, cols, ldx, lds;
-  int steps, n_partial;
+  int steps, n_partial, sym;  // sym: half of the symmetric products' tiles
   float a, b, c, eps;
   const double* partial;
   unsigned* counter;
@@ -730,7 +731,7 @@ __device__ __forceinline__ NsPhase ns_phase(const NsRun& r, const NsMaps& maps, 
   NsPhase f = {};
   f.p.status = r.status;
   f.mode = i % 3;
-  f.sym = f.mode != 2;
+  f.sym = f.mode != 2 && r.sym;
   if (f.mode == 0) {
     f.p.m = f.p.n = s, f.p.k = tall ? r.rows : r.cols, f.p.ldd = r.lds;
     f.p.alpha = kNsInv, f.p.d_hi = r.ga;
@@ -891,15 +892,18 @@ __global__ void __launch_bounds__(kSThreads, 1)
         const int64_t row = m0 + 32 * q + lane, c0 = n0 + (BN / 2) * half;
         const uint32_t tb =
             tmem + buf * 256 + (uint32_t(32 * q) << 16) + uint32_t((BN / 2) * half);
+        unsigned long long* const done = &acc_full[buf];
         bool ok;
         if (f.mode == kGram)
-          ok = ns_epilogue<BN, kGram>(f.p, row, c0, tb, &acc_full[buf], bph, failed);
+          ok = f.sym ? ns_epilogue<BN, kGram, true>(f.p, row, c0, tb, done, bph, failed)
+                     : ns_epilogue<BN, kGram, false>(f.p, row, c0, tb, done, bph, failed);
         else if (f.mode == kSquare)
-          ok = ns_epilogue<BN, kSquare>(f.p, row, c0, tb, &acc_full[buf], bph, failed);
+          ok = f.sym ? ns_epilogue<BN, kSquare, true>(f.p, row, c0, tb, done, bph, failed)
+                     : ns_epilogue<BN, kSquare, false>(f.p, row, c0, tb, done, bph, failed);
         else if (f.mode == kStep)
-          ok = ns_epilogue<BN, kStep>(f.p, row, c0, tb, &acc_full[buf], bph, failed);
+          ok = ns_epilogue<BN, kStep, false>(f.p, row, c0, tb, done, bph, failed);
         else
-          ok = ns_epilogue<BN, kLast>(f.p, row, c0, tb, &acc_full[buf], bph, failed);
+          ok = ns_epilogue<BN, kLast, false>(f.p, row, c0, tb, done, bph, failed);
         if (ok && lane == 0)
           asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(
                            smem_u32(&acc_empty[buf]))
@@ -1005,10 +1009,14 @@ cudaError_t ns_gemm(const NsOperand& a, const NsOperand& b, const NsArgs& args, 
 
 // All steps in one launch. BN: 128 columns a tile where that fills the GPU.
 template <int BN, bool BF16>
-cudaError_t ns_fused(const NsRun& r, cudaStream_t s) {
+cudaError_t ns_fused(NsRun r, cudaStream_t s) {
   using L = NsLayout<BN>;
   NsMaps maps;
   const int64_t side = r.rows < r.cols ? r.rows : r.cols;
+  const int sms = ns_sms();
+  // all tiles of A and B where the SMs can take them at once: no slower, and
+  // the mirrored stores fall away
+  r.sym = (side + kSM - 1) / kSM * ((side + BN - 1) / BN) > sms;
   for (int i = 0; i < 2; ++i)
     if (!encode_half(&maps.x_mn[i], r.x[i], r.rows, r.cols, r.ldx, kSK) ||
         !encode_half(&maps.x_a[i], r.x[i], r.rows, r.cols, r.ldx, kSM) ||
@@ -1023,17 +1031,18 @@ cudaError_t ns_fused(const NsRun& r, cudaStream_t s) {
   constexpr size_t smem = L::kBytes + 1024;
   const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
   if (e != cudaSuccess) return e;
-  const int64_t tiles = (r.rows + kSM - 1) / kSM * ((r.cols + BN - 1) / BN);
-  const int sms = ns_sms();
+  const int64_t xt = (r.rows + kSM - 1) / kSM * ((r.cols + BN - 1) / BN);
+  const int64_t at = (side + kSM - 1) / kSM * ((side + BN - 1) / BN);
+  const int64_t tiles = xt > at ? xt : at;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(tiles < sms ? tiles : sms));
   cfg.blockDim = dim3(kSThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeCooperative;
-  at[0].val.cooperative = 1;
-  cfg.attrs = at;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, maps, r);
 }
