@@ -61,7 +61,9 @@ struct NsLayout {
   static constexpr int kStages = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
   static constexpr uint32_t kA = kSM * 128, kB = BN * 128;
   static constexpr uint32_t kBOff = kStages * kA;
-  static constexpr uint32_t kBarOff = kBOff + kStages * kB;
+  // per epilogue warp: 32 rows x 32 fp16, rows 80 bytes apart (no bank twice)
+  static constexpr uint32_t kEpiOff = kBOff + kStages * kB;
+  static constexpr uint32_t kBarOff = kEpiOff + kSEpiWarps * 32 * 80;
   static constexpr uint32_t kBytes = kBarOff + 256;
   // Accumulators of a tile: consecutive MMAs on one wait for each other, about
   // 150 clocks, which 128 x 256 products cover and narrower ones do not; the
@@ -188,13 +190,36 @@ __device__ __forceinline__ void transpose32(float* v, int lane) {
   }
 }
 
+// Store a warp's 32 x 32 fp16 tile, lane l holding row l in w[0..15]: through
+// the warp's staging tile, so that an instruction writes 8 rows of 64 bytes
+// and not 32 of 16 (which took the epilogue three times as long).
+__device__ __forceinline__ void store_tile(uint8_t* stage, const uint32_t* w, __half* d,
+                                           int64_t ldd, int64_t row0, int64_t c0, int64_t m,
+                                           int64_t n) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int g = 0; g < 4; ++g)
+    *reinterpret_cast<uint4*>(stage + lane * 80 + 16 * g) =
+        make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
+  __syncwarp();
+  // (rows are padded to whole 16-byte chunks)
+  const int64_t c = c0 + 8 * (lane & 3);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 80 + 16 * (lane & 3));
+    if (row0 + r < m && c < n) *reinterpret_cast<uint4*>(d + (row0 + r) * ldd + c) = v;
+  }
+  __syncwarp();
+}
+
 // The epilogue of one warp for its row (lane) and the BN / 2 columns from n0
 // on, in rounds of 32: waits for the products, reads them from tensor memory
 // at `tb` and stores D. Returns false (and stores NaN) if the wait ran out.
 template <int BN, int MODE, bool SYM>
 __device__ __forceinline__ bool ns_epilogue(const NsArgs& p, int64_t row, int64_t n0, uint32_t tb,
-                                            unsigned long long* acc_full, uint32_t phase,
-                                            int* failed) {
+                                            uint8_t* stage, unsigned long long* acc_full,
+                                            uint32_t phase, int* failed) {
   constexpr int kCols = BN / 2;
   constexpr bool kHasC = MODE != kGram, kHasLo = MODE == kStep || MODE == kLast;
   // C's share of 32 columns, loaded a round ahead (the first one before the
@@ -299,40 +324,38 @@ __device__ __forceinline__ bool ns_epilogue(const NsArgs& p, int64_t row, int64_
         }
       }
     } else {
+      const int64_t row0 = row - (threadIdx.x & 31);
+      uint32_t w[16];
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int64_t c = c0 + 8 * g;
-        const float* e = o + 8 * g;
-        if (row >= p.m || c >= p.n) continue;
-        uint32_t w[4];
+      for (int j = 0; j < 16; ++j) w[j] = pack_h2(o[2 * j], o[2 * j + 1]);
+      if constexpr (SYM) {
+        // each entry of the symmetric result has one writer, the element on
+        // or above the diagonal, for both sides
+        if (c0 >= row0 + 31) {
+          store_tile(stage, w, p.d_hi, p.ldd, row0, c0, p.m, p.n);
+        } else if (row < p.m) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = pack_h2(e[2 * j], e[2 * j + 1]);
-        if constexpr (SYM) {
-          // each entry of the symmetric result has one writer: the element on
-          // or above the diagonal, for both sides
+          for (int j = 0; j < 32; ++j)
+            if (c0 + j >= row && c0 + j < p.n)
+              p.d_hi[row * p.ldd + c0 + j] =
+                  __ushort_as_half(uint16_t(w[j / 2] >> (16 * (j & 1))));
+        }
+        if (row < p.m) {
+          __half* to = p.d_hi + c0 * p.ldd + row;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const __half hv = __ushort_as_half(uint16_t(w[j / 2] >> (16 * (j & 1))));
-            if (c + j >= row && c + j < p.n) {
-              p.d_hi[(c + j) * p.ldd + row] = hv;
-              if (c < row) p.d_hi[row * p.ldd + c + j] = hv;
-            }
+          for (int j = 0; j < 32; ++j, to += p.ldd)
+            if (c0 + j >= row && c0 + j < p.n)
+              *to = __ushort_as_half(uint16_t(w[j / 2] >> (16 * (j & 1))));
+        }
+      } else {
+        store_tile(stage, w, p.d_hi, p.ldd, row0, c0, p.m, p.n);
+        if constexpr (kHasLo) {
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const float2 f = unpack_h2(w[j]);
+            w[j] = pack_h2(__fsub_rn(o[2 * j], f.x), __fsub_rn(o[2 * j + 1], f.y));
           }
-          if (c >= row)
-            *reinterpret_cast<uint4*>(p.d_hi + row * p.ldd + c) =
-                make_uint4(w[0], w[1], w[2], w[3]);
-        } else {
-          *reinterpret_cast<uint4*>(p.d_hi + row * p.ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
-          if constexpr (kHasLo) {
-            uint32_t lw[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float2 f = unpack_h2(w[j]);
-              lw[j] = pack_h2(__fsub_rn(e[2 * j], f.x), __fsub_rn(e[2 * j + 1], f.y));
-            }
-            *reinterpret_cast<uint4*>(p.d_lo + row * p.ldd + c) =
-                make_uint4(lw[0], lw[1], lw[2], lw[3]);
-          }
+          store_tile(stage, w, p.d_lo, p.ldd, row0, c0, p.m, p.n);
         }
       }
     }
@@ -556,6 +579,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
       const bool ok = ns_epilogue<BN, MODE, kSym>(p, m0 + 32 * q + lane, n0 + (BN / 2) * half,
                                             tmem + buf * 256 + (uint32_t(32 * q) << 16) +
                                                 uint32_t((BN / 2) * half),
+                                            sm + L::kEpiOff + (warp - 2) * (32 * 80),
                                             &acc_full[buf], bph, failed);
       if (ok && lane == 0)
         asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(&acc_empty[buf]))
@@ -693,9 +717,9 @@ __global__ void __launch_bounds__(256)
 // short for a launch each: the same roles and tiles as k_ns_gemm, but the
 // pipeline runs on from product to product, with a barrier over the grid
 // between them (a counter in the workspace, zeroed by k_ns_norm) in place of
-// the end of one launch and the start of the next. The thread that loads and
-// the epilogue warps wait at it; what other CTAs stored is then read through
-// the asynchronous proxy, hence the fence on both sides.
+// the end of one launch and the start of the next. The warps that load and
+// the epilogue warps wait at it; the loads read what other CTAs stored through
+// the asynchronous proxy, hence their proxy fence behind the acquire.
 // ---------------------------------------------------------------------------
 
 // Tensor maps with boxes of 64 columns x 64 rows, kSM rows (K-major A) and BN
@@ -774,7 +798,6 @@ __device__ __forceinline__ bool ns_grid_wait(const unsigned* counter, unsigned t
   return false;
 }
 __device__ __forceinline__ void ns_grid_arrive(unsigned* counter) {
-  __threadfence();
   asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(counter) : "memory");
 }
 
@@ -829,7 +852,6 @@ __global__ void __launch_bounds__(kSThreads, 1)
   ns_start<BF16>(r.g, r.rows, r.cols, r.ldx, r.eps, r.partial, r.n_partial, r.x[0], r.xl,
                  reinterpret_cast<float*>(sm));
   asm volatile("tcgen05.fence::before_thread_sync;");
-  asm volatile("fence.proxy.async;" ::: "memory");
   __syncthreads();
   asm volatile("tcgen05.fence::after_thread_sync;");
   const uint32_t tmem = *tmem_base;
@@ -893,24 +915,25 @@ __global__ void __launch_bounds__(kSThreads, 1)
         const uint32_t tb =
             tmem + buf * 256 + (uint32_t(32 * q) << 16) + uint32_t((BN / 2) * half);
         unsigned long long* const done = &acc_full[buf];
+        uint8_t* const stage = sm + L::kEpiOff + (warp - 2) * (32 * 80);
         bool ok;
         if (f.mode == kGram)
-          ok = f.sym ? ns_epilogue<BN, kGram, true>(f.p, row, c0, tb, done, bph, failed)
-                     : ns_epilogue<BN, kGram, false>(f.p, row, c0, tb, done, bph, failed);
+          ok = f.sym ? ns_epilogue<BN, kGram, true>(f.p, row, c0, tb, stage, done, bph, failed)
+                     : ns_epilogue<BN, kGram, false>(f.p, row, c0, tb, stage, done, bph, failed);
         else if (f.mode == kSquare)
-          ok = f.sym ? ns_epilogue<BN, kSquare, true>(f.p, row, c0, tb, done, bph, failed)
-                     : ns_epilogue<BN, kSquare, false>(f.p, row, c0, tb, done, bph, failed);
+          ok = f.sym ? ns_epilogue<BN, kSquare, true>(f.p, row, c0, tb, stage, done, bph, failed)
+                     : ns_epilogue<BN, kSquare, false>(f.p, row, c0, tb, stage, done, bph, failed);
         else if (f.mode == kStep)
-          ok = ns_epilogue<BN, kStep, false>(f.p, row, c0, tb, done, bph, failed);
+          ok = ns_epilogue<BN, kStep, false>(f.p, row, c0, tb, stage, done, bph, failed);
         else
-          ok = ns_epilogue<BN, kLast, false>(f.p, row, c0, tb, done, bph, failed);
+          ok = ns_epilogue<BN, kLast, false>(f.p, row, c0, tb, stage, done, bph, failed);
         if (ok && lane == 0)
           asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(
                            smem_u32(&acc_empty[buf]))
                        : "memory");
       }
-      // this CTA's share is stored: one arrival for its 8 warps
-      asm volatile("fence.proxy.async;" ::: "memory");
+      // this CTA's share is stored: one arrival for its 8 warps, whose release
+      // covers what the barrier ordered before it
       asm volatile("bar.sync 1, %0;" ::"r"(32 * kSEpiWarps) : "memory");
       if (warp == 2 && lane == 0) {
         if (failed_flag(failed))
