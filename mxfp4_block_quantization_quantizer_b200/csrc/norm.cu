@@ -40,11 +40,10 @@ namespace {
 
 constexpr int kLnMaxWarps = 16;      // warps of a CTA that share a row
 constexpr int kLnMaxParts = 32;      // ... and of a cluster
-// Rows in flight per group, and what the forward kernels are compiled for:
-// the largest vector counts run with at most 8 warps a CTA, three CTAs an SM.
+// Rows in flight per group.
 __host__ __device__ constexpr int ln_depth(int nv) { return nv == 1 ? 4 : 2; }
-__host__ __device__ constexpr int ln_threads(bool bf16, int nv) { return nv == (bf16 ? 6 : 8) ? 256 : 512; }
-__host__ __device__ constexpr int ln_blocks(bool bf16, int nv) { return nv == (bf16 ? 6 : 8) ? 3 : 1; }
+// Warps of a CTA that narrow rows share (backward: few partial sums).
+constexpr int kLnFwdWarps = 4, kLnBwdWarps = 16;
 constexpr int64_t kLnMaxCols = 1 << 16;  // far above what a cluster holds
 constexpr int kLnGenThreads = 512;   // the kernels for wider rows
 constexpr int kLnRedThreads = 1024;
@@ -127,12 +126,15 @@ __device__ __forceinline__ float rsqrt_exact(float v) {
   return v > 0.0f && v < __uint_as_float(0x7F800000u) ? n : r;
 }
 
-// Barrier of the W warps of row group g (id 1 + g), or of one warp.
+// Barrier of the W > 1 warps of row group g, of at most MAXG in the CTA. (With
+// the barrier's number in a register a CTA reserves all 16, and four CTAs all
+// of an SM's.)
+template <int MAXG>
 __device__ __forceinline__ void group_sync(int g, int W) {
-  if (W == 1)
-    __syncwarp();
-  else
-    asm volatile("bar.sync %0, %1;" ::"r"(g + 1), "r"(W * 32) : "memory");
+  if (g == MAXG - 1)
+    asm volatile("bar.sync %0, %1;" ::"n"(MAXG), "r"(W * 32) : "memory");
+  else if constexpr (MAXG > 1)
+    group_sync<MAXG - 1>(g, W);
 }
 // Every thread of both CTAs of a cluster (release, then acquire).
 __device__ __forceinline__ void pair_sync() {
@@ -259,6 +261,28 @@ __device__ __forceinline__ void stage_param(const float* param, float fill, cons
     }
   }
 }
+// The same parameter of vector v straight into registers.
+template <int VEC, bool EDGE>
+__device__ __forceinline__ void load_param(const float* param, float fill, const Place& p, int v,
+                                           F2* out) {
+  const int c = v * VEC - p.off;
+  if (!EDGE && param != nullptr && v < p.nvec && (reinterpret_cast<uintptr_t>(param) & 15u) == 0) {
+#pragma unroll
+    for (int j = 0; j < VEC / 4; ++j) {
+      const float4 q = __ldg(reinterpret_cast<const float4*>(param + c) + j);
+      out[2 * j] = f2(q.x, q.y), out[2 * j + 1] = f2(q.z, q.w);
+    }
+  } else {
+    float q[VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const bool in = c + j >= 0 && c + j < p.cols;
+      q[j] = !in ? 0.0f : (param != nullptr ? __ldg(param + c + j) : fill);
+    }
+#pragma unroll
+    for (int j = 0; j < VEC / 2; ++j) out[j] = f2(q[2 * j], q[2 * j + 1]);
+  }
+}
 template <int VEC>
 __device__ __forceinline__ void read_param(const float* from, int slots, int s, F2* out) {
 #pragma unroll
@@ -295,32 +319,35 @@ __device__ __forceinline__ void store_part(void* to, int e, int cols, uint4 r) {
 // rounded y: a group is 32 / VEC adjacent lanes (cols is a multiple of 32 and
 // rows are aligned, so a group never splits over warps).
 template <bool BF16, int NV, bool EDGE, bool MULTI, bool QUANT>
-__global__ void __launch_bounds__(ln_threads(BF16, NV), ln_blocks(BF16, NV))
+__global__ void __launch_bounds__(512)
     k_ln_fwd(const void* __restrict__ x, int64_t rows, int cols, int64_t ldx, int misaligned,
              const float* __restrict__ weight, const float* __restrict__ bias, float eps,
              void* __restrict__ y, float* __restrict__ mean_out, float* __restrict__ rstd_out,
              uint8_t* __restrict__ codes, uint8_t* __restrict__ scales, LnSplit split) {
   constexpr int VEC = BF16 ? 8 : 4, NP = VEC / 2, D = ln_depth(NV);
   using V = Vec<BF16, VEC>;
-  extern __shared__ __align__(16) uint4 ring[];  // [warps][D][NV][32], then w, b
+  extern __shared__ __align__(16) uint4 ring[];  // [warps][D][NV][32]
   __shared__ float2 red[2][kLnMaxParts];
   const Place p = place<VEC, NV, EDGE>(split, rows, cols, ldx, misaligned);
-  const int slots = p.W * NV * 32, s0 = p.w * NV * 32 + p.lane;
-  float* const sw = reinterpret_cast<float*>(ring + (blockDim.x >> 5) * (D * NV * 32));
-  float* const sb = sw + slots * VEC;
   uint4* const mine = ring + p.warp * (D * NV * 32) + p.lane;
 
   Walk wx = walk<BF16>(x, rows, ldx, p);
   int to_fetch = p.n;
+  int64_t f_row = p.row0;  // (a tensor's ends lie in its first and last row)
   auto fetch = [&](int d) {
     if (to_fetch > 0) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
-        if (p.v0 + 32 * i < p.nvec)
-          fetch_vec<BF16, EDGE>(mine + (d * NV + i) * 32, wx.at + 512 * i, wx.first, wx.end);
+        if (p.v0 + 32 * i < p.nvec) {
+          if (EDGE && (f_row == 0 || f_row == rows - 1))
+            fetch_vec<BF16, true>(mine + (d * NV + i) * 32, wx.at + 512 * i, wx.first, wx.end);
+          else
+            fetch_vec<BF16, false>(mine + (d * NV + i) * 32, wx.at + 512 * i, wx.first, wx.end);
+        }
     }
     cp_async_commit();
     wx.at += wx.step;
+    if (EDGE) f_row += p.stride;
     --to_fetch;
   };
   // vectors past the row's end are zeros that nothing overwrites
@@ -330,11 +357,14 @@ __global__ void __launch_bounds__(ln_threads(BF16, NV), ln_blocks(BF16, NV))
 #pragma unroll
       for (int d = 0; d < D; ++d) mine[(d * NV + i) * 32] = make_uint4(0, 0, 0, 0);
     }
-  stage_param<VEC, NV, EDGE>(weight, 1.0f, p, sw);
-  stage_param<VEC, NV, EDGE>(bias, 0.0f, p, sb);
-  cp_async_commit();
 #pragma unroll
   for (int d = 0; d < D; ++d) fetch(d);
+  F2 wk[NV * NP], bk[NV * NP];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    load_param<VEC, EDGE>(weight, 1.0f, p, p.v0 + 32 * i, wk + i * NP);
+    load_param<VEC, EDGE>(bias, 0.0f, p, p.v0 + 32 * i, bk + i * NP);
+  }
   uint8_t* to = static_cast<uint8_t*>(y) +
                 (p.row0 * cols + int64_t(p.v0) * VEC - p.off) * (BF16 ? 2 : 4);
   const int64_t to_step = p.stride * cols * (BF16 ? 2 : 4);
@@ -346,8 +376,6 @@ __global__ void __launch_bounds__(ln_threads(BF16, NV), ln_blocks(BF16, NV))
   const float my_inv = my_n > 0.0f ? __fdiv_rn(1.0f, my_n) : 0.0f;
   const float l_n = MULTI && l < parts ? part_count<VEC, NV>(p, l) : 0.0f;
   const float l_inv = l_n > 0.0f ? __fdiv_rn(1.0f, l_n) : 0.0f;
-  cp_async_wait<D>();  // the parameters
-  __syncthreads();
 
   // the cluster's CTAs walk the same rows; so do the warps of a group
   int d = 0, par = 0;
@@ -398,7 +426,7 @@ __global__ void __launch_bounds__(ln_threads(BF16, NV), ln_blocks(BF16, NV))
         pair_sync();
       } else {
         if (p.lane == 0) rd[p.warp] = make_float2(s, m2);
-        group_sync(p.g, p.W);
+        group_sync<kLnFwdWarps / 2>(p.g, p.W);
       }
       const float2 o = l < parts ? rd[p.g * p.W + l] : make_float2(0.0f, 0.0f);
       mean = __fmul_rn(part_sum(o.x, p.P), inv_n);
@@ -410,20 +438,17 @@ __global__ void __launch_bounds__(ln_threads(BF16, NV), ln_blocks(BF16, NV))
       if (mean_out != nullptr) mean_out[row] = mean;
       if (rstd_out != nullptr) rstd_out[row] = rstd;
     }
-    // h = x rstd - mean rstd: the product's rounding is of the size that the
-    // mean's own rounding brings
-    const float shift = -__fmul_rn(mean, rstd);
-    const F2 nm = f2(shift, shift), rs = f2(rstd, rstd);
+    // (x - mean) rstd, not x rstd - mean rstd: rows of one value stay at b
+    const F2 nm = f2(-mean, -mean), rs = f2(rstd, rstd);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int v = p.v0 + 32 * i;
       const bool in = v < p.nvec;
       if (!QUANT && !in) continue;
-      F2 o[NP], wv[NP], bv[NP];
-      read_param<VEC>(sw, slots, s0 + 32 * i, wv);
-      read_param<VEC>(sb, slots, s0 + 32 * i, bv);
+      F2 o[NP];
 #pragma unroll
-      for (int j = 0; j < NP; ++j) o[j] = fma2(fma2(a[i * NP + j], rs, nm), wv[j], bv[j]);
+      for (int j = 0; j < NP; ++j)
+        o[j] = fma2(mul2(add2(a[i * NP + j], nm), rs), wk[i * NP + j], bk[i * NP + j]);
       V out;
       out.pack(o);
       if (in && y != nullptr) {
@@ -565,6 +590,7 @@ __global__ void __launch_bounds__(512)
              const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
              void* __restrict__ dx, float* __restrict__ partial, LnSplit split) {
   constexpr int VEC = BF16 ? 8 : 4, NP = VEC / 2, D = ln_depth(NV);
+  constexpr bool kW = NV == 1;
   using V = Vec<BF16, VEC>;
   extern __shared__ __align__(16) uint4 ring[];  // [warps][D][2 NV][32], then w
   __shared__ float2 red[2][kLnMaxParts];
@@ -575,17 +601,25 @@ __global__ void __launch_bounds__(512)
 
   Walk wx = walk<BF16>(x, rows, ldx, p), wg = walk<BF16>(dy, rows, lddy, p);
   int to_fetch = p.n;
+  int64_t f_row = p.row0;  // (a tensor's ends lie in its first and last row)
   auto fetch = [&](int d) {
     if (to_fetch > 0) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (p.v0 + 32 * i < p.nvec) {
-          fetch_vec<BF16, EDGE>(mine + (d * NV + i) * 64, wx.at + 512 * i, wx.first, wx.end);
-          fetch_vec<BF16, EDGE>(mine + (d * NV + i) * 64 + 32, wg.at + 512 * i, wg.first, wg.end);
+          uint4* const to = mine + (d * NV + i) * 64;
+          if (EDGE && (f_row == 0 || f_row == rows - 1)) {
+            fetch_vec<BF16, true>(to, wx.at + 512 * i, wx.first, wx.end);
+            fetch_vec<BF16, true>(to + 32, wg.at + 512 * i, wg.first, wg.end);
+          } else {
+            fetch_vec<BF16, false>(to, wx.at + 512 * i, wx.first, wx.end);
+            fetch_vec<BF16, false>(to + 32, wg.at + 512 * i, wg.first, wg.end);
+          }
         }
     }
     cp_async_commit();
     wx.at += wx.step, wg.at += wg.step;
+    if (EDGE) f_row += p.stride;
     --to_fetch;
   };
   // vectors past the row's end are zeros that nothing overwrites
@@ -596,10 +630,12 @@ __global__ void __launch_bounds__(512)
       for (int d = 0; d < D; ++d)
         mine[(d * NV + i) * 64] = mine[(d * NV + i) * 64 + 32] = make_uint4(0, 0, 0, 0);
     }
-  stage_param<VEC, NV, EDGE>(weight, 1.0f, p, sw);
+  if constexpr (!kW) stage_param<VEC, NV, EDGE>(weight, 1.0f, p, sw);
   cp_async_commit();
 #pragma unroll
   for (int d = 0; d < D; ++d) fetch(d);
+  F2 wk[kW ? NP : 1];
+  if constexpr (kW) load_param<VEC, EDGE>(weight, 1.0f, p, p.v0, wk);
   uint8_t* to = static_cast<uint8_t*>(dx) +
                 (p.row0 * cols + int64_t(p.v0) * VEC - p.off) * (BF16 ? 2 : 4);
   const int64_t to_step = p.stride * cols * (BF16 ? 2 : 4);
@@ -615,8 +651,10 @@ __global__ void __launch_bounds__(512)
   float nmean = 0.0f, nrstd = 0.0f;
   const float *mp = mean_in + p.row0, *rp = rstd_in + p.row0;
   if (p.n > 0) nmean = __ldg(mp), nrstd = __ldg(rp);
-  cp_async_wait<D>();  // the weight
-  __syncthreads();
+  if constexpr (!kW) {
+    cp_async_wait<D>();  // the weight
+    __syncthreads();
+  }
 
   int d = 0, par = 0;
   for (int left = p.n; left > 0; --left, par ^= 1) {
@@ -649,7 +687,10 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       F2 wv[NP];
-      read_param<VEC>(sw, slots, s0 + 32 * i, wv);
+      if constexpr (!kW) read_param<VEC>(sw, slots, s0 + 32 * i, wv);
+      if constexpr (kW)
+#pragma unroll
+        for (int j = 0; j < NP; ++j) wv[j] = wk[j];
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         const int k = i * NP + j;
@@ -672,13 +713,14 @@ __global__ void __launch_bounds__(512)
         pair_sync();
       } else {
         if (p.lane == 0) rd[p.warp] = make_float2(s1, s2);
-        group_sync(p.g, p.W);
+        group_sync<kLnBwdWarps / 2>(p.g, p.W);
       }
       const float2 o = l < parts ? rd[p.g * p.W + l] : make_float2(0.0f, 0.0f);
       s1 = part_sum(o.x, p.P);
       s2 = part_sum(o.y, p.P);
     }
-    const float m1 = -__fmul_rn(s1, inv_n), m2 = -__fmul_rn(s2, inv_n);
+    // dx = g rstd - (c1 + h c2) rstd / n
+    const float ri = -__fmul_rn(rstd, inv_n), m1 = __fmul_rn(s1, ri), m2 = __fmul_rn(s2, ri);
     const F2 k1 = f2(m1, m1), k2 = f2(m2, m2);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -688,7 +730,7 @@ __global__ void __launch_bounds__(512)
 #pragma unroll
       for (int j = 0; j < NP; ++j) {
         const int k = i * NP + j;
-        o[j] = mul2(add2(fma2(h[k], k2, g[k]), k1), rs);
+        o[j] = fma2(h[k], k2, fma2(g[k], rs, k1));
       }
       V out;
       out.pack(o);
@@ -823,29 +865,26 @@ struct LnShape {
 };
 
 int sm_count() {
-  int dev = 0, sms = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess)
-    cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms;
+  static thread_local int known_dev = -1, known = 148;
+  int dev = 0;
+  if (cudaGetDevice(&dev) == cudaSuccess && dev != known_dev) {
+    cudaDeviceGetAttribute(&known, cudaDevAttrMultiProcessorCount, dev);
+    known_dev = dev;
+  }
+  return known;
 }
 
-// Vectors per thread (one of nvs, ascending) and warps per row. Where one
-// warp can hold a row it does, with the fewest vectors (no barrier, and the
-// work per row that does not grow with its length is done once); longer rows
-// take the largest count while that needs at most four warps, else the one
-// before it, and a cluster of two CTAs where 16 warps are not enough. Few
-// rows (less than two an SM) spread over the most warps. Rows that need less
-// than a CTA of `block_warps` warps share one.
-bool ln_shape(int64_t nvec, const int (&nvs)[3], int64_t rows, int block_warps, LnShape* s) {
+// Vectors per thread and warps per row: `big` vectors (whose parameters still
+// fit in registers), one where a warp then holds a row, or where rows are few
+// (less than two an SM: one vector a thread spreads a row over the most
+// threads). Rows that 16 warps cannot hold take a cluster of two CTAs. Rows
+// that need less than a CTA of `block_warps` warps share one.
+// 12608 x 1536 bf16, forward: 24 elements a thread 14.8 us, 48 (one warp a
+// row, parameters in shared memory, whose bandwidth then binds) 20.2 us.
+bool ln_shape(int64_t nvec, int big, int64_t rows, int block_warps, LnShape* s) {
   const bool few = rows < 2 * int64_t(sm_count());
-  auto warps = [&](int i) { return (nvec + 32 * nvs[i] - 1) / (32 * nvs[i]); };
-  int i = warps(2) <= 4 ? 2 : 1;
-  if (few && warps(0) <= kLnMaxWarps) i = 0;
-  if (!few || warps(0) == 1)
-    for (int j = 2; j >= 0; --j)
-      if (warps(j) == 1) i = j;
-  int64_t W = warps(i);
-  s->nv = nvs[i];
+  s->nv = nvec <= 32 || (few && nvec <= 32 * kLnMaxWarps) ? 1 : big;
+  int64_t W = (nvec + 32 * s->nv - 1) / (32 * s->nv);
   s->split.CS = 1;
   if (W > kLnMaxWarps) {
     s->split.CS = 2;
@@ -923,8 +962,7 @@ cudaError_t fwd_launch(const FwdArgs& a, const LnShape& sh, int misaligned) {
   constexpr int VEC = BF16 ? 8 : 4;
   auto kern = k_ln_fwd<BF16, NV, EDGE, MULTI, QUANT>;
   const void* k = reinterpret_cast<const void*>(kern);
-  const size_t smem = size_t(sh.threads) * NV * 16 * ln_depth(NV) +
-                      size_t(sh.split.W) * NV * 32 * VEC * 8;
+  const size_t smem = size_t(sh.threads) * NV * 16 * ln_depth(NV);
   const cudaError_t e = allow_smem(k, smem);
   if (e != cudaSuccess) return e;
   const int grid = ln_grid(k, sh, smem, a.rows, EDGE, VEC, int64_t(1) << 30);
@@ -942,7 +980,7 @@ cudaError_t fwd_nv(const FwdArgs& a, const LnShape& sh, bool edge, int misaligne
 template <bool BF16>
 cudaError_t fwd_any(const FwdArgs& a) {
   constexpr int kSize = BF16 ? 2 : 4, VEC = 16 / kSize;
-  constexpr int kNv[3] = {1, BF16 ? 3 : 4, BF16 ? 6 : 8};
+  constexpr int kBig = BF16 ? 3 : 4;
   LnShape sh;
   bool edge;
   int mis;
@@ -950,16 +988,13 @@ cudaError_t fwd_any(const FwdArgs& a) {
   const int64_t lds[] = {a.ldx, a.cols};
   if (a.cols <= kLnMaxCols && vector_rows(ptrs, lds, 2, a.cols, kSize, &edge, &mis) &&
       !(edge && a.codes != nullptr) &&
-      ln_shape((a.cols + VEC - 1) / VEC + (edge ? 1 : 0), kNv, a.rows, 8, &sh)) {
+      ln_shape((a.cols + VEC - 1) / VEC + (edge ? 1 : 0), kBig, a.rows, kLnFwdWarps, &sh)) {
     const bool multi = sh.split.W * sh.split.CS > 1;
-    if (sh.nv == kNv[0])
-      return multi ? fwd_nv<BF16, kNv[0], true>(a, sh, edge, mis)
-                   : fwd_nv<BF16, kNv[0], false>(a, sh, edge, mis);
-    if (sh.nv == kNv[1])
-      return multi ? fwd_nv<BF16, kNv[1], true>(a, sh, edge, mis)
-                   : fwd_nv<BF16, kNv[1], false>(a, sh, edge, mis);
-    return multi ? fwd_nv<BF16, kNv[2], true>(a, sh, edge, mis)
-                 : fwd_nv<BF16, kNv[2], false>(a, sh, edge, mis);
+    if (sh.nv == 1)
+      return multi ? fwd_nv<BF16, 1, true>(a, sh, edge, mis)
+                   : fwd_nv<BF16, 1, false>(a, sh, edge, mis);
+    return multi ? fwd_nv<BF16, kBig, true>(a, sh, edge, mis)
+                 : fwd_nv<BF16, kBig, false>(a, sh, edge, mis);
   }
   auto kern = k_ln_fwd_wide<BF16>;
   const int grid =
@@ -1022,14 +1057,14 @@ template <bool BF16>
 cudaError_t bwd_any(const BwdArgs& a) {
   constexpr int kSize = BF16 ? 2 : 4, VEC = 16 / kSize;
   // at most 16 elements a thread: two sums for each stay in registers
-  constexpr int kBig = BF16 ? 2 : 4, kNv[3] = {1, kBig, kBig};
+  constexpr int kBig = BF16 ? 2 : 4;
   LnShape sh;
   bool edge;
   int mis;
   const void* const ptrs[] = {a.x, a.dy, a.dx};
   const int64_t lds[] = {a.ldx, a.lddy, a.cols};
   if (a.cols <= kLnMaxCols && vector_rows(ptrs, lds, 3, a.cols, kSize, &edge, &mis) &&
-      ln_shape((a.cols + VEC - 1) / VEC + (edge ? 1 : 0), kNv, a.rows, 8, &sh)) {
+      ln_shape((a.cols + VEC - 1) / VEC + (edge ? 1 : 0), kBig, a.rows, kLnBwdWarps, &sh)) {
     const bool multi = sh.split.W * sh.split.CS > 1;
     if (sh.nv == 1)
       return multi ? bwd_nv<BF16, 1, true>(a, sh, edge, mis)

@@ -1174,8 +1174,13 @@ cudaError_t allow_smem(const void* kernel, size_t bytes) {
   cudaGetDevice(&dev);
   Entry& c = cache[(reinterpret_cast<uintptr_t>(kernel) >> 4) % kEntries];
   if (c.kernel == kernel && c.dev == dev && c.bytes >= bytes) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(
+  cudaError_t e = cudaFuncSetAttribute(
       kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  // all of the SM's on-chip memory that can be shared memory: the default
+  // split otherwise follows one CTA's need and holds fewer CTAs
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                             int(cudaSharedmemCarveoutMaxShared));
   if (e == cudaSuccess) c = {kernel, dev, bytes};
   return e;
 }
