@@ -7,6 +7,7 @@ There is no fallback: if the library is missing, or a tensor is not on a CUDA
 device, the call raises.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -425,12 +426,17 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+_entry = {}   # entry points by name, as they are first called
+
+
 def _call(name, device, stream, *args):
     """Call the entry point `name` on `stream` (by default the current stream
     of `device`) with `device` as the current one, where its launches go."""
+    fn = _entry.get(name)
+    if fn is None:
+        fn = _entry[name] = getattr(lib(), name)
     i = device.index
     s = torch._C._cuda_getCurrentRawStream(i) if stream is None else stream.cuda_stream
-    fn = getattr(lib(), name)
     if torch._C._cuda_getDevice() == i:
         status = fn(*args, s)
     else:
@@ -438,6 +444,20 @@ def _call(name, device, stream, *args):
             status = fn(*args, s)
     if status != 0:
         raise Mxfp4Error(status, name)
+
+
+def _f32(t, name, n, device):
+    """_buffer for fp32, whose usual answer costs less."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.is_contiguous()
+            and t.numel() == n and t.is_cuda and t.device == device):
+        _buffer(t, name, torch.float32, n, device)
+
+
+def _like(x):
+    """A new contiguous tensor of x's shape and type."""
+    if x.is_contiguous():
+        return torch.empty_like(x)
+    return torch.empty(x.shape, dtype=x.dtype, device=x.device)
 
 
 def _rows2d(t, name):
@@ -483,11 +503,10 @@ def gemv(x, b_codes, b_blocked, out_dtype=torch.bfloat16, out=None, workspace=No
         raise TypeError("x must be bfloat16")
     m, k = x.shape
     d = x.device
-    _cuda2d(b_codes, "b_codes")
+    if not isinstance(b_codes, torch.Tensor) or b_codes.dim() != 2 or b_codes.shape[1] * 2 != k:
+        raise ValueError("b_codes must be a 2-D tensor with k/2 bytes per row")
     n = b_codes.shape[0]
     _buffer(b_codes, "b_codes", torch.uint8, n * k // 2, d)
-    if b_codes.shape[1] * 2 != k:
-        raise ValueError("b_codes must have k/2 bytes per row")
     _buffer(b_blocked, "b_blocked", torch.uint8, -(-n // 128) * 128 * (-(-k // 128) * 4), d)
     if out is None:
         out = torch.empty((m, n), dtype=out_dtype, device=d)
@@ -495,7 +514,7 @@ def gemv(x, b_codes, b_blocked, out_dtype=torch.bfloat16, out=None, workspace=No
         _buffer(out, "out", out.dtype, m * n, d)
         _apart(out, "out", x)
     st = None if status is None else _addr(_buffer(status, "status", torch.int32, 1, d))
-    need = lib().mxfp4_gemv_workspace(m, n, k)
+    need = _workspace_size("mxfp4_gemv_workspace", m, n, k)
     workspace = _workspace(workspace, need, d) if need > 0 else None
     _call("mxfp4_gemv", d, stream, x.data_ptr(), m, n, k, ldx, b_codes.data_ptr(),
           b_blocked.data_ptr(), out.data_ptr(), _dtype_code(out), _addr(workspace), max(need, 0),
@@ -505,11 +524,11 @@ def gemv(x, b_codes, b_blocked, out_dtype=torch.bfloat16, out=None, workspace=No
 
 def _norm_inputs(x, weight, bias):
     ldx = _rows2d(x, "x")
-    dt = _dtype_code(x)
-    for name, t in (("weight", weight), ("bias", bias)):
-        if t is not None:
-            _buffer(t, name, torch.float32, x.shape[1], x.device)
-    return ldx, dt
+    if weight is not None:
+        _f32(weight, "weight", x.shape[1], x.device)
+    if bias is not None:
+        _f32(bias, "bias", x.shape[1], x.device)
+    return ldx, _dtype_code(x)
 
 
 def layernorm(x, weight=None, bias=None, eps=1e-5, want_stats=False, out=None, stream=None):
@@ -522,10 +541,10 @@ def layernorm(x, weight=None, bias=None, eps=1e-5, want_stats=False, out=None, s
     d = x.device
     mean = rstd = None
     if out is None:
-        out = y = torch.empty((R, C), dtype=x.dtype, device=d)
+        out = y = _like(x)
         if want_stats:
-            mean, rstd = (torch.empty(R, dtype=torch.float32, device=d),
-                          torch.empty(R, dtype=torch.float32, device=d))
+            mean = torch.empty(R, dtype=torch.float32, device=d)
+            rstd = torch.empty_like(mean)
             out = (y, mean, rstd)
     else:
         y = out
@@ -574,6 +593,13 @@ def layernorm_quantize(x, weight=None, bias=None, eps=1e-5, want_y=False, want_s
     return out
 
 
+@functools.lru_cache(maxsize=4096)
+def _workspace_size(name, *shape):
+    """Bytes that the entry point `name` needs for a shape (its _workspace
+    function: host arithmetic, the same answer every time)."""
+    return getattr(lib(), name)(*shape)
+
+
 def _workspace(workspace, need, device):
     """A caller's workspace (uint8, at least `need` bytes) or a new one."""
     if workspace is None:
@@ -593,17 +619,18 @@ def layernorm_backward(dy, x, mean, rstd, weight=None, want_params=True, out=Non
     lddy = _rows2d(dy, "dy")
     if dy.dtype != x.dtype or dy.shape != x.shape:
         raise ValueError("dy must have the type and shape of x")
-    _on_device(dy, "dy", x.device)
     R, C = x.shape
     d = x.device
-    _buffer(mean, "mean", torch.float32, R, d)
-    _buffer(rstd, "rstd", torch.float32, R, d)
+    _on_device(dy, "dy", d)
+    _f32(mean, "mean", R, d)
+    _f32(rstd, "rstd", R, d)
     dw = db = None
     if out is None:
-        out = dx = torch.empty((R, C), dtype=x.dtype, device=d)
+        out = dx = _like(x)
         if want_params:
-            dw, db = (torch.empty(C, dtype=torch.float32, device=d),
-                      torch.empty(C, dtype=torch.float32, device=d))
+            dw = (torch.empty(C, dtype=torch.float32, device=d) if weight is None
+                  else torch.empty_like(weight))
+            db = torch.empty_like(dw)
             out = (dx, dw, db)
     else:
         dx = out
@@ -615,7 +642,8 @@ def layernorm_backward(dy, x, mean, rstd, weight=None, want_params=True, out=Non
         _apart(dx, "out", x, dy)
     size = 0
     if want_params:
-        workspace = _workspace(workspace, lib().mxfp4_layernorm_backward_workspace(R, C), d)
+        workspace = _workspace(workspace, _workspace_size("mxfp4_layernorm_backward_workspace", R, C),
+                               d)
         size = workspace.numel()
     else:
         workspace = None
@@ -643,7 +671,7 @@ def newton_schulz(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=
         if out.data_ptr() != g.data_ptr() or out.dtype != g.dtype:
             _apart(out, "out", g)
     odt = _dtype_code(out)
-    need = lib().mxfp4_newton_schulz_workspace(R, C)
+    need = _workspace_size("mxfp4_newton_schulz_workspace", R, C)
     workspace = _workspace(workspace, need, d)
     st = None if status is None else _addr(_buffer(status, "status", torch.int32, 1, d))
     a, b, c = coeffs

@@ -932,6 +932,10 @@ int ln_grid(const void* kern, const LnShape& sh, size_t smem, int64_t rows, bool
 template <typename... P, typename... A>
 cudaError_t ln_launch(void (*kern)(P...), int grid, const LnShape& sh, size_t smem,
                       cudaStream_t s, A... args) {
+  if (sh.split.CS == 1) {
+    kern<<<unsigned(grid), unsigned(sh.threads), smem, s>>>(args...);
+    return cudaGetLastError();
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(unsigned(grid));
   cfg.blockDim = dim3(unsigned(sh.threads));
@@ -942,7 +946,7 @@ cudaError_t ln_launch(void (*kern)(P...), int grid, const LnShape& sh, size_t sm
   at[0].val.clusterDim.x = unsigned(sh.split.CS);
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = sh.split.CS > 1 ? 1 : 0;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
