@@ -8,7 +8,7 @@
 // Bound by the tensor cores: with s <= l the sides, a step costs s s l flops
 // for A (half of a symmetric product), s^3 for A A (half) and 2 s s l for
 // B X. Three products a step, each a persistent tcgen05 GEMM with a fused
-// epilogue (a launch each, or all in one launch for small matrices); only the tiles on and above the diagonal of A and B are computed
+// epilogue; only the tiles on and above the diagonal of A and B are computed
 // and written to both sides.
 //
 // Numbers: operands are fp16, not bf16, at the same tensor rate and with
@@ -40,6 +40,7 @@ constexpr int kSEpiWarps = 8;
 constexpr int kSThreads = 32 * (3 + kSEpiWarps);  // A loads, MMA, epilogue, B loads
 constexpr int kSLoadB = 2 + kSEpiWarps;           // the warp of the B loads
 constexpr int kNsPartials = 592;    // partial sums of the norm
+constexpr int64_t kNsPairTiles = 120;  // fewest tiles for CTA pairs
 
 // What a product's epilogue does.
 enum NsMode { kGram = 0, kSquare = 1, kStep = 2, kLast = 3 };
@@ -56,9 +57,11 @@ struct NsArgs {
   int* status;
 };
 
+__host__ __device__ constexpr int ns_acc(int bn) { return 256 / bn; }
+
 template <int BN>
 struct NsLayout {
-  static constexpr int kStages = BN == 256 ? 4 : (BN == 128 ? 6 : 8);
+  static constexpr int kStages = BN == 128 ? 6 : 8;
   static constexpr uint32_t kA = kSM * 128, kB = BN * 128;
   static constexpr uint32_t kBOff = kStages * kA;
   // per epilogue warp: 32 rows x 32 fp16, rows 80 bytes apart (no bank twice)
@@ -68,7 +71,7 @@ struct NsLayout {
   // Accumulators of a tile: consecutive MMAs on one wait for each other, about
   // 150 clocks, which 128 x 256 products cover and narrower ones do not; the
   // four MMAs of a stage take turns, and the epilogue adds. Two tiles' worth.
-  static constexpr int kAcc = 256 / BN;
+  static constexpr int kAcc = ns_acc(BN);
   static constexpr uint32_t kTmemCols = 512;
   // kind::f16: fp32 accumulator, fp16 operands (0), majorness bits 15, 16
   __host__ __device__ static constexpr uint32_t idesc(bool a_mn, bool b_mn) {
@@ -228,7 +231,6 @@ __device__ __forceinline__ bool ns_epilogue(const NsArgs& p, int64_t row, int64_
   struct Chunk {
     uint4 hi[4], lo[4];
   };
-  // (from L2: in the fused kernel other SMs rewrite these buffers)
   auto fetch = [&](Chunk& f, int64_t c0) {
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
@@ -256,7 +258,7 @@ __device__ __forceinline__ bool ns_epilogue(const NsArgs& p, int64_t row, int64_
       if (cb + 32 < kCols) fetch(next, c0 + 32);
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-    for (int a = 1; a < NsLayout<BN>::kAcc; ++a) {
+    for (int a = 1; a < ns_acc(BN); ++a) {
       uint32_t u[32];
       MXFP4_TMEM_LD32(u, tb + cb + a * BN);
       asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
@@ -594,6 +596,257 @@ __global__ void __launch_bounds__(kSThreads, 1)
                  "r"(L::kTmemCols));
 }
 
+// ---------------------------------------------------------------------------
+// 256 x 256 tiles by pairs of CTAs (tcgen05 cta_group::2). With one CTA a tile
+// of 128 x 256 an SM takes in 48 KB for 512 clocks of MMAs, more than its port
+// to L2 delivers (64 bytes a clock): the loads alone took 3.1 of 4.0 ms on
+// 4096 x 14336. In a pair each CTA loads its 128 rows of A and half of B's
+// 256, 32 KB a stage, and the tensor cores of both read both halves. The CTA
+// of rank 0 leads: it issues the MMAs for both, and the stages' barriers are
+// its own; the loads of both CTAs complete on them, and its commits arrive in
+// both CTAs.
+// ---------------------------------------------------------------------------
+
+struct PairLayout {
+  static constexpr int kStages = 6;
+  static constexpr uint32_t kA = kSM * 128, kB = kSM * 128;
+  static constexpr uint32_t kBOff = kStages * kA;
+  static constexpr uint32_t kEpiOff = kBOff + kStages * kB;
+  static constexpr uint32_t kBarOff = kEpiOff + kSEpiWarps * 32 * 80;
+  static constexpr uint32_t kBytes = kBarOff + 256;
+  __host__ __device__ static constexpr uint32_t idesc(bool a_mn, bool b_mn) {
+    return (1u << 4) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
+           (uint32_t(256 >> 3) << 17) | (uint32_t(256 >> 4) << 24);
+  }
+};
+
+// The address of the same shared-memory byte in the CTA of rank `rank`.
+__device__ __forceinline__ uint32_t peer_addr(const void* p, uint32_t rank) {
+  uint32_t d;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(smem_u32(p)), "r"(rank));
+  return d;
+}
+__device__ __forceinline__ void pair_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
+               "barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A load into this CTA's shared memory that completes on the barrier at
+// cluster address `bar`, which may be the other CTA's.
+__device__ __forceinline__ void pair_load(void* dst, const CUtensorMap* map, int x, int y,
+                                          uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3}], [%4];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void pair_mma(uint32_t tmem_c, uint64_t adesc, uint64_t bdesc,
+                                         uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(tmem_c),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate));
+}
+// Arrive on the barrier at bar's offset in both CTAs once this thread's MMAs
+// have completed.
+__device__ __forceinline__ void pair_commit(unsigned long long* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+      "[%0], %1;" ::"r"(smem_u32(bar)),
+      "h"(uint16_t(3)));
+}
+
+template <bool A_MN, bool B_MN, int MODE>
+__global__ void __launch_bounds__(kSThreads, 1)
+    k_ns_pair(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+              const NsArgs p) {
+  using L = PairLayout;
+  constexpr bool kSym = MODE == kGram || MODE == kSquare;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  unsigned long long* full = reinterpret_cast<unsigned long long*>(sm + L::kBarOff);
+  unsigned long long* empty = full + L::kStages;
+  unsigned long long* acc_full = empty + L::kStages;  // two accumulators
+  unsigned long long* acc_empty = acc_full + 2;
+  unsigned long long* drain = acc_empty + 2;
+  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drain + 1);
+  int* failed = reinterpret_cast<int*>(tmem_base + 1);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
+  uint32_t rank;
+  asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+  const int64_t mt = (p.m + 255) / 256, nt = (p.n + 255) / 256;
+  const int64_t n_tiles = kSym ? nt * (nt + 1) / 2 : mt * nt;
+  const int64_t first = blockIdx.x / 2, step = gridDim.x / 2;
+  const int n_kb = int((p.k + kSK - 1) / kSK);
+  // rows of this CTA and columns of the pair
+  auto tile_at = [&](int64_t t, int64_t& m0, int64_t& n0) {
+    int64_t i, j;
+    if constexpr (kSym) {
+      // column j of the upper triangle has j + 1 tiles; the longest first
+      for (j = nt - 1; t > j; --j) t -= j + 1;
+      i = t;
+    } else {
+      constexpr int64_t G = 8;  // row tiles swept together (their panels stay in L2)
+      const int64_t per = G * nt, g = t / per, r = t % per;
+      const int64_t gm = mt - g * G < G ? mt - g * G : G;
+      i = g * G + r % gm, j = r / gm;
+    }
+    m0 = i * 256 + int64_t(rank) * kSM, n0 = j * 256;
+  };
+  auto fail = [&] {
+    // both CTAs of the pair give up together
+    atomicExch(failed, 1);
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(peer_addr(failed, rank ^ 1u)), "r"(1)
+                 : "memory");
+  };
+
+  if (tid == 0) {
+    for (int s = 0; s < L::kStages; ++s) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&full[s])));
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&empty[s])));
+    }
+    for (int s = 0; s < 2; ++s) {
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&acc_full[s])));
+      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&acc_empty[s])),
+                   "r"(2 * kSEpiWarps));
+    }
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(drain)));
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    *failed = 0;
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_base)),
+                 "r"(512));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;");
+  __syncthreads();
+  pair_sync();  // barriers and tensor memory of both CTAs are ready
+  asm volatile("tcgen05.fence::after_thread_sync;");
+  const uint32_t tmem = *tmem_base;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+
+  if (warp == 0 || warp == kSLoadB) {
+    // A's warp of the leading CTA announces the whole stage: four loads of
+    // 16 KB (a load may complete before that: the count goes below zero)
+    const bool is_a = warp == 0, lead = elect_one();
+    const CUtensorMap* const map = is_a ? &tm_a : &tm_b;
+    const bool mn = is_a ? A_MN : B_MN;
+    uint8_t* const base = is_a ? sm : sm + L::kBOff;
+    uint32_t s = 0, ph = 0;
+    bool ok = true;
+    for (int64_t t = first; t < n_tiles && ok; t += step) {
+      int64_t m0, n0;
+      tile_at(t, m0, n0);
+      const int row0 = int(is_a ? m0 : n0 + int64_t(rank) * kSM);
+      for (int kb = 0; kb < n_kb; ++kb) {
+        if (!warp_wait(&empty[s], ph ^ 1u, failed)) {
+          ok = false;
+          break;
+        }
+        const uint32_t bar = peer_addr(&full[s], 0);
+        uint8_t* const to = base + s * L::kA;
+        const int k0 = kb * kSK;
+        if (lead) {
+          if (is_a && rank == 0) expect_tx(&full[s], 2 * (L::kA + L::kB));
+          if (mn) {
+            pair_load(to, map, row0, k0, bar);
+            pair_load(to + 8192, map, row0 + 64, k0, bar);
+          } else {
+            pair_load(to, map, k0, row0, bar);
+          }
+        }
+        if (++s == L::kStages) s = 0, ph ^= 1u;
+      }
+      ok = ok && __all_sync(0xFFFFFFFFu, !failed_flag(failed));
+    }
+    if (!ok) {
+      // loads may be in flight that no barrier here accounts for any more:
+      // give them a millisecond to land
+      fail();
+      for (int i = 0; i < 1000; ++i) __nanosleep(1000);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    if (rank == 0) {
+      const bool lead = elect_one();
+      const uint64_t a0 = A_MN ? smem_desc_mn(sm) : smem_desc_sw128(sm);
+      const uint64_t b0 = B_MN ? smem_desc_mn(sm + L::kBOff) : smem_desc_sw128(sm + L::kBOff);
+      constexpr uint32_t ka = A_MN ? 128u : 2u, kb_ = B_MN ? 128u : 2u;
+      uint32_t s = 0, ph = 0, ti = 0;
+      bool ok = true;
+      for (int64_t t = first; t < n_tiles && ok; t += step, ++ti) {
+        const uint32_t buf = ti & 1, bph = (ti >> 1) & 1u;
+        if (!warp_wait(&acc_empty[buf], bph ^ 1u, failed)) {
+          ok = false;
+          break;
+        }
+        asm volatile("tcgen05.fence::after_thread_sync;");
+        const uint32_t acc = tmem + buf * 256;
+        for (int kb = 0; kb < n_kb; ++kb) {
+          if (!warp_wait(&full[s], ph, failed)) {
+            ok = false;
+            break;
+          }
+          asm volatile("tcgen05.fence::after_thread_sync;");
+          const uint64_t ad = a0 + s * (L::kA >> 4), bd = b0 + s * (L::kB >> 4);
+          unsigned long long* const bar = &empty[s];
+          if (lead) {
+#pragma unroll
+            for (uint32_t j = 0; j < kSK / 16; ++j)
+              pair_mma(acc, ad + j * ka, bd + j * kb_, L::idesc(A_MN, B_MN),
+                       (kb > 0 || j > 0) ? 1u : 0u);
+            pair_commit(bar);
+          }
+          if (++s == L::kStages) s = 0, ph ^= 1u;
+        }
+        if (lead) pair_commit(&acc_full[buf]);
+        __syncwarp();
+      }
+      if (!ok) fail();
+      // every MMA issued has completed, and with them every load of both CTAs
+      if (lead)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                smem_u32(drain)));
+      __syncwarp();
+      if (!wait_parity(drain, 0)) fail();
+      __syncwarp();
+    }
+  } else {
+    const int q = warp & 3, half = (warp - 2) >> 2;
+    int64_t ti = 0;
+    for (int64_t t = first; t < n_tiles; t += step, ++ti) {
+      int64_t m0, n0;
+      tile_at(t, m0, n0);
+      const uint32_t buf = uint32_t(ti & 1), bph = uint32_t(ti >> 1) & 1u;
+      const bool ok = ns_epilogue<256, MODE, kSym>(
+          p, m0 + 32 * q + lane, n0 + 128 * half,
+          tmem + buf * 256 + (uint32_t(32 * q) << 16) + uint32_t(128 * half),
+          sm + L::kEpiOff + (warp - 2) * (32 * 80), &acc_full[buf], bph, failed);
+      if (lane == 0) {
+        if (ok)
+          asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(
+                           peer_addr(&acc_empty[buf], 0))
+                       : "memory");
+        else
+          fail();
+      }
+      __syncwarp();
+    }
+  }
+  asm volatile("tcgen05.fence::before_thread_sync;");
+  __syncthreads();
+  pair_sync();  // neither CTA ends while the other's MMAs, loads or arrivals reach it
+  report_failure(p.status, failed);
+  if (warp == 1)
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
 // Sum of the squares of G in fp64: partial[b] over this CTA's elements.
 template <bool BF16>
 __device__ __forceinline__ float ns_load(const void* g, int64_t i) {
@@ -602,9 +855,7 @@ __device__ __forceinline__ float ns_load(const void* g, int64_t i) {
 }
 template <bool BF16>
 __global__ void __launch_bounds__(256)
-    k_ns_norm(const void* __restrict__ g, int64_t n, double* __restrict__ partial,
-              unsigned* __restrict__ counter) {
-  if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;
+    k_ns_norm(const void* __restrict__ g, int64_t n, double* __restrict__ partial) {
   constexpr int VEC = BF16 ? 8 : 4;
   __shared__ double sh[8];
   double s = 0.0;
@@ -638,15 +889,16 @@ __global__ void __launch_bounds__(256)
   }
 }
 
-// X = 2^12 G / (|G|_F + eps) as hi + lo, pitch ld, by all threads of the
-// grid. Every CTA adds the partial sums itself, in one order; f: two floats
-// of shared memory.
+// X = 2^12 G / (|G|_F + eps) as hi + lo, pitch ld. Every CTA adds the
+// partial sums itself, in one order.
 template <bool BF16>
-__device__ __forceinline__ void ns_start(const void* __restrict__ g, int64_t rows, int64_t cols,
-                                         int64_t ld, float eps,
-                                         const double* __restrict__ partial, int n_partial,
-                                         __half* __restrict__ hi, __half* __restrict__ lo,
-                                         float* f) {
+__global__ void __launch_bounds__(256)
+    k_ns_start(const void* __restrict__ g, int64_t rows, int64_t cols, int64_t ld, float eps,
+               const double* __restrict__ partial, int n_partial, __half* __restrict__ hi,
+               __half* __restrict__ lo) {
+  __shared__ float f[2];
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x < 32) {
     double s = 0.0;
     for (int i = threadIdx.x; i < n_partial; i += 32) s += partial[i];
@@ -700,255 +952,6 @@ __device__ __forceinline__ void ns_start(const void* __restrict__ g, int64_t row
     *reinterpret_cast<uint4*>(hi + row * ld + c) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
     *reinterpret_cast<uint4*>(lo + row * ld + c) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
   }
-}
-template <bool BF16>
-__global__ void __launch_bounds__(256)
-    k_ns_start(const void* __restrict__ g, int64_t rows, int64_t cols, int64_t ld, float eps,
-               const double* __restrict__ partial, int n_partial, __half* __restrict__ hi,
-               __half* __restrict__ lo) {
-  __shared__ float f[2];
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  ns_start<BF16>(g, rows, cols, ld, eps, partial, n_partial, hi, lo, f);
-}
-
-// ---------------------------------------------------------------------------
-// All steps in one cooperative launch, for matrices whose products are too
-// short for a launch each: the same roles and tiles as k_ns_gemm, but the
-// pipeline runs on from product to product, with a barrier over the grid
-// between them (a counter in the workspace, zeroed by k_ns_norm) in place of
-// the end of one launch and the start of the next. The warps that load and
-// the epilogue warps wait at it; the loads read what other CTAs stored through
-// the asynchronous proxy, hence their proxy fence behind the acquire.
-// ---------------------------------------------------------------------------
-
-// Tensor maps with boxes of 64 columns x 64 rows, kSM rows (K-major A) and BN
-// rows (K-major B).
-struct NsMaps {
-  CUtensorMap x_mn[2], x_a[2], ga_a, ga_b, gb_a, gb_b, x_b[2];
-};
-struct NsRun {
-  const void* g;
-  int64_t rows, cols, ldx, lds;
-  int steps, n_partial, sym;  // sym: half of the symmetric products' tiles
-  float a, b, c, eps;
-  const double* partial;
-  unsigned* counter;
-  __half *x[2], *xl, *ga, *gb;
-  void* out;
-  int out_bf16, out_vec;
-  float out_scale;
-  int* status;
-};
-
-// Product `i` of step i / 3: its shape, epilogue arguments and operands.
-struct NsPhase {
-  NsArgs p;
-  const CUtensorMap *ta, *tb;
-  bool a_mn, b_mn, sym;
-  int mode;
-};
-__device__ __forceinline__ NsPhase ns_phase(const NsRun& r, const NsMaps& maps, int i) {
-  const bool tall = r.rows > r.cols;
-  const int64_t s = tall ? r.cols : r.rows;
-  const int step = i / 3, cur = step & 1;
-  NsPhase f = {};
-  f.p.status = r.status;
-  f.mode = i % 3;
-  f.sym = f.mode != 2 && r.sym;
-  if (f.mode == 0) {
-    f.p.m = f.p.n = s, f.p.k = tall ? r.rows : r.cols, f.p.ldd = r.lds;
-    f.p.alpha = kNsInv, f.p.d_hi = r.ga;
-    f.ta = tall ? &maps.x_mn[cur] : &maps.x_a[cur];
-    f.tb = tall ? &maps.x_mn[cur] : &maps.x_b[cur];
-    f.a_mn = f.b_mn = tall;
-  } else if (f.mode == 1) {
-    f.p.m = f.p.n = f.p.k = s, f.p.ldd = r.lds;
-    f.p.alpha = __fmul_rn(r.c, kNsInv), f.p.beta = r.b, f.p.c_hi = r.ga, f.p.d_hi = r.gb;
-    f.ta = &maps.ga_a, f.tb = &maps.ga_b;
-  } else {
-    f.p.m = r.rows, f.p.n = r.cols, f.p.k = s, f.p.ldd = r.ldx;
-    f.p.alpha = kNsInv, f.p.beta = r.a, f.p.c_hi = r.x[cur], f.p.c_lo = r.xl;
-    f.p.d_hi = r.x[cur ^ 1], f.p.d_lo = r.xl;
-    f.p.out = r.out, f.p.out_bf16 = r.out_bf16, f.p.out_vec = r.out_vec;
-    f.p.out_scale = r.out_scale;
-    f.ta = tall ? &maps.x_a[cur] : &maps.gb_a;
-    f.tb = tall ? &maps.gb_b : &maps.x_mn[cur];
-    f.b_mn = !tall;
-    if (step + 1 == r.steps) f.mode = 3;
-  }
-  return f;
-}
-
-// Waits until `target` CTA arrivals are counted (bounded). A CTA that gave up
-// sets the counter's bit 30: every later wait of every CTA then fails too, so
-// nothing is computed from what that CTA did not finish.
-constexpr unsigned kNsGaveUp = 1u << 30;
-__device__ __forceinline__ bool ns_grid_wait(const unsigned* counter, unsigned target,
-                                             const int* failed) {
-  for (int i = 0; i < (1 << 21); ++i) {
-    unsigned v;
-    asm volatile("ld.acquire.gpu.global.u32 %0, [%1];" : "=r"(v) : "l"(counter) : "memory");
-    if (v >= target) return (v & kNsGaveUp) == 0;
-    if ((i & 255) == 255) {
-      if (failed_flag(failed)) return false;
-      __nanosleep(64);
-    }
-  }
-  return false;
-}
-__device__ __forceinline__ void ns_grid_arrive(unsigned* counter) {
-  asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(counter) : "memory");
-}
-
-template <int BN, bool BF16>
-__global__ void __launch_bounds__(kSThreads, 1)
-    k_ns_fused(const __grid_constant__ NsMaps maps, const __grid_constant__ NsRun r) {
-  using L = NsLayout<BN>;
-  extern __shared__ __align__(1024) uint8_t smem_raw[];
-  uint8_t* sm = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  unsigned long long* full = reinterpret_cast<unsigned long long*>(sm + L::kBarOff);
-  unsigned long long* empty = full + L::kStages;
-  unsigned long long* acc_full = empty + L::kStages;  // two accumulators
-  unsigned long long* acc_empty = acc_full + 2;
-  unsigned long long* drain = acc_empty + 2;
-  uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drain + 1);
-  int* failed = reinterpret_cast<int*>(tmem_base + 1);
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
-  const int phases = 3 * r.steps;
-  auto tiles_of = [&](const NsPhase& f, int64_t& mt, int64_t& nt) {
-    mt = (f.p.m + kSM - 1) / kSM, nt = (f.p.n + BN - 1) / BN;
-    return ns_tiles<BN>(f.sym, mt, nt);
-  };
-  auto tile_of = [&](const NsPhase& f, int64_t t, int64_t mt, int64_t nt, int64_t& m0,
-                     int64_t& n0) {
-    if (f.sym)
-      ns_tile<BN, true>(t, mt, nt, m0, n0);
-    else
-      ns_tile<BN, false>(t, mt, nt, m0, n0);
-  };
-
-  if (tid == 0) {
-    for (int s = 0; s < L::kStages; ++s) {
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 2;" ::"r"(smem_u32(&full[s])));
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&empty[s])));
-    }
-    for (int s = 0; s < 2; ++s) {
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(&acc_full[s])));
-      asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(&acc_empty[s])),
-                   "r"(kSEpiWarps));
-    }
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(smem_u32(drain)));
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    *failed = 0;
-  }
-  if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(tmem_base)),
-                 "r"(L::kTmemCols));
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-  }
-  ns_start<BF16>(r.g, r.rows, r.cols, r.ldx, r.eps, r.partial, r.n_partial, r.x[0], r.xl,
-                 reinterpret_cast<float*>(sm));
-  asm volatile("tcgen05.fence::before_thread_sync;");
-  __syncthreads();
-  asm volatile("tcgen05.fence::after_thread_sync;");
-  const uint32_t tmem = *tmem_base;
-  if (tid == 0) ns_grid_arrive(r.counter);
-
-  auto load_all = [&](auto ld, bool is_a) {
-    bool ok = true;
-    for (int i = 0; i < phases && ok; ++i) {
-      const NsPhase f = ns_phase(r, maps, i);
-      int64_t mt, nt;
-      const int64_t n_tiles = tiles_of(f, mt, nt);
-      const int n_kb = int((f.p.k + kSK - 1) / kSK);
-      if (!__all_sync(0xFFFFFFFFu,
-                      ns_grid_wait(r.counter, gridDim.x * unsigned(i + 1), failed))) {
-        atomicExch(failed, 1);
-        break;
-      }
-      asm volatile("fence.proxy.async;" ::: "memory");
-      for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x) {
-        int64_t m0, n0;
-        tile_of(f, t, mt, nt, m0, n0);
-        ok = ld.tile(is_a ? f.ta : f.tb, is_a ? f.a_mn : f.b_mn, int(is_a ? m0 : n0), n_kb);
-      }
-    }
-    ld.drain();
-  };
-  if (warp == 0) {
-    load_all(NsLoader<BN, true>(sm, full, empty, failed), true);
-  } else if (warp == kSLoadB) {
-    load_all(NsLoader<BN, false>(sm, full, empty, failed), false);
-  } else if (warp == 1) {
-    NsIssuer<BN> mma(sm, full, empty, tmem, failed);
-    bool ok = true;
-    for (int i = 0; i < phases && ok; ++i) {
-      const NsPhase f = ns_phase(r, maps, i);
-      int64_t mt, nt;
-      const int64_t n_tiles = tiles_of(f, mt, nt);
-      mma.operands(f.a_mn, f.b_mn);
-      for (int64_t t = blockIdx.x; t < n_tiles && ok; t += gridDim.x)
-        ok = mma.tile(int((f.p.k + kSK - 1) / kSK), acc_full, acc_empty);
-    }
-    mma.finish(ok, drain);
-  } else {
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    int64_t ti = 0;
-    for (int i = 0; i < phases; ++i) {
-      const NsPhase f = ns_phase(r, maps, i);
-      int64_t mt, nt;
-      const int64_t n_tiles = tiles_of(f, mt, nt);
-      // (after a failure nothing is waited for: NaN is stored and the others
-      // are not held up)
-      if (lane == 0 && !failed_flag(failed) &&
-          !ns_grid_wait(r.counter, gridDim.x * unsigned(i + 1), failed))
-        atomicExch(failed, 1);
-      __syncwarp();
-      for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x, ++ti) {
-        int64_t m0, n0;
-        tile_of(f, t, mt, nt, m0, n0);
-        const uint32_t buf = uint32_t(ti & 1), bph = uint32_t(ti >> 1) & 1u;
-        const int64_t row = m0 + 32 * q + lane, c0 = n0 + (BN / 2) * half;
-        const uint32_t tb =
-            tmem + buf * 256 + (uint32_t(32 * q) << 16) + uint32_t((BN / 2) * half);
-        unsigned long long* const done = &acc_full[buf];
-        uint8_t* const stage = sm + L::kEpiOff + (warp - 2) * (32 * 80);
-        bool ok;
-        if (f.mode == kGram)
-          ok = f.sym ? ns_epilogue<BN, kGram, true>(f.p, row, c0, tb, stage, done, bph, failed)
-                     : ns_epilogue<BN, kGram, false>(f.p, row, c0, tb, stage, done, bph, failed);
-        else if (f.mode == kSquare)
-          ok = f.sym ? ns_epilogue<BN, kSquare, true>(f.p, row, c0, tb, stage, done, bph, failed)
-                     : ns_epilogue<BN, kSquare, false>(f.p, row, c0, tb, stage, done, bph, failed);
-        else if (f.mode == kStep)
-          ok = ns_epilogue<BN, kStep, false>(f.p, row, c0, tb, stage, done, bph, failed);
-        else
-          ok = ns_epilogue<BN, kLast, false>(f.p, row, c0, tb, stage, done, bph, failed);
-        if (ok && lane == 0)
-          asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(
-                           smem_u32(&acc_empty[buf]))
-                       : "memory");
-      }
-      // this CTA's share is stored: one arrival for its 8 warps, whose release
-      // covers what the barrier ordered before it
-      asm volatile("bar.sync 1, %0;" ::"r"(32 * kSEpiWarps) : "memory");
-      if (warp == 2 && lane == 0) {
-        if (failed_flag(failed))
-          atomicOr(r.counter, kNsGaveUp);
-        else
-          ns_grid_arrive(r.counter);
-      }
-    }
-  }
-  asm volatile("tcgen05.fence::before_thread_sync;");
-  __syncthreads();
-  report_failure(r.status, failed);
-  if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                 "r"(L::kTmemCols));
 }
 
 // Tensor map over fp16 [rows][cols] with pitch ld: boxes of 64 columns (one
@@ -1017,57 +1020,53 @@ cudaError_t ns_gemm_bn(const NsOperand& a, const NsOperand& b, const NsArgs& arg
   return ns_launch(kern, int(tiles < sms ? tiles : sms), kSThreads, smem, s, ta, tb, args);
 }
 
-// Tile width: 256 columns reuse the most; narrower tiles where 256 would
-// leave SMs idle (fewer tiles than SMs).
+template <bool A_MN, bool B_MN, int MODE>
+cudaError_t ns_gemm_pair(const NsOperand& a, const NsOperand& b, const NsArgs& args,
+                         cudaStream_t s) {
+  using L = PairLayout;
+  CUtensorMap ta, tb;
+  if (!encode_half(&ta, a.p, a.rows, a.cols, a.ld, A_MN ? kSK : kSM) ||
+      !encode_half(&tb, b.p, b.rows, b.cols, b.ld, B_MN ? kSK : kSM))
+    return cudaErrorInvalidValue;
+  auto kern = k_ns_pair<A_MN, B_MN, MODE>;
+  constexpr size_t smem = L::kBytes + 1024;
+  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
+  if (e != cudaSuccess) return e;
+  const int64_t mt = (args.m + 255) / 256, nt = (args.n + 255) / 256;
+  const int64_t tiles = MODE == kGram || MODE == kSquare ? nt * (nt + 1) / 2 : mt * nt;
+  const int64_t pairs = ns_sms() / 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(2 * (tiles < pairs ? tiles : pairs)));
+  cfg.blockDim = dim3(kSThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = 2;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, ta, tb, args);
+}
+
+// Tiles: 256 x 256 by pairs where there are two rounds of them or nearly
+// (a round's epilogue then overlaps the next) and ragged edges leave little of
+// them idle; else 128 columns where those fill two thirds of the GPU, else 64.
 template <bool A_MN, bool B_MN, int MODE>
 cudaError_t ns_gemm(const NsOperand& a, const NsOperand& b, const NsArgs& args, cudaStream_t s) {
   constexpr bool sym = MODE == kGram || MODE == kSquare;
   const int64_t mt = (args.m + kSM - 1) / kSM;
-  if (ns_tiles<256>(sym, mt, (args.n + 255) / 256) >= 148)
-    return ns_gemm_bn<256, A_MN, B_MN, MODE>(a, b, args, s);
-  if (ns_tiles<128>(sym, mt, (args.n + 127) / 128) >= 148)
+  const int64_t m2 = (args.m + 255) / 256, n2 = (args.n + 255) / 256;
+  const int64_t pairs = 74, tiles = sym ? n2 * (n2 + 1) / 2 : m2 * n2;
+  const int64_t rounds = (tiles + pairs - 1) / pairs;
+  const double used = double(args.m) * double(args.n) / (sym ? 2 : 1);
+  if (tiles >= kNsPairTiles && used >= 0.7 * double(rounds * pairs) * 65536.0)
+    return ns_gemm_pair<A_MN, B_MN, MODE>(a, b, args, s);
+  if (ns_tiles<128>(sym, mt, (args.n + 127) / 128) >= 100)
     return ns_gemm_bn<128, A_MN, B_MN, MODE>(a, b, args, s);
   return ns_gemm_bn<64, A_MN, B_MN, MODE>(a, b, args, s);
-}
-
-// All steps in one launch. BN: 128 columns a tile where that fills the GPU.
-template <int BN, bool BF16>
-cudaError_t ns_fused(NsRun r, cudaStream_t s) {
-  using L = NsLayout<BN>;
-  NsMaps maps;
-  const int64_t side = r.rows < r.cols ? r.rows : r.cols;
-  const int sms = ns_sms();
-  // all tiles of A and B where the SMs can take them at once: no slower, and
-  // the mirrored stores fall away
-  r.sym = (side + kSM - 1) / kSM * ((side + BN - 1) / BN) > sms;
-  for (int i = 0; i < 2; ++i)
-    if (!encode_half(&maps.x_mn[i], r.x[i], r.rows, r.cols, r.ldx, kSK) ||
-        !encode_half(&maps.x_a[i], r.x[i], r.rows, r.cols, r.ldx, kSM) ||
-        !encode_half(&maps.x_b[i], r.x[i], r.rows, r.cols, r.ldx, BN))
-      return cudaErrorInvalidValue;
-  if (!encode_half(&maps.ga_a, r.ga, side, side, r.lds, kSM) ||
-      !encode_half(&maps.ga_b, r.ga, side, side, r.lds, BN) ||
-      !encode_half(&maps.gb_a, r.gb, side, side, r.lds, kSM) ||
-      !encode_half(&maps.gb_b, r.gb, side, side, r.lds, BN))
-    return cudaErrorInvalidValue;
-  auto kern = k_ns_fused<BN, BF16>;
-  constexpr size_t smem = L::kBytes + 1024;
-  const cudaError_t e = allow_smem(reinterpret_cast<const void*>(kern), smem);
-  if (e != cudaSuccess) return e;
-  const int64_t xt = (r.rows + kSM - 1) / kSM * ((r.cols + BN - 1) / BN);
-  const int64_t at = (side + kSM - 1) / kSM * ((side + BN - 1) / BN);
-  const int64_t tiles = xt > at ? xt : at;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(tiles < sms ? tiles : sms));
-  cfg.blockDim = dim3(kSThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeCooperative;
-  attr[0].val.cooperative = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, maps, r);
 }
 
 int64_t pad64(int64_t v) { return (v + 63) / 64 * 64; }
@@ -1077,7 +1076,7 @@ int64_t pad256(int64_t v) { return (v + 255) / 256 * 256; }
 
 int64_t newton_schulz_workspace(int64_t rows, int64_t cols) {
   const int64_t s = rows < cols ? rows : cols;
-  return 3 * pad256(rows * pad64(cols) * 2) + 2 * pad256(s * pad64(s) * 2) + kNsPartials * 8 + 256;
+  return 3 * pad256(rows * pad64(cols) * 2) + 2 * pad256(s * pad64(s) * 2) + kNsPartials * 8;
 }
 
 cudaError_t launch_newton_schulz(const void* g, bool bf16, int64_t rows, int64_t cols, int steps,
@@ -1096,28 +1095,12 @@ cudaError_t launch_newton_schulz(const void* g, bool bf16, int64_t rows, int64_t
   const int64_t n = rows * cols;
   const int64_t want = (n / 8 + 255) / 256;
   const int n_partial = int(want < 1 ? 1 : (want < kNsPartials ? want : kNsPartials));
-  unsigned* counter = reinterpret_cast<unsigned*>(partial + kNsPartials);
   if (bf16)
-    k_ns_norm<true><<<n_partial, 256, 0, st>>>(g, n, partial, counter);
+    k_ns_norm<true><<<n_partial, 256, 0, st>>>(g, n, partial);
   else
-    k_ns_norm<false><<<n_partial, 256, 0, st>>>(g, n, partial, counter);
+    k_ns_norm<false><<<n_partial, 256, 0, st>>>(g, n, partial);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  // One launch for all products where 256-column tiles would not fill the GPU
-  const int64_t mt = (rows + kSM - 1) / kSM;
-  if (mt * ((cols + 255) / 256) < 148) {
-    NsRun r = {};
-    r.g = g, r.rows = rows, r.cols = cols, r.ldx = ldx, r.lds = lds;
-    r.steps = steps, r.n_partial = n_partial;
-    r.a = a, r.b = b, r.c = c, r.eps = eps;
-    r.partial = partial, r.counter = counter;
-    r.x[0] = x[0], r.x[1] = x[1], r.xl = xl, r.ga = ga, r.gb = gb;
-    r.out = out, r.out_bf16 = out_bf16, r.out_vec = cols % 8 == 0;
-    r.out_scale = scale * kNsInv, r.status = status;
-    if (mt * ((cols + 127) / 128) >= 148)
-      return bf16 ? ns_fused<128, true>(r, st) : ns_fused<128, false>(r, st);
-    return bf16 ? ns_fused<64, true>(r, st) : ns_fused<64, false>(r, st);
-  }
   const int64_t chunk_blocks = (rows * ((cols + 7) / 8) + 255) / 256;
   const int start_grid = int(chunk_blocks < 148 * 8 ? chunk_blocks : 148 * 8);
   e = bf16 ? ns_launch(k_ns_start<true>, start_grid, 256, 0, st, g, rows, cols, ldx, eps,

@@ -50,9 +50,11 @@ def step64(x, c):
     return c[0] * x + (c[1] * p + c[2] * (p @ p)) @ x
 
 
-# tiles of 64, 128 and 256 columns, single and ragged tiles, wide and tall
+# tiles of 64 and 128 columns and of CTA pairs, single and ragged tiles, several
+# tiles a CTA, wide and tall
 SHAPES = [(1, 1), (1, 7), (9, 1), (64, 64), (128, 256), (130, 70), (33, 1000), (1000, 33),
-          (257, 259), (300, 2049), (2050, 300), (512, 512), (1537, 1001), (1001, 1537)]
+          (257, 259), (300, 2049), (2050, 300), (512, 512), (1537, 1001), (1001, 1537),
+          (1900, 4099), (4099, 1900), (2944, 2944), (520, 9000), (2304, 13000)]
 
 
 @pytest.mark.parametrize("coeffs", [(0.0, 1.0, 0.0), (1.0, 0.0, 1.0), MUON])
