@@ -118,6 +118,16 @@ __device__ __forceinline__ float part_sum(float v, int P) {
   return v;
 }
 
+// Sums of two values over a warp with one shuffle more than for one: lane 0
+// gets a's (and every lane of the lower half), lane 16 b's.
+__device__ __forceinline__ float warp_sum2(float a, float b, int lane) {
+  const bool up = (lane & 16) != 0;
+  float v = __fadd_rn(up ? b : a, __shfl_xor_sync(0xFFFFFFFFu, up ? a : b, 16));
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(0xFFFFFFFFu, v, o));
+  return v;
+}
+
 // v^-1/2 to an ulp: the approximation and one Newton step.
 __device__ __forceinline__ float rsqrt_exact(float v) {
   const float r = rsqrtf(v);
@@ -376,6 +386,9 @@ __global__ void __launch_bounds__(512)
   const float my_inv = my_n > 0.0f ? __fdiv_rn(1.0f, my_n) : 0.0f;
   const float l_n = MULTI && l < parts ? part_count<VEC, NV>(p, l) : 0.0f;
   const float l_inv = l_n > 0.0f ? __fdiv_rn(1.0f, l_n) : 0.0f;
+  const float n0 = __shfl_sync(0xFFFFFFFFu, l_n, 0), n1 = __shfl_sync(0xFFFFFFFFu, l_n, 1);
+  const float inv0 = __shfl_sync(0xFFFFFFFFu, l_inv, 0);
+  const float inv1 = __shfl_sync(0xFFFFFFFFu, l_inv, 1);
 
   // the cluster's CTAs walk the same rows; so do the warps of a group
   int d = 0, par = 0;
@@ -428,10 +441,20 @@ __global__ void __launch_bounds__(512)
         if (p.lane == 0) rd[p.warp] = make_float2(s, m2);
         group_sync<kLnFwdWarps / 2>(p.g, p.W);
       }
-      const float2 o = l < parts ? rd[p.g * p.W + l] : make_float2(0.0f, 0.0f);
-      mean = __fmul_rn(part_sum(o.x, p.P), inv_n);
-      const float dm = __fsub_rn(__fmul_rn(o.x, l_inv), mean);
-      m2 = part_sum(l < parts ? __fmaf_rn(__fmul_rn(l_n, dm), dm, o.y) : 0.0f, p.P);
+      if (parts == 2) {
+        // (every lane the same reads: shorter than shuffles)
+        const float2 o0 = rd[p.g * 2], o1 = rd[p.g * 2 + 1];
+        mean = __fmul_rn(__fadd_rn(o0.x, o1.x), inv_n);
+        const float d0 = __fsub_rn(__fmul_rn(o0.x, inv0), mean);
+        const float d1 = __fsub_rn(__fmul_rn(o1.x, inv1), mean);
+        m2 = __fadd_rn(__fmaf_rn(__fmul_rn(n0, d0), d0, o0.y),
+                       __fmaf_rn(__fmul_rn(n1, d1), d1, o1.y));
+      } else {
+        const float2 o = l < parts ? rd[p.g * p.W + l] : make_float2(0.0f, 0.0f);
+        mean = __fmul_rn(part_sum(o.x, p.P), inv_n);
+        const float dm = __fsub_rn(__fmul_rn(o.x, l_inv), mean);
+        m2 = part_sum(l < parts ? __fmaf_rn(__fmul_rn(l_n, dm), dm, o.y) : 0.0f, p.P);
+      }
     }
     const float rstd = rsqrt_exact(__fmaf_rn(m2, inv_n, eps));
     if (p.v0 == 0) {
@@ -704,20 +727,36 @@ __global__ void __launch_bounds__(512)
         c2 = fma2(g[k], h[k], c2);
       }
     }
-    float s1 = warp_sum(__fadd_rn(f2_lo(c1), f2_hi(c1)));
-    float s2 = warp_sum(__fadd_rn(f2_lo(c2), f2_hi(c2)));
+    const float half_sum = warp_sum2(__fadd_rn(f2_lo(c1), f2_hi(c1)),
+                                     __fadd_rn(f2_lo(c2), f2_hi(c2)), p.lane);
+    float s1, s2;
     if constexpr (MULTI) {
       float2* rd = red[par];
       if (p.CS > 1) {
-        if (p.lane < 2) store_pair(&rd[p.rank * p.W + p.w], make_float2(s1, s2), p.lane);
+        const float other = __shfl_sync(0xFFFFFFFFu, half_sum, 16);
+        const float mine_ = __shfl_sync(0xFFFFFFFFu, half_sum, 0);
+        if (p.lane < 2) store_pair(&rd[p.rank * p.W + p.w], make_float2(mine_, other), p.lane);
         pair_sync();
       } else {
-        if (p.lane == 0) rd[p.warp] = make_float2(s1, s2);
+        if ((p.lane & 15) == 0)
+          reinterpret_cast<float*>(&rd[p.warp])[p.lane >> 4] = half_sum;
         group_sync<kLnBwdWarps / 2>(p.g, p.W);
       }
-      const float2 o = l < parts ? rd[p.g * p.W + l] : make_float2(0.0f, 0.0f);
-      s1 = part_sum(o.x, p.P);
-      s2 = part_sum(o.y, p.P);
+      if (parts <= 4) {
+        // (every lane the same reads: shorter than shuffles)
+        s1 = s2 = 0.0f;
+        for (int k = 0; k < parts; ++k) {
+          const float2 o = rd[p.g * p.W + k];
+          s1 = __fadd_rn(s1, o.x), s2 = __fadd_rn(s2, o.y);
+        }
+      } else {
+        const float2 o = l < parts ? rd[p.g * p.W + l] : make_float2(0.0f, 0.0f);
+        s1 = part_sum(o.x, p.P);
+        s2 = part_sum(o.y, p.P);
+      }
+    } else {
+      s1 = __shfl_sync(0xFFFFFFFFu, half_sum, 0);
+      s2 = __shfl_sync(0xFFFFFFFFu, half_sum, 16);
     }
     // dx = g rstd - (c1 + h c2) rstd / n
     const float ri = -__fmul_rn(rstd, inv_n), m1 = __fmul_rn(s1, ri), m2 = __fmul_rn(s2, ri);
