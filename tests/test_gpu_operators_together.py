@@ -1,0 +1,113 @@
+"""The norm, the products, the update and the answer of a quantized linear
+layer, one after the other as a training step and a decoding step use them."""
+import pytest
+import torch
+
+import mxfp4_block_quantization_quantizer_b200 as m
+
+pytestmark = pytest.mark.gpu
+
+
+def randn(*shape, seed):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randn(shape, generator=g, device="cuda")
+
+
+def test_training_step_then_an_answer():
+    rows, k, n = 256, 512, 384
+    x = randn(rows, k, seed=1).to(torch.bfloat16)
+    gain, off = 1 + 0.1 * randn(k, seed=2), 0.1 * randn(k, seed=3)
+    w = 0.02 * randn(n, k, seed=4)                   # fp32 master weight
+
+    # forward: norm and Q_D in one pass, the product of 4-bit operands
+    xc, xs, y, mean, rstd = m.layernorm_quantize(x, gain, off, want_y=True, want_stats=True)
+    wc, ws = m.quantize(w)
+    wb = m.scales_to_blocked(ws)
+    out = m.gemm(xc, m.scales_to_blocked(xs), wc, wb, k)
+    qy = m.dequantize(xc, xs, rows, k, out_dtype=torch.float32).double()
+    qw = m.dequantize(wc, ws, n, k, out_dtype=torch.float32).double()
+    bound = (k - 1) * 2.0 ** -24 * (qy.abs() @ qw.abs().T)
+    assert ((out.double() - qy @ qw.T).abs() <= bound).all()
+    # the same product with y left in bf16
+    fine = m.gemv(y, wc, wb, out_dtype=torch.float32)
+    bound = (k + 64) * 2.0 ** -24 * 1.25 * (y.double().abs() @ qw.abs().T) + 1e-6
+    assert ((fine.double() - y.double() @ qw.T).abs() <= bound).all()
+
+    # backward through the norm, for a gradient that comes from the product
+    dout = randn(rows, n, seed=5)
+    dy = (dout.double() @ qw).to(torch.bfloat16)
+    dx, dgain, doff = m.layernorm_backward(dy, x, mean, rstd, gain)
+    xd = x.double().requires_grad_()
+    gd, od = gain.double().requires_grad_(), off.double().requires_grad_()
+    torch.nn.functional.layer_norm(xd, (k,), gd, od, 1e-5).backward(dy.double())
+    for got, want, eps in ((dx, xd.grad, 2.0 ** -8), (dgain, gd.grad, 2.0 ** -18),
+                           (doff, od.grad, 2.0 ** -18)):
+        assert (got.double() - want).norm() <= eps * want.norm()
+
+    # update: the weight's gradient made orthogonal, Q-Ramping, Q-EMA
+    grad = (dout.double().T @ y.double()).float()
+    delta = m.newton_schulz(grad, scale=-0.01)
+    sv = torch.linalg.svdvals(delta.double()) / 0.01
+    # (256 rows: a gradient of rank 256, whose values five steps bring near 1)
+    assert sv.max() < 1.3 and sv[:192].min() > 0.6 and sv[256:].max() < 0.05
+    w0, zeros = w.clone(), [torch.zeros_like(w) for _ in range(4)]
+    m.qramp_step(w, delta, *zeros, torch.zeros(w.shape, dtype=torch.uint8, device="cuda"), 0)
+    assert torch.equal(w, w0 + delta)
+    ema = w0.clone()
+    ec, es = m.qema_quantize(w, ema, 0.998)
+
+    # answer: one token, a batch of tokens and a graph of both, on the averaged weight
+    eb = m.scales_to_blocked(es)
+    ew = m.dequantize(ec, es, n, k, out_dtype=torch.float32).double()
+    tokens = randn(5, k, seed=6).to(torch.bfloat16)
+
+    def answer():
+        h = m.layernorm(tokens, gain, off)
+        return m.gemv(h, ec, eb), m.gemv(h[:1], ec, eb)
+    batch, one = answer()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gb, go = answer()
+    for seed in (7, 8):
+        tokens.copy_(randn(5, k, seed=seed))
+        graph.replay()
+        batch, one = answer()
+        assert torch.equal(gb, batch) and torch.equal(go, one)
+        want = m.layernorm(tokens, gain, off).double() @ ew.T
+        assert (batch.double() - want).norm() <= 2.0 ** -8 * want.norm()
+        assert (one.double() - want[:1]).norm() <= 2.0 ** -8 * want[:1].norm()
+
+
+def test_two_graphs_and_eager_calls_share_nothing():
+    """Two captured graphs of the operators with workspaces, replayed one over
+    the other on two streams while eager calls run on a third."""
+    codes, scales = m.quantize(0.02 * randn(1024, 1024, seed=10))
+    blocked = m.scales_to_blocked(scales)
+    gain = 1 + 0.1 * randn(1024, seed=11)
+    xs = [randn(40, 1024, seed=s).to(torch.bfloat16) for s in (12, 13, 14)]
+
+    def work(x):
+        y, mean, rstd = m.layernorm(x, gain, want_stats=True)
+        z = m.gemv(y, codes, blocked)
+        return (z, *m.layernorm_backward(z, x, mean, rstd, gain), m.newton_schulz(z))
+    want = [[t.clone() for t in work(x)] for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    graphs, outs = [], []
+    for x, s in zip(xs[:2], streams):
+        g = torch.cuda.CUDAGraph()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.graph(g, stream=s):
+            outs.append(work(x))
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        with torch.cuda.stream(streams[2]):
+            eager = work(xs[2])
+    torch.cuda.synchronize()
+    for got, ref in zip(outs + [eager], want):
+        for a, b in zip(got, ref):
+            assert torch.equal(a, b)
