@@ -44,6 +44,9 @@ constexpr int kLnMaxParts = 32;      // ... and of a cluster
 __host__ __device__ constexpr int ln_depth(int nv) { return nv == 1 ? 4 : 2; }
 // Warps of a CTA that narrow rows share (backward: few partial sums).
 constexpr int kLnFwdWarps = 4, kLnBwdWarps = 16;
+// The backward kernel that takes several rows at a time: most warps of a row,
+// and warps and row groups of a CTA that narrow rows share.
+constexpr int kLnRowWarps = 16, kLnRowShare = 12, kLnRowGroups = 6;
 constexpr int64_t kLnMaxCols = 1 << 16;  // far above what a cluster holds
 constexpr int kLnGenThreads = 512;   // the kernels for wider rows
 constexpr int kLnRedThreads = 1024;
@@ -311,6 +314,8 @@ __device__ __forceinline__ void mask_vec(F2* a, int e, int cols) {
     a[j] = f2(l ? f2_lo(a[j]) : 0.0f, h ? f2_hi(a[j]) : 0.0f);
   }
 }
+// Store a vector's elements that belong to the row, one by one (pieces of 8, 4
+// and 2 bytes took longer: more branches).
 template <bool BF16, int VEC>
 __device__ __forceinline__ void store_part(void* to, int e, int cols, uint4 r) {
   const uint32_t w[4] = {r.x, r.y, r.z, r.w};
@@ -814,6 +819,194 @@ __global__ void __launch_bounds__(512)
   if (p.CS > 1) pair_sync();
 }
 
+// Backward, aligned rows of at most kLnRowWarps warps with one vector a thread:
+// R rows of the group at a time. The sums of R rows are reduced together (2 R values
+// over 32 lanes by exchanging halves: R = 4 takes 9 shuffles and one barrier
+// instead of 40 and 4), and x and dy are read from shared memory a second time
+// for dx and the column sums, so that a thread holds little: more warps run,
+// and the R rows are independent work. 12608 x 1536 bf16: 27.6 us, a row at a
+// time (k_ln_bwd) 31.5 us; 12608 x 384: 13.5 and 19.1 us.
+template <int N>
+__device__ __forceinline__ float exchange_sum(float (&v)[N], int lane, int mask) {
+  if constexpr (N == 1) {
+    float t = v[0];
+    for (int o = mask; o > 0; o >>= 1) t = __fadd_rn(t, __shfl_xor_sync(0xFFFFFFFFu, t, o));
+    return t;
+  } else {
+    const bool up = (lane & mask) != 0;
+    float h[N / 2];
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i) {
+      const float give = up ? v[i] : v[i + N / 2], keep = up ? v[i + N / 2] : v[i];
+      h[i] = __fadd_rn(keep, __shfl_xor_sync(0xFFFFFFFFu, give, mask));
+    }
+    return exchange_sum<N / 2>(h, lane, mask / 2);
+  }
+}
+
+template <bool BF16, bool MULTI, bool PARAMS>
+__global__ void __launch_bounds__(kLnRowWarps * 32)
+    k_ln_bwd_rows(const void* __restrict__ dy, const void* __restrict__ x, int64_t rows, int cols,
+                  int64_t lddy, int64_t ldx, const float* __restrict__ weight,
+                  const float* __restrict__ mean_in, const float* __restrict__ rstd_in,
+                  void* __restrict__ dx, float* __restrict__ partial, LnSplit split) {
+  constexpr int VEC = BF16 ? 8 : 4, NP = VEC / 2, R = 4, NV = 2 * R;  // NV sums
+  constexpr int kPer = 32 / NV;  // lanes that hold the same sum
+  using V = Vec<BF16, VEC>;
+  extern __shared__ __align__(16) uint4 ring[];  // [warps][2][R][2][32]
+  __shared__ float red[2][kLnRowWarps][NV];
+  const Place p = place<VEC, 1, false>(split, rows, cols, ldx, 0);
+  uint4* const mine = ring + p.warp * (2 * R * 64) + p.lane;
+  const bool live = p.v0 < p.nvec;
+  const int e = p.v0 * VEC;
+
+  Walk wx = walk<BF16>(x, rows, ldx, p), wg = walk<BF16>(dy, rows, lddy, p);
+  int to_fetch = p.n;
+  const float *mp = mean_in + p.row0, *rp = rstd_in + p.row0;
+  float nmean[R], nrstd[R];
+  auto fetch = [&](int b) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      if (to_fetch > 0) {
+        uint4* const to = mine + (b * R + r) * 64;
+        if (live) {
+          fetch_vec<BF16, false>(to, wx.at, wx.first, wx.end);
+          fetch_vec<BF16, false>(to + 32, wg.at, wg.first, wg.end);
+        }
+      }
+      wx.at += wx.step, wg.at += wg.step;
+      --to_fetch;
+    }
+    cp_async_commit();
+  };
+  auto fetch_stats = [&](int left) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      nmean[r] = r < left ? __ldg(mp) : 0.0f;
+      nrstd[r] = r < left ? __ldg(rp) : 0.0f;
+      mp += p.stride, rp += p.stride;
+    }
+  };
+  if (!live) {
+#pragma unroll
+    for (int i = 0; i < 2 * R * 2; ++i) mine[i * 32] = make_uint4(0, 0, 0, 0);
+  }
+  fetch(0);
+  fetch(1);
+  fetch_stats(p.n);
+  F2 wk[NP];
+  load_param<VEC, false>(weight, 1.0f, p, p.v0, wk);
+  uint8_t* to = static_cast<uint8_t*>(dx) + (p.row0 * cols + e) * (BF16 ? 2 : 4);
+  const int64_t to_step = p.stride * cols * (BF16 ? 2 : 4);
+  const float inv_n = __fdiv_rn(1.0f, float(cols));
+  const F2 zero = f2(0.0f, 0.0f);
+  F2 aw[PARAMS ? NP : 1], ab[PARAMS ? NP : 1];
+  if constexpr (PARAMS) {
+#pragma unroll
+    for (int k = 0; k < NP; ++k) aw[k] = ab[k] = zero;
+  }
+
+  // h = (x - mean) rstd and dy of row r of buffer b
+  auto read = [&](int b, int r, float mean, float rstd, F2* h, F2* g) {
+    V in;
+    in.r = mine[(b * R + r) * 64];
+    in.unpack(h);
+    in.r = mine[(b * R + r) * 64 + 32];
+    in.unpack(g);
+    const F2 nm = f2(-mean, -mean), rs = f2(rstd, rstd);
+#pragma unroll
+    for (int k = 0; k < NP; ++k) h[k] = mul2(add2(h[k], nm), rs);
+  };
+
+  int b = 0;
+  for (int left = p.n; left > 0; left -= R, b ^= 1) {
+    float mean[R], rstd[R], s[NV];
+#pragma unroll
+    for (int r = 0; r < R; ++r) mean[r] = nmean[r], rstd[r] = nrstd[r];
+    fetch_stats(left - R);
+    cp_async_wait<1>();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      F2 h[NP], g[NP], c1 = zero, c2 = zero;
+      if (r < left) {
+        read(b, r, mean[r], rstd[r], h, g);
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          const F2 gw = mul2(g[k], wk[k]);
+          c1 = add2(c1, gw);
+          c2 = fma2(gw, h[k], c2);
+        }
+      }
+      s[2 * r] = __fadd_rn(f2_lo(c1), f2_hi(c1));
+      s[2 * r + 1] = __fadd_rn(f2_lo(c2), f2_hi(c2));
+    }
+    // lane l then holds the warp's sum l / kPer
+    float sum = exchange_sum<NV>(s, p.lane, 16);
+    if constexpr (MULTI) {
+      // one barrier for R rows: the buffer of this parity is written again two
+      // rounds on, past the next round's barrier
+      if (p.lane % kPer == 0) red[b][p.warp][p.lane / kPer] = sum;
+      group_sync<kLnRowGroups>(p.g, p.W);
+      sum = 0.0f;
+      for (int k = 0; k < p.W; ++k)
+        sum = __fadd_rn(sum, red[b][p.g * p.W + k][p.lane / kPer]);
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const float s1 = __shfl_sync(0xFFFFFFFFu, sum, 2 * r * kPer);
+      const float s2 = __shfl_sync(0xFFFFFFFFu, sum, (2 * r + 1) * kPer);
+      if (r < left) {
+        F2 h[NP], g[NP], o[NP];
+        read(b, r, mean[r], rstd[r], h, g);
+        // dx = g rstd - (c1 + h c2) rstd / n
+        const float ri = -__fmul_rn(rstd[r], inv_n);
+        const float m1 = __fmul_rn(s1, ri), m2 = __fmul_rn(s2, ri);
+        const F2 k1 = f2(m1, m1), k2 = f2(m2, m2), rs = f2(rstd[r], rstd[r]);
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+          if constexpr (PARAMS) {
+            aw[k] = fma2(g[k], h[k], aw[k]);
+            ab[k] = add2(ab[k], g[k]);
+          }
+          o[k] = fma2(h[k], k2, fma2(mul2(g[k], wk[k]), rs, k1));
+        }
+        V out;
+        out.pack(o);
+        if (live) __stcs(reinterpret_cast<uint4*>(to), out.r);
+      }
+      to += to_step;
+    }
+    fetch(b);
+  }
+  cp_async_wait<0>();
+
+  if constexpr (PARAMS) {
+    // the groups of a CTA (same columns) add into shared memory
+    // one after the other; the last one writes the partial row
+    float* pw = partial + int64_t(blockIdx.x) * 2 * cols;
+    float* sacc = reinterpret_cast<float*>(ring);  // [2][VEC][slots]
+    const int G = (blockDim.x >> 5) / p.W, slots = p.W * 32;
+    if (G > 1) __syncthreads();  // every group is done with the ring
+    for (int gi = 0; gi < G; ++gi) {
+      if (p.g == gi) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          const int at = j * slots + p.v0;
+          float a = (j & 1) ? f2_hi(aw[j / 2]) : f2_lo(aw[j / 2]);
+          float bb = (j & 1) ? f2_hi(ab[j / 2]) : f2_lo(ab[j / 2]);
+          if (gi > 0) a = __fadd_rn(a, sacc[at]), bb = __fadd_rn(bb, sacc[slots * VEC + at]);
+          if (gi + 1 < G) {
+            sacc[at] = a, sacc[slots * VEC + at] = bb;
+          } else if (e + j < cols) {
+            pw[e + j] = a, pw[cols + e + j] = bb;
+          }
+        }
+      }
+      if (G > 1) __syncthreads();
+    }
+  }
+}
+
 // Rows wider than the registers of 16 warps: dx with one CTA a row, and the
 // column sums by a kernel of their own that reads x and dy again.
 template <bool BF16>
@@ -1087,6 +1280,37 @@ cudaError_t bwd_launch(const BwdArgs& a, const LnShape& sh, int misaligned) {
   return params_launch(a, grid / sh.split.CS);
 }
 
+template <bool BF16, bool MULTI, bool PARAMS>
+cudaError_t bwd_rows(const BwdArgs& a, const LnShape& sh) {
+  constexpr int VEC = BF16 ? 8 : 4;
+  auto kern = k_ln_bwd_rows<BF16, MULTI, PARAMS>;
+  const void* k = reinterpret_cast<const void*>(kern);
+  const size_t smem = size_t(sh.threads) * 2 * 4 * 2 * 16;
+  cudaError_t e = allow_smem(k, smem);
+  if (e != cudaSuccess) return e;
+  const int grid = ln_grid(k, sh, smem, a.rows, false, VEC, kLnMaxPartials);
+  e = ln_launch(kern, grid, sh, smem, a.s, a.dy, a.x, a.rows, int(a.cols), a.lddy, a.ldx,
+                a.weight, a.mean, a.rstd, a.dx, a.partial, sh.split);
+  if (e != cudaSuccess || !PARAMS) return e;
+  return params_launch(a, grid);
+}
+template <bool BF16>
+cudaError_t bwd_rows_any(const BwdArgs& a, int64_t nvec) {
+  LnShape sh;
+  const int W = int((nvec + 31) / 32);
+  sh.nv = 1;
+  sh.split.W = W, sh.split.CS = 1, sh.split.P = 1;
+  // groups share a CTA (at most kLnRowGroups, whose barriers are numbered)
+  const int G = W >= kLnRowShare ? 1 : kLnRowShare / W;
+  sh.split.G = W > 1 && G > kLnRowGroups ? kLnRowGroups : G;
+  sh.threads = 32 * W * sh.split.G;
+  if (W > 1)
+    return a.dw != nullptr ? bwd_rows<BF16, true, true>(a, sh)
+                           : bwd_rows<BF16, true, false>(a, sh);
+  return a.dw != nullptr ? bwd_rows<BF16, false, true>(a, sh)
+                         : bwd_rows<BF16, false, false>(a, sh);
+}
+
 template <bool BF16, int NV, bool MULTI>
 cudaError_t bwd_nv(const BwdArgs& a, const LnShape& sh, bool edge, int misaligned) {
   if (a.dw != nullptr)
@@ -1102,12 +1326,18 @@ cudaError_t bwd_any(const BwdArgs& a) {
   // at most 16 elements a thread: two sums for each stay in registers
   constexpr int kBig = BF16 ? 2 : 4;
   LnShape sh;
-  bool edge;
-  int mis;
+  bool edge = false;
+  int mis = 0;
   const void* const ptrs[] = {a.x, a.dy, a.dx};
   const int64_t lds[] = {a.ldx, a.lddy, a.cols};
-  if (a.cols <= kLnMaxCols && vector_rows(ptrs, lds, 3, a.cols, kSize, &edge, &mis) &&
-      ln_shape((a.cols + VEC - 1) / VEC + (edge ? 1 : 0), kBig, a.rows, kLnBwdWarps, &sh)) {
+  const bool vec = a.cols <= kLnMaxCols &&
+                   vector_rows(ptrs, lds, 3, a.cols, kSize, &edge, &mis);
+  const int64_t nvec = (a.cols + VEC - 1) / VEC + (edge ? 1 : 0);
+  // several rows at a time where a row fits and there are rows for every SM
+  // (rows off the boundary: a row at a time, 32 against 36 us at 5000 x 2563)
+  if (vec && !edge && nvec <= 32 * kLnRowWarps && a.rows >= 4 * int64_t(sm_count()))
+    return bwd_rows_any<BF16>(a, nvec);
+  if (vec && ln_shape(nvec, kBig, a.rows, kLnBwdWarps, &sh)) {
     const bool multi = sh.split.W * sh.split.CS > 1;
     if (sh.nv == 1)
       return multi ? bwd_nv<BF16, 1, true>(a, sh, edge, mis)

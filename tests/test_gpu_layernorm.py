@@ -18,7 +18,8 @@ U = 2.0 ** -24
 BF, F = torch.bfloat16, torch.float32
 SHAPES = [(1, 1), (1, 4096), (3, 5), (7, 48), (9, 63), (64, 384), (197, 1536), (700, 256),
           (33, 1111), (620, 1111), (5, 16384), (3, 16392), (2, 20001), (2, 40000), (300, 8192),
-          (1300, 96), (1201, 2048), (310, 5000), (12, 9001)]
+          (1300, 96), (1201, 2048), (310, 5000), (12, 9001), (5003, 8), (2999, 640), (4001, 264),
+          (901, 4096), (595, 4104), (3333, 1000)]
 
 
 def depth(cols):
