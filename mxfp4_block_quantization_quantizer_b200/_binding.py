@@ -453,11 +453,23 @@ def _f32(t, name, n, device):
         _buffer(t, name, torch.float32, n, device)
 
 
-def _like(x):
+def _new(shape, dtype, device, stream):
+    """A new tensor for work on `stream` (None: the current one). From the
+    memory of that stream, where what used it before has ended in order, and
+    kept until the caller's current stream is done with it too."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _like(x, stream):
     """A new contiguous tensor of x's shape and type."""
-    if x.is_contiguous():
+    if stream is None and x.is_contiguous():
         return torch.empty_like(x)
-    return torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    return _new(x.shape, x.dtype, x.device, stream)
 
 
 def _rows2d(t, name):
@@ -509,13 +521,13 @@ def gemv(x, b_codes, b_blocked, out_dtype=torch.bfloat16, out=None, workspace=No
     _buffer(b_codes, "b_codes", torch.uint8, n * k // 2, d)
     _buffer(b_blocked, "b_blocked", torch.uint8, -(-n // 128) * 128 * (-(-k // 128) * 4), d)
     if out is None:
-        out = torch.empty((m, n), dtype=out_dtype, device=d)
+        out = _new((m, n), out_dtype, d, stream)
     else:
         _buffer(out, "out", out.dtype, m * n, d)
         _apart(out, "out", x)
     st = None if status is None else _addr(_buffer(status, "status", torch.int32, 1, d))
     need = _workspace_size("mxfp4_gemv_workspace", m, n, k)
-    workspace = _workspace(workspace, need, d) if need > 0 else None
+    workspace = _workspace(workspace, need, d, stream) if need > 0 else None
     _call("mxfp4_gemv", d, stream, x.data_ptr(), m, n, k, ldx, b_codes.data_ptr(),
           b_blocked.data_ptr(), out.data_ptr(), _dtype_code(out), _addr(workspace), max(need, 0),
           st)
@@ -541,10 +553,10 @@ def layernorm(x, weight=None, bias=None, eps=1e-5, want_stats=False, out=None, s
     d = x.device
     mean = rstd = None
     if out is None:
-        out = y = _like(x)
+        out = y = _like(x, stream)
         if want_stats:
-            mean = torch.empty(R, dtype=torch.float32, device=d)
-            rstd = torch.empty_like(mean)
+            mean = _new(R, torch.float32, d, stream)
+            rstd = _new(R, torch.float32, d, stream)
             out = (y, mean, rstd)
     else:
         y = out
@@ -568,12 +580,12 @@ def layernorm_quantize(x, weight=None, bias=None, eps=1e-5, want_y=False, want_s
     R, C = x.shape
     d = x.device
     if out is None:
-        out = (_empty_u8((R, C // 2), d), _empty_u8((R, C // 32), d))
+        out = (_new((R, C // 2), torch.uint8, d, stream),
+               _new((R, C // 32), torch.uint8, d, stream))
         if want_y:
-            out += (torch.empty((R, C), dtype=x.dtype, device=d),)
+            out += (_new((R, C), x.dtype, d, stream),)
         if want_stats:
-            out += (torch.empty(R, dtype=torch.float32, device=d),
-                    torch.empty(R, dtype=torch.float32, device=d))
+            out += (_new(R, torch.float32, d, stream), _new(R, torch.float32, d, stream))
     if len(out) != 2 + bool(want_y) + 2 * bool(want_stats):
         raise ValueError("out must hold codes, scales and what is wanted beside them")
     codes, scales = out[:2]
@@ -600,10 +612,10 @@ def _workspace_size(name, *shape):
     return getattr(lib(), name)(*shape)
 
 
-def _workspace(workspace, need, device):
+def _workspace(workspace, need, device, stream):
     """A caller's workspace (uint8, at least `need` bytes) or a new one."""
     if workspace is None:
-        return torch.empty(max(need, 16), dtype=torch.uint8, device=device)
+        return _new(max(need, 16), torch.uint8, device, stream)
     if not isinstance(workspace, torch.Tensor) or workspace.numel() < need:
         raise ValueError("workspace must be a uint8 tensor of at least %d bytes" % need)
     return _buffer(workspace, "workspace", torch.uint8, workspace.numel(), device)
@@ -626,11 +638,10 @@ def layernorm_backward(dy, x, mean, rstd, weight=None, want_params=True, out=Non
     _f32(rstd, "rstd", R, d)
     dw = db = None
     if out is None:
-        out = dx = _like(x)
+        out = dx = _like(x, stream)
         if want_params:
-            dw = (torch.empty(C, dtype=torch.float32, device=d) if weight is None
-                  else torch.empty_like(weight))
-            db = torch.empty_like(dw)
+            dw = _new(C, torch.float32, d, stream)
+            db = _new(C, torch.float32, d, stream)
             out = (dx, dw, db)
     else:
         dx = out
@@ -643,7 +654,7 @@ def layernorm_backward(dy, x, mean, rstd, weight=None, want_params=True, out=Non
     size = 0
     if want_params:
         workspace = _workspace(workspace, _workspace_size("mxfp4_layernorm_backward_workspace", R, C),
-                               d)
+                               d, stream)
         size = workspace.numel()
     else:
         workspace = None
@@ -665,14 +676,14 @@ def newton_schulz(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=
     R, C = g.shape
     d = g.device
     if out is None:
-        out = torch.empty((R, C), dtype=out_dtype or g.dtype, device=d)
+        out = _new((R, C), out_dtype or g.dtype, d, stream)
     else:
         _buffer(out, "out", out.dtype, R * C, d)
         if out.data_ptr() != g.data_ptr() or out.dtype != g.dtype:
             _apart(out, "out", g)
     odt = _dtype_code(out)
     need = _workspace_size("mxfp4_newton_schulz_workspace", R, C)
-    workspace = _workspace(workspace, need, d)
+    workspace = _workspace(workspace, need, d, stream)
     st = None if status is None else _addr(_buffer(status, "status", torch.int32, 1, d))
     a, b, c = coeffs
     _call("mxfp4_newton_schulz", d, stream, g.data_ptr(), dt, R, C, steps, a, b, c, eps, scale,

@@ -12,7 +12,7 @@
 // Bound by memory: forward reads x and writes y, backward reads x and dy and
 // writes dx, once each. W warps take whole rows (E = VEC NV elements a thread
 // in registers; rows too wide for one CTA are split over a cluster of two).
-// The loads of the next kLnDepth rows are in flight at any time as 16-byte
+// The loads of the next rows (ln_depth) are in flight at any time as 16-byte
 // asynchronous copies into shared memory: each thread copies what it will
 // read itself, so no barrier orders them, and no register holds them. Every
 // statistic is fp32: each warp takes its own mean first and sums squares
@@ -247,6 +247,11 @@ __device__ __forceinline__ Walk walk(const void* base, int64_t rows, int64_t ld,
   w.step = p.stride * ld * kSize;
   return w;
 }
+// Rows at either end of a tensor whose vectors may reach past it.
+template <int VEC>
+__device__ __forceinline__ int64_t end_rows(int64_t ld) {
+  return ld > VEC ? 1 : VEC / int(ld) + 1;
+}
 
 // A parameter (fp32 [cols], nullptr: `fill`) of this CTA's vectors in shared
 // memory: [VEC / 4][slots] float4, slot s = vector rank W NV 32 + s (so that
@@ -348,13 +353,14 @@ __global__ void __launch_bounds__(512)
 
   Walk wx = walk<BF16>(x, rows, ldx, p);
   int to_fetch = p.n;
-  int64_t f_row = p.row0;  // (a tensor's ends lie in its first and last row)
+  int64_t f_row = p.row0;
+  const int64_t ends = EDGE ? end_rows<VEC>(ldx) : 1;
   auto fetch = [&](int d) {
     if (to_fetch > 0) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (p.v0 + 32 * i < p.nvec) {
-          if (EDGE && (f_row == 0 || f_row == rows - 1))
+          if (EDGE && (f_row < ends || f_row >= rows - ends))
             fetch_vec<BF16, true>(mine + (d * NV + i) * 32, wx.at + 512 * i, wx.first, wx.end);
           else
             fetch_vec<BF16, false>(mine + (d * NV + i) * 32, wx.at + 512 * i, wx.first, wx.end);
@@ -629,14 +635,15 @@ __global__ void __launch_bounds__(512)
 
   Walk wx = walk<BF16>(x, rows, ldx, p), wg = walk<BF16>(dy, rows, lddy, p);
   int to_fetch = p.n;
-  int64_t f_row = p.row0;  // (a tensor's ends lie in its first and last row)
+  int64_t f_row = p.row0;
+  const int64_t ends = EDGE ? end_rows<VEC>(ldx < lddy ? ldx : lddy) : 1;
   auto fetch = [&](int d) {
     if (to_fetch > 0) {
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (p.v0 + 32 * i < p.nvec) {
           uint4* const to = mine + (d * NV + i) * 64;
-          if (EDGE && (f_row == 0 || f_row == rows - 1)) {
+          if (EDGE && (f_row < ends || f_row >= rows - ends)) {
             fetch_vec<BF16, true>(to, wx.at + 512 * i, wx.first, wx.end);
             fetch_vec<BF16, true>(to + 32, wg.at + 512 * i, wg.first, wg.end);
           } else {

@@ -111,3 +111,35 @@ def test_two_graphs_and_eager_calls_share_nothing():
     for got, ref in zip(outs + [eager], want):
         for a, b in zip(got, ref):
             assert torch.equal(a, b)
+
+
+def test_side_stream_owns_its_memory():
+    """Work queued on a side stream keeps its workspace and outputs while the
+    current stream goes on allocating and writing."""
+    codes, scales = m.quantize(0.02 * randn(1024, 1024, seed=20))
+    blocked = m.scales_to_blocked(scales)
+    gain = 1 + 0.1 * randn(1024, seed=21)
+    x = randn(40, 1024, seed=22).to(torch.bfloat16)
+    dy = randn(40, 1024, seed=23).to(torch.bfloat16)
+
+    def work(stream=None):
+        y, mean, rstd = m.layernorm(x, gain, want_stats=True, stream=stream)
+        q = m.layernorm_quantize(x, gain, stream=stream)
+        z = m.gemv(x, codes, blocked, stream=stream)
+        return (y, mean, rstd, *q, z,
+                *m.layernorm_backward(dy, x, mean, rstd, gain, stream=stream),
+                m.newton_schulz(x, stream=stream))
+    want = work()
+    side = torch.cuda.Stream()
+    sizes = [t.numel() * t.element_size() for t in want]
+    sizes += [1 << b for b in range(9, 22)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)     # the side stream starts late
+        got = work(side)
+        junk = [torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda") for n in sizes]
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        del got, junk
