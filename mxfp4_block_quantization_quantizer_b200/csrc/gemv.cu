@@ -61,9 +61,6 @@ struct VLayout {
   static constexpr int kRowBlocks = (kN + 127) / 128;      // scale tiles of B per 128 k
   static constexpr int kStages = T == 2 ? 5 : (T == 8 ? 4 : (T == 16 ? 3 : 4));
   static constexpr int kPerSm = T == 32 ? 1 : 2;           // CTAs an SM
-  // Consecutive MMAs on one accumulator wait for each other; with few columns
-  // that takes longer than the MMA, so a stage's four MMAs alternate.
-  static constexpr int kAcc = T == 2 ? 4 : (T == 8 ? 2 : 1);
   // bytes of a stage: codes, their scales, digits and their scales (the last
   // two as one block, the unit of the digit workspace)
   static constexpr uint32_t kA = kVM * 128, kSfa = 1024;
@@ -76,9 +73,9 @@ struct VLayout {
   static constexpr uint32_t kBytes = kBarOff + 256;
   static_assert(kPerSm * (kBytes + 2048) <= 227 * 1024, "CTAs an SM");
   static_assert(kX % 1024 == 0, "swizzle atoms");
-  // tensor memory: accumulators, then per stage the scales of A (8 columns)
+  // tensor memory: accumulator, then per stage the scales of A (8 columns)
   // and B (8 a row block), so that copying a stage's scales waits for no MMA
-  static constexpr uint32_t kSfCol = kAcc * kN;
+  static constexpr uint32_t kSfCol = kN;
   static constexpr uint32_t kSfStage = 8 + 8 * kRowBlocks;
   static constexpr uint32_t kTmemUsed = kSfCol + kSfStage * kStages;
   static constexpr uint32_t kTmemCols = kTmemUsed <= 128 ? 128 : (kTmemUsed <= 256 ? 256 : 512);
@@ -389,9 +386,9 @@ __global__ void __launch_bounds__(kVThreads)
           for (int g = 0; g < 4; ++g) {
             if (g >= left) break;
             const uint32_t id = 2u * (g & 1);
-            v_mma(tmem + (g % L::kAcc) * L::kN, a0 + (s * (L::kA >> 4) + 2 * g),
+            v_mma(tmem, a0 + (s * (L::kA >> 4) + 2 * g),
                   x0 + (s * (L::kX >> 4) + 2 * g), L::kIdesc | (id << 29) | (id << 4),
-                  (s > 0 || g >= L::kAcc || kb > kb0) ? 1u : 0u,
+                  (s > 0 || g > 0 || kb > kb0) ? 1u : 0u,
                   (sfa + 4 * (g >> 1)) | (id << 30),
                   (sfb + 4 * (g >> 1) * L::kRowBlocks) | (id << 30));
           }
@@ -426,9 +423,6 @@ __global__ void __launch_bounds__(kVThreads)
                      : "memory");
     }
   }
-  // accumulators that had an MMA (a short slab may not reach all of them)
-  const int used = min(L::kAcc, sh.steps - 4 * kb0);
-
   // Epilogue: warp w reads lane quarter w % 4, rows 32 q + lane. In a cluster
   // the rows are shared out for the joining, 128 / split to a rank: every
   // rank stores its sums for them at their owner, which adds them in order.
@@ -449,27 +443,25 @@ __global__ void __launch_bounds__(kVThreads)
 #pragma unroll 1
     for (int c = 0; c < tokens; c += kC) {
       float v[kC];
+      uint32_t r[kVDigits][4];
 #pragma unroll
-      for (int j = 0; j < kC; ++j) v[j] = 0.0f;
+      for (int p = 0; p < kVDigits; ++p) {
+        const uint32_t at = tb + p * T + c;
+        if constexpr (kC == 2)
+          asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];"
+                       : "=r"(r[p][0]), "=r"(r[p][1])
+                       : "r"(at));
+        else
+          asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(r[p][0]), "=r"(r[p][1]), "=r"(r[p][2]), "=r"(r[p][3])
+                       : "r"(at));
+      }
+      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
 #pragma unroll
-      for (int p = kVDigits - 1; p >= 0; --p) {
+      for (int j = 0; j < kC; ++j) {
+        v[j] = __uint_as_float(r[kVDigits - 1][j]);
 #pragma unroll
-        for (int a = 0; a < L::kAcc; ++a) {
-          if (a >= used) break;
-          uint32_t r[4];
-          const uint32_t at = tb + a * L::kN + p * T + c;
-          if constexpr (kC == 2)
-            asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0, %1}, [%2];"
-                         : "=r"(r[0]), "=r"(r[1])
-                         : "r"(at));
-          else
-            asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                         : "r"(at));
-          asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-          for (int j = 0; j < kC; ++j) v[j] = __fadd_rn(v[j], __uint_as_float(r[j]));
-        }
+        for (int p = kVDigits - 2; p >= 0; --p) v[j] = __fadd_rn(v[j], __uint_as_float(r[p][j]));
       }
 #pragma unroll
       for (int j = 0; j < kC; ++j) {

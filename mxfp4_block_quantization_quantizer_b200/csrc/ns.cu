@@ -9,7 +9,10 @@
 // for A (half of a symmetric product), s^3 for A A (half) and 2 s s l for
 // B X. Three products a step, each a persistent tcgen05 GEMM with a fused
 // epilogue; only the tiles on and above the diagonal of A and B are computed
-// and written to both sides.
+// and written to both sides. (The sums of a tile stay in one accumulator: four
+// that a stage's MMAs took in turn made small products 2 to 5% slower.) Small
+// matrices are bound by the latency of 17 launches that depend on one another,
+// about 5 us each; each may set itself up while the one before it ends.
 //
 // Numbers: operands are fp16, not bf16, at the same tensor rate and with
 // three more significant bits. Their range suffices because everything here
@@ -57,8 +60,6 @@ struct NsArgs {
   int* status;
 };
 
-__host__ __device__ constexpr int ns_acc(int bn) { return 256 / bn; }
-
 template <int BN>
 struct NsLayout {
   static constexpr int kStages = BN == 128 ? 6 : 8;
@@ -68,11 +69,7 @@ struct NsLayout {
   static constexpr uint32_t kEpiOff = kBOff + kStages * kB;
   static constexpr uint32_t kBarOff = kEpiOff + kSEpiWarps * 32 * 80;
   static constexpr uint32_t kBytes = kBarOff + 256;
-  // Accumulators of a tile: consecutive MMAs on one wait for each other, about
-  // 150 clocks, which 128 x 256 products cover and narrower ones do not; the
-  // four MMAs of a stage take turns, and the epilogue adds. Two tiles' worth.
-  static constexpr int kAcc = ns_acc(BN);
-  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kTmemCols = 2 * BN;  // two accumulators
   // kind::f16: fp32 accumulator, fp16 operands (0), majorness bits 15, 16
   __host__ __device__ static constexpr uint32_t idesc(bool a_mn, bool b_mn) {
     return (1u << 4) | (uint32_t(a_mn) << 15) | (uint32_t(b_mn) << 16) |
@@ -104,8 +101,8 @@ __device__ __forceinline__ uint64_t smem_desc_mn(const void* p) {
 
 // Tile `t` of the order that all roles walk. Full products: groups of 16 row
 // tiles swept across all column tiles (their panels stay in L2). Symmetric
-// products: the tiles that reach the diagonal or above, 256 (or BN) columns'
-// worth of rows at a time.
+// products: the tiles that reach the diagonal or above, column by column
+// (narrow tiles: row by row).
 template <int BN, bool SYM>
 __device__ __forceinline__ void ns_tile(int64_t t, int64_t mt, int64_t nt, int64_t& m0,
                                         int64_t& n0) {
@@ -257,15 +254,6 @@ __device__ __forceinline__ bool ns_epilogue(const NsArgs& p, int64_t row, int64_
     if constexpr (kHasC)
       if (cb + 32 < kCols) fetch(next, c0 + 32);
     asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-    for (int a = 1; a < ns_acc(BN); ++a) {
-      uint32_t u[32];
-      MXFP4_TMEM_LD32(u, tb + cb + a * BN);
-      asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        v[j] = __float_as_uint(__fadd_rn(__uint_as_float(v[j]), __uint_as_float(u[j])));
-    }
     if (!ok || failed_flag(failed)) {
 #pragma unroll
       for (int j = 0; j < 32; ++j) v[j] = 0x7FC00000u;
@@ -464,7 +452,7 @@ struct NsIssuer {
     const uint32_t buf = ti & 1, bph = (ti >> 1) & 1u;
     if (!warp_wait(&acc_empty[buf], bph ^ 1u, failed)) return false;
     asm volatile("tcgen05.fence::after_thread_sync;");
-    const uint32_t acc = tmem + buf * 256;
+    const uint32_t acc = tmem + buf * BN;
     bool ok = true;
     for (int kb = 0; kb < n_kb; ++kb) {
       if (!warp_wait(&full[s], ph, failed)) {
@@ -477,8 +465,7 @@ struct NsIssuer {
       if (lead) {
 #pragma unroll
         for (uint32_t j = 0; j < kSK / 16; ++j)
-          mma_f16(acc + (j % L::kAcc) * BN, ad + j * ka, bd + j * kb_, idesc,
-                  (kb > 0 || j >= L::kAcc) ? 1u : 0u);
+          mma_f16(acc, ad + j * ka, bd + j * kb_, idesc, (kb > 0 || j > 0) ? 1u : 0u);
         commit_to(bar);
       }
       if (++s == L::kStages) s = 0, ph ^= 1u;
@@ -579,7 +566,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
       ns_tile<BN, kSym>(t, mt, nt, m0, n0);
       const uint32_t buf = uint32_t(ti & 1), bph = uint32_t(ti >> 1) & 1u;
       const bool ok = ns_epilogue<BN, MODE, kSym>(p, m0 + 32 * q + lane, n0 + (BN / 2) * half,
-                                            tmem + buf * 256 + (uint32_t(32 * q) << 16) +
+                                            tmem + buf * BN + (uint32_t(32 * q) << 16) +
                                                 uint32_t((BN / 2) * half),
                                             sm + L::kEpiOff + (warp - 2) * (32 * 80),
                                             &acc_full[buf], bph, failed);
