@@ -513,8 +513,8 @@ int gemv_tokens(int64_t m) { return m <= 2 ? 2 : (m <= 8 ? 8 : (m <= 16 ? 16 : 3
 // Slabs of k (a power of two up to the portable cluster size): up to one CTA
 // an SM in any case, up to `per_sm` CTAs an SM (whose loads together keep an
 // SM's share of the memory bandwidth busy) where that leaves a slab four
-// stages. 8192 x 28672 (2 CTAs an SM / 1): 25.4 / 30.8 us; 4096 x 4096, with
-// slabs of 2 / 4 stages: 9.3 / 7.6 us (clusters start one after another).
+// stages. 8192 x 28672 (2 CTAs an SM / 1): 23.8 / 24.6 us; 4096 x 4096, with
+// slabs of 2 / 4 stages: 8.3 / 6.5 us (clusters start one after another).
 int gemv_split(int64_t tiles, int64_t stages, int per_sm) {
   int split = 1;
   while (split < 8 && stages >= 2 * split &&

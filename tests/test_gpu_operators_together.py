@@ -143,3 +143,61 @@ def test_side_stream_owns_its_memory():
         for a, b in zip(got, want):
             assert torch.equal(a, b)
         del got, junk
+
+
+def test_layernorm_past_32_bit_offsets():
+    """More than 2^31 elements: the last rows are those of a call on them
+    alone, and the first ones too (a row's bits depend on its content and the
+    split of a row over warps, which follows from the columns)."""
+    cols, rows = 2048, (1 << 20) + 77
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device="cuda")
+    x.view(-1)[:] = 1.0
+    ends = randn(2 * 2048, cols, seed=30).to(torch.bfloat16)
+    x[:2048], x[-2048:] = ends[:2048], ends[2048:]
+    w, b = 1 + 0.1 * randn(cols, seed=31), randn(cols, seed=32)
+    y, mean, rstd = m.layernorm(x, w, b, want_stats=True)
+    codes, scales = m.layernorm_quantize(x, w, b)
+    assert torch.equal(y[5000], b.to(torch.bfloat16))           # a constant row
+    small = m.layernorm(ends, w, b, want_stats=True)
+    qc, qs = m.layernorm_quantize(ends, w, b)
+    for got, want in zip((y, mean, rstd, codes, scales), (*small, qc, qs)):
+        assert torch.equal(got[:2048], want[:2048])
+        assert torch.equal(got[-2048:], want[2048:])
+    dx, dw, db = m.layernorm_backward(x, x, mean, rstd, w)
+    sx, _, _ = m.layernorm_backward(ends, ends, *small[1:], w)
+    assert torch.equal(dx[:2048], sx[:2048]) and torch.equal(dx[-2048:], sx[2048:])
+    # constant rows have h = 0: dw is that of the ends; db counts every row
+    h = (ends.double() - small[1].double()[:, None]) * small[2].double()[:, None]
+    want_w = (ends.double() * h).sum(0)
+    # each product is off by 2^-22 of its size, the fixed-order fp32 sums by
+    # at most 2^-24 for each of the (rows / CTA + CTAs) additions that are not
+    # of zeros: 4096 bounds them
+    tol = (2.0 ** -22 + 4096 * 2.0 ** -24) * (ends.double() * h).abs().sum(0) + 1e-6
+    assert ((dw.double() - want_w).abs() <= tol).all()
+    want_b = ends.double().sum(0) + (rows - 4096)
+    # about 2^20 ones: sums of a CTA (below 2^24) are off by 2^-24 of what
+    # they hold at each of about 7200 additions
+    tol = 8192 * 2.0 ** -24 * (ends.double().abs().sum(0) + (rows - 4096))
+    assert ((db.double() - want_b).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("rows", [1, 3, 17])
+def test_gemv_past_32_bit_offsets(rows):
+    """A weight of more than 2^31 bytes of codes: its last row block."""
+    n, k = 65536 + 64, 65536
+    g = torch.Generator(device="cuda")
+    g.manual_seed(33)
+    codes = torch.zeros(n, k // 2, dtype=torch.uint8, device="cuda")
+    last = n - n % 128 - 128
+    codes[last:] = torch.randint(0, 256, (n - last, k // 2), dtype=torch.uint8, device="cuda",
+                                 generator=g)
+    scales = torch.full((n, k // 32), 120, dtype=torch.uint8, device="cuda")
+    blocked = m.scales_to_blocked(scales)
+    x = randn(rows, k, seed=34).to(torch.bfloat16)
+    y = m.gemv(x, codes, blocked, out_dtype=torch.float32)
+    assert (y[:, :last] == 0).all()
+    w = m.dequantize(codes[last:].contiguous(), scales[last:].contiguous(), n - last, k,
+                     out_dtype=torch.float32).double()
+    want = x.double() @ w.T
+    bound = (k + 64) * 2.0 ** -24 * 1.25 * (x.double().abs() @ w.abs().T) + 1e-6
+    assert ((y[:, last:].double() - want).abs() <= bound).all()
