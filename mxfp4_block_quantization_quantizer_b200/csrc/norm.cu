@@ -538,7 +538,7 @@ __global__ void __launch_bounds__(512)
   if (p.CS > 1) pair_sync();  // no CTA ends while the other may still write to it
 }
 
-// Rows wider than the registers of 16 warps: one CTA a row, three passes
+// Rows wider than the registers of a cluster: one CTA a row, three passes
 // over it (the second and third from L2).
 __device__ __forceinline__ float block_sum(float v, float* sh) {
   v = warp_sum(v);
@@ -1014,7 +1014,7 @@ __global__ void __launch_bounds__(kLnRowWarps * 32)
   }
 }
 
-// Rows wider than the registers of 16 warps: dx with one CTA a row, and the
+// Rows wider than the registers of a cluster: dx with one CTA a row, and the
 // column sums by a kernel of their own that reads x and dy again.
 template <bool BF16>
 __global__ void __launch_bounds__(kLnGenThreads)
@@ -1223,19 +1223,35 @@ cudaError_t fwd_nv(const FwdArgs& a, const LnShape& sh, bool edge, int misaligne
 template <bool BF16>
 cudaError_t fwd_any(const FwdArgs& a) {
   constexpr int kSize = BF16 ? 2 : 4, VEC = 16 / kSize;
-  constexpr int kBig = BF16 ? 3 : 4;
+  // Vectors a thread, more (32 elements, the parameters in registers beside
+  // them at 128 registers a thread) where fewer lanes are then idle, or where
+  // a row needs a cluster otherwise (whose barrier a row cost more than a few
+  // spilled registers). bf16, 3 / 4: 8192 x 4096 32.3 / 25.3 us, 4096 x 14336
+  // 103 / 49 us; fp32, 4 / 8: 4096 x 8192 45.4 / 47.5 us, 4096 x 14336
+  // 143 / 86 us.
+  constexpr int kBig = BF16 ? 3 : 4, kWide = BF16 ? 4 : 8;
   LnShape sh;
-  bool edge;
-  int mis;
+  bool edge = false;
+  int mis = 0;
   const void* const ptrs[] = {a.x, a.y};
   const int64_t lds[] = {a.ldx, a.cols};
-  if (a.cols <= kLnMaxCols && vector_rows(ptrs, lds, 2, a.cols, kSize, &edge, &mis) &&
+  const bool vec = a.cols <= kLnMaxCols && vector_rows(ptrs, lds, 2, a.cols, kSize, &edge, &mis);
+  const int64_t nvec = (a.cols + VEC - 1) / VEC + (edge ? 1 : 0);
+  const int64_t wb = (nvec + 32 * kBig - 1) / (32 * kBig);
+  const int64_t ww = (nvec + 32 * kWide - 1) / (32 * kWide);
+  const bool more = wb > kLnMaxWarps || ww * kWide < wb * kBig;
+  if (vec &&
       !(edge && a.codes != nullptr) &&
-      ln_shape((a.cols + VEC - 1) / VEC + (edge ? 1 : 0), kBig, a.rows, kLnFwdWarps, &sh)) {
+      ln_shape(nvec, more ? kWide : kBig, a.rows, kLnFwdWarps, &sh)) {
     const bool multi = sh.split.W * sh.split.CS > 1;
     if (sh.nv == 1)
       return multi ? fwd_nv<BF16, 1, true>(a, sh, edge, mis)
                    : fwd_nv<BF16, 1, false>(a, sh, edge, mis);
+    if (more) {
+      if constexpr (BF16)
+        if (!multi) return fwd_nv<BF16, kWide, false>(a, sh, edge, mis);
+      return fwd_nv<BF16, kWide, true>(a, sh, edge, mis);
+    }
     return multi ? fwd_nv<BF16, kBig, true>(a, sh, edge, mis)
                  : fwd_nv<BF16, kBig, false>(a, sh, edge, mis);
   }
