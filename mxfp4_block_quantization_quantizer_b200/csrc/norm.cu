@@ -31,6 +31,11 @@
 // two ends of a row moves as aligned 16-byte vectors (vectors that reach into
 // a neighbouring row are read whole and masked, and stored element by
 // element).
+//
+// Measured, of a plain copy's rate: forward 12608 x 1536 bf16 15.0 us (78%),
+// 8192 x 4096 bf16 24.4 us (84%), 4096 x 14336 fp32 84 us (85%), 5000 x 2563
+// bf16 (off the boundary) 21 us (38%); backward 12608 x 1536 bf16 27.6 us
+// (65%), 8192 x 4096 bf16 42.5 us (72%), 4096 x 14336 fp32 153 us (71%).
 #include "launch.cuh"
 #include "mxfp4_device.cuh"
 

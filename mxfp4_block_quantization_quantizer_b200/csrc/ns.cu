@@ -11,8 +11,10 @@
 // epilogue; only the tiles on and above the diagonal of A and B are computed
 // and written to both sides. (The sums of a tile stay in one accumulator: four
 // that a stage's MMAs took in turn made small products 2 to 5% slower.) Small
-// matrices are bound by the latency of 17 launches that depend on one another,
-// about 5 us each; each may set itself up while the one before it ends.
+// matrices are bound by the latency of launches that depend on one another,
+// about 5 us each (256 x 512, five steps, 17 launches: 84 us); each may set
+// itself up while the one before it ends. Large ones: 4096 x 14336, five
+// steps, 3.4 to 3.5 ms, 1.13 to 1.16 PFLOP/s of the flops above.
 //
 // Numbers: operands are fp16, not bf16, at the same tensor rate and with
 // three more significant bits. Their range suffices because everything here
