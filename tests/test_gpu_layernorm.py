@@ -258,3 +258,26 @@ def test_two_streams_at_once():
     for g in got:
         for a, c in zip(g, want):
             assert torch.equal(a, c)
+
+
+# more rows than a round of the persistent grid, at the widths where a thread
+# holds most: one warp a row, several, a whole CTA, a cluster of two
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("shape", [(2500, 1024), (2500, 1023), (1500, 2563), (700, 4096),
+                                   (701, 8192), (611, 8195), (611, 14336), (597, 14337),
+                                   (350, 16384), (333, 24576), (310, 24577)])
+def test_many_wide_rows(shape, dt):
+    x, dy, w, b = inputs(*shape, dt, 12)
+    x[-1] = 2.0
+    x[3, -1] = float("inf")
+    y, mean, rstd = m.layernorm(x, w, b, want_stats=True)
+    assert torch.isnan(y[3]).all()
+    keep = [i for i in range(shape[0]) if i != 3]
+    check_forward(x[keep], w, b, 1e-5, y[keep], mean[keep], rstd[keep])
+    if shape[1] % 32 == 0:
+        codes, scales = m.layernorm_quantize(x, w, b)
+        want = m.quantize(y)
+        assert torch.equal(codes, want[0]) and torch.equal(scales, want[1])
+    x[3, -1] = 0.0
+    y, mean, rstd = m.layernorm(x, w, b, want_stats=True)
+    check_backward(dy, x, mean, rstd, w, *m.layernorm_backward(dy, x, mean, rstd, w))
