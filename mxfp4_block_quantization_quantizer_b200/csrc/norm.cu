@@ -801,7 +801,9 @@ __global__ void __launch_bounds__(512)
 
   if constexpr (PARAMS) {
     // the groups of a CTA (same columns, same `off`) add into shared memory
-    // one after the other; the last one writes the partial row
+    // one after the other; the last one writes the partial row (a CTA whose
+    // first group has no row has none: the workspace ends before its place)
+    const bool used = p.row0 - p.g * (EDGE ? VEC : 1) < rows;
     float* pw = partial + int64_t(blockIdx.x / p.CS) * 2 * cols;
     float* sacc = reinterpret_cast<float*>(ring);  // [2][slots VEC]
     const int G = (blockDim.x >> 5) / p.W;
@@ -819,7 +821,7 @@ __global__ void __launch_bounds__(512)
             if (g > 0) a = __fadd_rn(a, sacc[at]), b = __fadd_rn(b, sacc[slots * VEC + at]);
             if (g + 1 < G) {
               sacc[at] = a, sacc[slots * VEC + at] = b;
-            } else if (c0 + j >= 0 && c0 + j < cols) {
+            } else if (used && c0 + j >= 0 && c0 + j < cols) {
               pw[c0 + j] = a, pw[cols + c0 + j] = b;
             }
           }
@@ -1173,6 +1175,16 @@ int ln_grid(const void* kern, const LnShape& sh, size_t smem, int64_t rows, bool
   return int((n < unit ? unit : n) * sh.split.CS);
 }
 
+// How many of a backward grid's `blocks` clusters have rows, the first ones
+// (see Place): each writes a partial row of dw and db. At most `rows`, also
+// where the grid was rounded up to the vector length.
+int64_t ln_partials(const LnShape& sh, int64_t rows, bool edge, int vec, int64_t blocks) {
+  const int64_t unit = edge ? vec : 1, round = sh.split.G * unit;
+  const int64_t rest = rows % round < unit ? rows % round : unit;
+  const int64_t n = rows / round * unit + rest;
+  return n < blocks ? n : blocks;
+}
+
 template <typename... P, typename... A>
 cudaError_t ln_launch(void (*kern)(P...), int grid, const LnShape& sh, size_t smem,
                       cudaStream_t s, A... args) {
@@ -1305,7 +1317,7 @@ cudaError_t bwd_launch(const BwdArgs& a, const LnShape& sh, int misaligned) {
   e = ln_launch(kern, grid, sh, smem, a.s, a.dy, a.x, a.rows, int(a.cols), a.lddy, a.ldx,
                 misaligned, a.weight, a.mean, a.rstd, a.dx, a.partial, sh.split);
   if (e != cudaSuccess || !PARAMS) return e;
-  return params_launch(a, grid / sh.split.CS);
+  return params_launch(a, int(ln_partials(sh, a.rows, EDGE, VEC, grid / sh.split.CS)));
 }
 
 template <bool BF16, bool MULTI, bool PARAMS>
@@ -1320,7 +1332,7 @@ cudaError_t bwd_rows(const BwdArgs& a, const LnShape& sh) {
   e = ln_launch(kern, grid, sh, smem, a.s, a.dy, a.x, a.rows, int(a.cols), a.lddy, a.ldx,
                 a.weight, a.mean, a.rstd, a.dx, a.partial, sh.split);
   if (e != cudaSuccess || !PARAMS) return e;
-  return params_launch(a, grid);
+  return params_launch(a, int(ln_partials(sh, a.rows, false, VEC, grid)));
 }
 template <bool BF16>
 cudaError_t bwd_rows_any(const BwdArgs& a, int64_t nvec) {

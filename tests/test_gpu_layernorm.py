@@ -281,3 +281,45 @@ def test_many_wide_rows(shape, dt):
     x[3, -1] = 0.0
     y, mean, rstd = m.layernorm(x, w, b, want_stats=True)
     check_backward(dy, x, mean, rstd, w, *m.layernorm_backward(dy, x, mean, rstd, w))
+
+
+# rows off the 16-byte boundary share a grid of whole groups of 8 (4) blocks;
+# few rows leave some of them without any: one warp a row, several, a cluster,
+# and more columns than a cluster holds
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("rows", [1, 3, 5, 9, 33, 100, 197, 301, 595])
+@pytest.mark.parametrize("cols", [5, 63, 1111, 4099, 9001, 16383, 70001])
+def test_backward_stays_inside_its_workspace(rows, cols, dt):
+    """A workspace of exactly the stated size: the bytes on both sides stay as
+    they were, and what it held before does not matter."""
+    if rows * cols > 6_000_000:
+        rows = max(1, 6_000_000 // cols) | 1
+    x, dy, w, b = inputs(rows, cols, dt, 16)
+    _, mean, rstd = m.layernorm(x, w, b, want_stats=True)
+    need = m.lib().mxfp4_layernorm_backward_workspace(rows, cols)
+    pad = 16 * 8 * cols + 4096           # more than 8 partial rows [2][cols]
+    buf = torch.full((256 + need + pad,), 0xFF, dtype=torch.uint8, device="cuda")
+    out = m.layernorm_backward(dy, x, mean, rstd, w, workspace=buf[256:256 + need])
+    torch.cuda.synchronize()
+    assert (buf[:256] == 0xFF).all() and (buf[256 + need:] == 0xFF).all()
+    check_backward(dy, x, mean, rstd, w, *out)
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("rows", [1, 6, 21])
+def test_backward_of_shifted_tensors_stays_inside_its_workspace(rows, dt):
+    """Whole vectors a row, but every tensor starts one element late."""
+    cols = 256
+    x, dy, w, b = inputs(rows, cols, dt, 17)
+    late = [torch.zeros(rows * cols + 1, dtype=dt, device="cuda")[1:].view(rows, cols)
+            for _ in range(3)]
+    late[0].copy_(x), late[1].copy_(dy)
+    _, mean, rstd = m.layernorm(x, w, b, want_stats=True)
+    dw, db = torch.empty(cols, device="cuda"), torch.empty(cols, device="cuda")
+    need = m.lib().mxfp4_layernorm_backward_workspace(rows, cols)
+    buf = torch.full((256 + need + 40 * cols * 8,), 0xFF, dtype=torch.uint8, device="cuda")
+    m.layernorm_backward(late[1], late[0], mean, rstd, w, out=(late[2], dw, db),
+                         workspace=buf[256:256 + need])
+    torch.cuda.synchronize()
+    assert (buf[:256] == 0xFF).all() and (buf[256 + need:] == 0xFF).all()
+    check_backward(dy, x, mean, rstd, w, late[2], dw, db)
