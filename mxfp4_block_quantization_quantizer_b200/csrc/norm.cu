@@ -159,6 +159,15 @@ __device__ __forceinline__ void pair_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\t"
                "barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// A cluster's CTAs may start at different times, and none may be written to
+// before it runs: every thread arrives as its kernel begins and waits before
+// the first row, when the loads ahead of that are under way.
+__device__ __forceinline__ void pair_started() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_wait_started() {
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 __device__ __forceinline__ void store_pair(float2* p, float2 v, uint32_t rank) {
   uint32_t a;
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
@@ -354,6 +363,7 @@ __global__ void __launch_bounds__(512)
   extern __shared__ __align__(16) uint4 ring[];  // [warps][D][NV][32]
   __shared__ float2 red[2][kLnMaxParts];
   const Place p = place<VEC, NV, EDGE>(split, rows, cols, ldx, misaligned);
+  if (MULTI && p.CS > 1) pair_started();
   uint4* const mine = ring + p.warp * (D * NV * 32) + p.lane;
 
   Walk wx = walk<BF16>(x, rows, ldx, p);
@@ -406,6 +416,7 @@ __global__ void __launch_bounds__(512)
   const float inv0 = __shfl_sync(0xFFFFFFFFu, l_inv, 0);
   const float inv1 = __shfl_sync(0xFFFFFFFFu, l_inv, 1);
 
+  if (MULTI && p.CS > 1) pair_wait_started();
   // the cluster's CTAs walk the same rows; so do the warps of a group
   int d = 0, par = 0;
   int64_t row = p.row0;
@@ -634,6 +645,7 @@ __global__ void __launch_bounds__(512)
   extern __shared__ __align__(16) uint4 ring[];  // [warps][D][2 NV][32], then w
   __shared__ float2 red[2][kLnMaxParts];
   const Place p = place<VEC, NV, EDGE>(split, rows, cols, ldx, misaligned);
+  if (MULTI && p.CS > 1) pair_started();
   const int slots = p.W * NV * 32, s0 = p.w * NV * 32 + p.lane;
   float* const sw = reinterpret_cast<float*>(ring + (blockDim.x >> 5) * (D * 2 * NV * 32));
   uint4* const mine = ring + p.warp * (D * 2 * NV * 32) + p.lane;
@@ -695,6 +707,7 @@ __global__ void __launch_bounds__(512)
     cp_async_wait<D>();  // the weight
     __syncthreads();
   }
+  if (MULTI && p.CS > 1) pair_wait_started();
 
   int d = 0, par = 0;
   for (int left = p.n; left > 0; --left, par ^= 1) {

@@ -323,3 +323,29 @@ def test_backward_of_shifted_tensors_stays_inside_its_workspace(rows, dt):
     torch.cuda.synchronize()
     assert (buf[:256] == 0xFF).all() and (buf[256 + need:] == 0xFF).all()
     check_backward(dy, x, mean, rstd, w, late[2], dw, db)
+
+
+@pytest.mark.parametrize("dt,cols", [(F, 24576), (BF, 24576), (F, 14336), (BF, 14336)])
+def test_clusters_that_start_apart(dt, cols):
+    """Rows over two CTAs while products on another stream hold most of the
+    SMs, which come free one after another: a row of each cluster is its
+    first, and the same bits come out as on an idle GPU."""
+    x, dy, w, b = inputs(200, cols, dt, 18)
+
+    def work():
+        y, mean, rstd = m.layernorm(x, w, b, want_stats=True)
+        return (y, mean, rstd, *m.layernorm_backward(dy, x, mean, rstd, w))
+    want = work()
+    check_forward(x, w, b, 1e-5, *want[:3])
+    check_backward(dy, x, want[1], want[2], w, *want[3:])
+    side = torch.cuda.Stream()
+    a = torch.randn(2048, 2048, device="cuda", dtype=BF)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        with torch.cuda.stream(side):
+            for _ in range(6):
+                a @ a
+        got = work()
+        for p, q in zip(got, want):
+            assert torch.equal(p, q)
+    torch.cuda.synchronize()
