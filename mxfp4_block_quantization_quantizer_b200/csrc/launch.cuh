@@ -13,7 +13,7 @@ int persistent_grid(const void* kernel, int threads, size_t smem,
                     int64_t work_blocks);
 
 // Lets `kernel` take `bytes` of dynamic shared memory on the current device
-// (asked of the runtime when the limit has to grow).
+// (the runtime is asked once per thread, kernel and device).
 cudaError_t allow_smem(const void* kernel, size_t bytes);
 
 // oas: the overflow-aware scale rule instead of the OCP one.

@@ -1163,26 +1163,36 @@ int persistent_grid(const void* kernel, int threads, size_t smem,
 }
 
 cudaError_t allow_smem(const void* kernel, size_t bytes) {
+  // The limit belongs to the kernel and the device, for all threads: it is
+  // set to the one value that every call asks for, the most a block of this
+  // kernel can have, so that no thread lowers what another one relies on.
   struct Entry {
     const void* kernel;
     int dev;
-    size_t bytes;
+    size_t most;
   };
   constexpr int kEntries = 64;
   static thread_local Entry cache[kEntries] = {};
   int dev = 0;
   cudaGetDevice(&dev);
   Entry& c = cache[(reinterpret_cast<uintptr_t>(kernel) >> 4) % kEntries];
-  if (c.kernel == kernel && c.dev == dev && c.bytes >= bytes) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(
-      kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
-  // all of the SM's on-chip memory that can be shared memory: the default
-  // split otherwise follows one CTA's need and holds fewer CTAs
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             int(cudaSharedmemCarveoutMaxShared));
-  if (e == cudaSuccess) c = {kernel, dev, bytes};
-  return e;
+  if (c.kernel != kernel || c.dev != dev) {
+    int block = 0;
+    cudaFuncAttributes attr;
+    cudaError_t e = cudaDeviceGetAttribute(&block, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&attr, kernel);
+    if (e != cudaSuccess) return e;
+    const size_t most = size_t(block) - attr.sharedSizeBytes;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(most));
+    // all of the SM's on-chip memory that can be shared memory: the default
+    // split otherwise follows one CTA's need and holds fewer CTAs
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                               int(cudaSharedmemCarveoutMaxShared));
+    if (e != cudaSuccess) return e;
+    c = {kernel, dev, most};
+  }
+  return bytes <= c.most ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 template <bool BF16, bool SR, bool OAS>

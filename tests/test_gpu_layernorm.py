@@ -349,3 +349,33 @@ def test_clusters_that_start_apart(dt, cols):
         for p, q in zip(got, want):
             assert torch.equal(p, q)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dt,wide,narrow", [(BF, 4096, 2048), (F, 2048, 1024), (F, 8192, 4112)])
+def test_threads_take_turns_at_one_kernel(dt, wide, narrow):
+    """One kernel asks for shared memory by the width of its rows. A second
+    thread that comes to it with narrower rows takes nothing from the first."""
+    import threading
+    make = lambda cols: inputs(700, cols, dt, 19)
+    (x, dy, w, b), (x2, dy2, w2, b2) = make(wide), make(narrow)
+
+    def work(x, dy, w, b):
+        y, mean, rstd = m.layernorm(x, w, b, want_stats=True)
+        return (y, *m.layernorm_backward(dy, x, mean, rstd, w))
+    want, want2 = work(x, dy, w, b), work(x2, dy2, w2, b2)
+    want = work(x, dy, w, b)                 # this thread's last width: the wide one
+    failures = []
+
+    def other():
+        try:
+            for p, q in zip(work(x2, dy2, w2, b2), want2):
+                assert torch.equal(p, q)
+        except BaseException as e:           # noqa: B902 (reported below)
+            failures.append(e)
+    for _ in range(3):
+        t = threading.Thread(target=other)   # a thread that has called nothing yet
+        t.start()
+        t.join()
+        assert not failures, failures
+        for p, q in zip(work(x, dy, w, b), want):
+            assert torch.equal(p, q)
