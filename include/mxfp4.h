@@ -411,13 +411,13 @@ int64_t mxfp4_gemv_workspace(int64_t m, int64_t n, int64_t k);
  *            ldx >= k a multiple of 8
  *   b_codes  device [n][k/2], 16-byte aligned
  *   b_scales device, blocked order (rows = n, groups = k/32), 16-byte aligned
- *   y        device [m][n] of y_dtype, 16-byte aligned, written; must not
- *            overlap x
+ *   y        device [m][n] of y_dtype, 16-byte aligned, written
  *   workspace  device, 16-byte aligned, workspace_bytes of scratch (at least
  *            mxfp4_gemv_workspace; NULL where that is 0); calls that run at
  *            the same time need workspaces of their own
  *   status   device int or NULL (MXFP4_STATUS_WAIT_TIMEOUT above); the tiles
  *            of a CTA whose wait ran out hold NaN
+ * y, workspace and status overlap neither the inputs nor one another.
  * k must be a multiple of 32, m at most 2^19, k at most 2^30. A group of x that holds Inf or
  * NaN makes its row of Y NaN, a scale byte of 0xFF its column.
  * Any m works; from about a hundred rows on, quantizing X (mxfp4_gemm) or
@@ -461,6 +461,7 @@ int64_t mxfp4_newton_schulz_workspace(int64_t rows, int64_t cols);
  *            time need workspaces of their own
  *   status   device int or NULL (MXFP4_STATUS_WAIT_TIMEOUT above); when it is
  *            set, the tiles of OUT that were not completed hold NaN
+ * workspace and status overlap neither g nor out nor one another.
  * Any rows, cols up to MXFP4_NS_MAX_DIM. G of zeros gives zeros (eps > 0);
  * Inf or NaN in G gives NaN.
  */
@@ -482,9 +483,10 @@ mxfp4_status mxfp4_newton_schulz(const void* g, int dtype, int64_t rows, int64_t
  *          aligned rows are faster
  *   weight, bias  device fp32 [cols] or NULL (1 and 0)
  *   eps    >= 0 and finite
- *   y      device, written: [rows][cols] of dtype; must not overlap x
+ *   y      device, written: [rows][cols] of dtype
  *   mean, rstd  device fp32 [rows] or NULL: the statistics the backward pass
  *          takes
+ * What is written overlaps neither the inputs nor one another.
  * Any rows, cols > 0 within the size limit. A row that holds Inf or NaN
  * gives NaN in that row.
  */
@@ -501,7 +503,8 @@ mxfp4_status mxfp4_layernorm(const void* x, int dtype, int64_t rows, int64_t col
  * forward pass).
  *   y       as in mxfp4_layernorm, or NULL
  *   codes, scales  device, ROWS layout; codes 16-byte aligned
- * cols must be a multiple of 32.
+ * cols must be a multiple of 32. What is written overlaps neither the inputs
+ * nor one another.
  */
 mxfp4_status mxfp4_layernorm_quantize(const void* x, int dtype, int64_t rows, int64_t cols,
                                       int64_t ldx, const float* weight, const float* bias,
@@ -522,12 +525,14 @@ int64_t mxfp4_layernorm_backward_workspace(int64_t rows, int64_t cols);
  *   dy, x   device, of dtype, row strides lddy and ldx (elements)
  *   weight  device fp32 [cols] or NULL (1)
  *   mean, rstd  device fp32 [rows], from the forward pass
- *   dx      device, written: [rows][cols] of dtype; must not overlap dy or x
+ *   dx      device, written: [rows][cols] of dtype
  *   dw, db  device fp32 [cols], written; both NULL to leave them out
  *   workspace  device, 16-byte aligned, workspace_bytes of scratch (at least
  *           mxfp4_layernorm_backward_workspace); not read by a later call.
  *           NULL only where dw and db are. Calls that run at the same time
  *           need workspaces of their own.
+ * dx and workspace overlap neither the inputs nor one another; dw and db
+ * overlap neither these two nor one another.
  */
 mxfp4_status mxfp4_layernorm_backward(const void* dy, const void* x, int dtype, int64_t rows,
                                       int64_t cols, int64_t lddy, int64_t ldx,

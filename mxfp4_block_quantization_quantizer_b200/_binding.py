@@ -491,15 +491,25 @@ def _rows2d(t, name):
     return ld
 
 
-def _apart(out, name, *inputs):
-    """Refuse an output whose storage range meets that of an input."""
-    for t in inputs:
-        if t.numel() and out.numel():
-            last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
-            a0, a1 = t.data_ptr(), t.data_ptr() + (last + 1) * t.element_size()
-            b0, b1 = out.data_ptr(), out.data_ptr() + out.numel() * out.element_size()
+def _span(t):
+    """First and last + 1 address of the elements of t."""
+    last = sum((n - 1) * s for n, s in zip(t.shape, t.stride()))
+    a = t.data_ptr()
+    return (a, a + (last + 1) * t.element_size()) if t.numel() else (a, a)
+
+
+def _apart(written, read=()):
+    """Refuse written tensors, (name, tensor or None) pairs, whose memory meets
+    that of a tensor that is read, or of one another."""
+    taken = [_span(t) for t in read if t is not None]
+    for name, t in written:
+        if t is None:
+            continue
+        a0, a1 = _span(t)
+        for b0, b1 in taken:
             if a0 < b1 and b0 < a1:
-                raise ValueError("%s overlaps an input" % name)
+                raise ValueError("%s overlaps another argument" % name)
+        taken.append((a0, a1))
 
 
 def gemv(x, b_codes, b_blocked, out_dtype=torch.bfloat16, out=None, workspace=None, stream=None,
@@ -520,14 +530,17 @@ def gemv(x, b_codes, b_blocked, out_dtype=torch.bfloat16, out=None, workspace=No
     n = b_codes.shape[0]
     _buffer(b_codes, "b_codes", torch.uint8, n * k // 2, d)
     _buffer(b_blocked, "b_blocked", torch.uint8, -(-n // 128) * 128 * (-(-k // 128) * 4), d)
+    given = out is not None or workspace is not None or status is not None
     if out is None:
         out = _new((m, n), out_dtype, d, stream)
     else:
         _buffer(out, "out", out.dtype, m * n, d)
-        _apart(out, "out", x)
     st = None if status is None else _addr(_buffer(status, "status", torch.int32, 1, d))
     need = _workspace_size("mxfp4_gemv_workspace", m, n, k)
     workspace = _workspace(workspace, need, d, stream) if need > 0 else None
+    if given:
+        _apart((("out", out), ("workspace", workspace), ("status", status)),
+               (x, b_codes, b_blocked))
     _call("mxfp4_gemv", d, stream, x.data_ptr(), m, n, k, ldx, b_codes.data_ptr(),
           b_blocked.data_ptr(), out.data_ptr(), _dtype_code(out), _addr(workspace), max(need, 0),
           st)
@@ -565,7 +578,7 @@ def layernorm(x, weight=None, bias=None, eps=1e-5, want_stats=False, out=None, s
             _buffer(mean, "mean", torch.float32, R, d)
             _buffer(rstd, "rstd", torch.float32, R, d)
         _buffer(y, "out", x.dtype, R * C, d)
-        _apart(y, "out", x)
+        _apart((("out", y), ("mean", mean), ("rstd", rstd)), (x, weight, bias))
     _call("mxfp4_layernorm", d, stream, x.data_ptr(), dt, R, C, ldx, _addr(weight), _addr(bias),
           eps, y.data_ptr(), _addr(mean), _addr(rstd))
     return out
@@ -579,6 +592,7 @@ def layernorm_quantize(x, weight=None, bias=None, eps=1e-5, want_y=False, want_s
     ldx, dt = _norm_inputs(x, weight, bias)
     R, C = x.shape
     d = x.device
+    given = out is not None
     if out is None:
         out = (_new((R, C // 2), torch.uint8, d, stream),
                _new((R, C // 32), torch.uint8, d, stream))
@@ -595,10 +609,12 @@ def layernorm_quantize(x, weight=None, bias=None, eps=1e-5, want_y=False, want_s
     _buffer(scales, "scales", torch.uint8, R * C // 32, d)
     if want_y:
         _buffer(y, "y", x.dtype, R * C, d)
-        _apart(y, "y", x)
     if want_stats:
         _buffer(mean, "mean", torch.float32, R, d)
         _buffer(rstd, "rstd", torch.float32, R, d)
+    if given:
+        _apart((("codes", codes), ("scales", scales), ("y", y), ("mean", mean), ("rstd", rstd)),
+               (x, weight, bias))
     _call("mxfp4_layernorm_quantize", d, stream, x.data_ptr(), dt, R, C, ldx, _addr(weight),
           _addr(bias), eps, _addr(y), _addr(mean), _addr(rstd), codes.data_ptr(),
           scales.data_ptr())
@@ -637,6 +653,7 @@ def layernorm_backward(dy, x, mean, rstd, weight=None, want_params=True, out=Non
     _f32(mean, "mean", R, d)
     _f32(rstd, "rstd", R, d)
     dw = db = None
+    given = out is not None or workspace is not None
     if out is None:
         out = dx = _like(x, stream)
         if want_params:
@@ -650,7 +667,6 @@ def layernorm_backward(dy, x, mean, rstd, weight=None, want_params=True, out=Non
             _buffer(dw, "dw", torch.float32, C, d)
             _buffer(db, "db", torch.float32, C, d)
         _buffer(dx, "out", x.dtype, R * C, d)
-        _apart(dx, "out", x, dy)
     size = 0
     if want_params:
         workspace = _workspace(workspace, _workspace_size("mxfp4_layernorm_backward_workspace", R, C),
@@ -658,6 +674,10 @@ def layernorm_backward(dy, x, mean, rstd, weight=None, want_params=True, out=Non
         size = workspace.numel()
     else:
         workspace = None
+    if given:
+        # dw and db are written when all inputs have been read
+        _apart((("out", dx), ("workspace", workspace)), (x, dy, mean, rstd, weight))
+        _apart((("out", dx), ("workspace", workspace), ("dw", dw), ("db", db)))
     _call("mxfp4_layernorm_backward", d, stream, dy.data_ptr(), x.data_ptr(), dt, R, C, lddy, ldx,
           _addr(weight), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), _addr(dw), _addr(db),
           _addr(workspace), size)
@@ -675,16 +695,19 @@ def newton_schulz(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=
     dt = _dtype_code(g)
     R, C = g.shape
     d = g.device
+    given = out is not None or workspace is not None or status is not None
     if out is None:
         out = _new((R, C), out_dtype or g.dtype, d, stream)
     else:
         _buffer(out, "out", out.dtype, R * C, d)
-        if out.data_ptr() != g.data_ptr() or out.dtype != g.dtype:
-            _apart(out, "out", g)
     odt = _dtype_code(out)
     need = _workspace_size("mxfp4_newton_schulz_workspace", R, C)
     workspace = _workspace(workspace, need, d, stream)
     st = None if status is None else _addr(_buffer(status, "status", torch.int32, 1, d))
+    if given:
+        in_place = out.data_ptr() == g.data_ptr() and out.dtype == g.dtype
+        _apart((("out", out), ("workspace", workspace), ("status", status)),
+               () if in_place else (g,))
     a, b, c = coeffs
     _call("mxfp4_newton_schulz", d, stream, g.data_ptr(), dt, R, C, steps, a, b, c, eps, scale,
           out.data_ptr(), odt, workspace.data_ptr(), workspace.numel(), st)

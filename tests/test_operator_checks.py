@@ -217,3 +217,72 @@ def test_newton_schulz_checks_its_tensors(fake):
         with pytest.raises((TypeError, ValueError)):
             f()
     assert len(fake) == n
+
+
+def carve(*sizes, gap=256):
+    """Disjoint byte ranges of one buffer, and the whole buffer."""
+    whole = torch.zeros(sum(-(-n // gap) * gap + gap for n in sizes), dtype=U8)
+    parts, at = [], 0
+    for n in sizes:
+        parts.append(whole[at:at + n])
+        at += -(-n // gap) * gap + gap
+    return whole, parts
+
+
+def test_written_memory_that_meets_another_argument_is_refused(fake):
+    """Every pair of a written tensor and another one that would be read or
+    written beside it: apart it is taken, sharing bytes it is refused."""
+    L = m.lib()
+
+    def each(call, args, written, allowed=()):
+        """args: name -> (bytes, function from a byte slice to the argument)."""
+        whole, parts = carve(*(n for n, _ in args.values()))
+        good = {k: f(p) for (k, (n, f)), p in zip(args.items(), parts)}
+        call(**good)
+        n = len(fake)
+        place = dict(zip(args, parts))
+        for a in written:
+            for b in args:
+                if a == b or (a, b) in allowed or (b, a) in allowed:
+                    continue
+                # a's bytes where b's last ones are, so that one byte meets
+                size, f = args[a]
+                end = place[b].data_ptr() - whole.data_ptr() + args[b][0]
+                step = 4
+                big = torch.zeros(end - step + size + 256, dtype=U8)
+                big_b = args[b][1](big[end - args[b][0]:end])
+                big_a = f(big[end - step:end - step + size])
+                with pytest.raises(ValueError, match="overlaps"):
+                    call(**{**good, b: big_b, a: big_a})
+        assert len(fake) == n
+    view = lambda t, *shape: (lambda s: s.view(t).view(*shape))
+    R, C, K, N = 4, 96, 256, 20
+    ln = dict(x=(R * C * 4, view(F, R, C)), weight=(C * 4, view(F, C)), bias=(C * 4, view(F, C)))
+    stats = dict(mean=(R * 4, view(F, R)), rstd=(R * 4, view(F, R)))
+    y = dict(y=(R * C * 4, view(F, R, C)))
+    each(lambda x, weight, bias, y, mean, rstd: m.layernorm(x, weight, bias, want_stats=True,
+                                                            out=(y, mean, rstd)),
+         {**ln, **y, **stats}, ("y", "mean", "rstd"))
+    q = dict(codes=(R * C // 2, view(U8, R, C // 2)), scales=(R * C // 32, view(U8, R, C // 32)))
+    each(lambda x, weight, bias, codes, scales, y, mean, rstd:
+         m.layernorm_quantize(x, weight, bias, want_y=True, want_stats=True,
+                              out=(codes, scales, y, mean, rstd)),
+         {**ln, **q, **y, **stats}, ("codes", "scales", "y", "mean", "rstd"))
+    ws = L.mxfp4_layernorm_backward_workspace(R, C)
+    back = dict(dy=ln["x"], x=ln["x"], weight=ln["weight"], **stats, dx=y["y"],
+                dw=(C * 4, view(F, C)), db=(C * 4, view(F, C)), ws=(ws, view(U8, ws)))
+    # dw and db are written when the inputs have been read
+    late = [(a, b) for a in ("dw", "db") for b in ("dy", "x", "weight", "mean", "rstd")]
+    each(lambda dy, x, weight, mean, rstd, dx, dw, db, ws:
+         m.layernorm_backward(dy, x, mean, rstd, weight, out=(dx, dw, db), workspace=ws),
+         back, ("dx", "dw", "db", "ws"), late)
+    ws = L.mxfp4_gemv_workspace(3, N, K)
+    each(lambda x, codes, blocked, out, ws, st: m.gemv(x, codes, blocked, out=out, workspace=ws,
+                                                       status=st),
+         dict(x=(3 * K * 2, view(BF, 3, K)), codes=(N * K // 2, view(U8, N, K // 2)),
+              blocked=(128 * 8, view(U8, 128, 8)), out=(3 * N * 4, view(F, 3, N)),
+              ws=(ws, view(U8, ws)), st=(4, view(torch.int32, 1))), ("out", "ws", "st"))
+    ws = L.mxfp4_newton_schulz_workspace(R, C)
+    each(lambda g, out, ws, st: m.newton_schulz(g, out=out, workspace=ws, status=st),
+         dict(g=(R * C * 4, view(F, R, C)), out=(R * C * 4, view(F, R, C)), ws=(ws, view(U8, ws)),
+              st=(4, view(torch.int32, 1))), ("out", "ws", "st"))
