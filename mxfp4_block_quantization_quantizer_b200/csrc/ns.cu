@@ -389,40 +389,46 @@ struct NsLoader {
   unsigned long long *full, *empty;
   int* failed;
   const bool lead;
-  uint32_t s = 0, ph = 0, issued = 0, last_ph = 0;
+  uint32_t n, s, ph;  // stages loaded so far, and where the next one goes
   __device__ NsLoader(uint8_t* sm, unsigned long long* full_, unsigned long long* empty_,
-                      int* failed_)
+                      int* failed_, uint32_t loaded = 0)
       : base(A ? sm : sm + L::kBOff), full(full_), empty(empty_), failed(failed_),
-        lead(elect_one()) {}
+        lead(elect_one()), n(loaded), s(loaded % L::kStages), ph((loaded / L::kStages) & 1u) {}
   __device__ __forceinline__ bool tile(const CUtensorMap* map, bool mn, int row0, int n_kb) {
     for (int kb = 0; kb < n_kb; ++kb) {
       if (!warp_wait(&empty[s], ph ^ 1u, failed)) {
         atomicExch(failed, 1);
         return false;
       }
-      issued |= 1u << s;
-      last_ph = (last_ph & ~(1u << s)) | (ph << s);
-      uint8_t* const to = base + s * kOp;
-      unsigned long long* const bar = &full[s];
-      const int k0 = kb * kSK;
-      if (lead) {
-        expect_tx(bar, kOp);
-        if (mn) {
-#pragma unroll
-          for (int j = 0; j < int(kOp / 8192); ++j)
-            tma_load_2d(to + j * 8192, map, row0 + 64 * j, k0, bar);
-        } else {
-          tma_load_2d(to, map, k0, row0, bar);
-        }
-      }
-      if (++s == L::kStages) s = 0, ph ^= 1u;
+      load(map, mn, row0, kb * kSK);
     }
     return __all_sync(0xFFFFFFFFu, !failed_flag(failed));
   }
-  // every load has landed (both operands': the phase completes with them)
-  __device__ __forceinline__ void drain() {
-    for (uint32_t st = 0; st < L::kStages; ++st)
-      if ((issued >> st) & 1u) wait_parity(&full[st], (last_ph >> st) & 1u);
+  __device__ __forceinline__ void load(const CUtensorMap* map, bool mn, int row0, int k0) {
+    uint8_t* const to = base + s * kOp;
+    unsigned long long* const bar = &full[s];
+    if (lead) {
+      expect_tx(bar, kOp);
+      if (mn) {
+#pragma unroll
+        for (int j = 0; j < int(kOp / 8192); ++j)
+          tma_load_2d(to + j * 8192, map, row0 + 64 * j, k0, bar);
+      } else {
+        tma_load_2d(to, map, k0, row0, bar);
+      }
+    }
+    if (++s == L::kStages) s = 0, ph ^= 1u;
+    ++n;
+  }
+  // After a failure loads that no MMA waited for may be in flight, and one of
+  // the two loading warps may have gone further than the other. That one loads
+  // as many stages (their space was free when the other took it), so that
+  // every phase begun completes, and waits for them.
+  __device__ __forceinline__ void drain(const CUtensorMap* map, bool mn, const uint32_t* counts) {
+    const uint32_t most = counts[0] > counts[1] ? counts[0] : counts[1];
+    while (n < most) load(map, mn, 0, 0);
+    for (uint32_t i = n < L::kStages ? 0 : n - L::kStages; i < n; ++i)
+      wait_parity(&full[i % L::kStages], (i / L::kStages) & 1u);
     __syncwarp();
   }
 };
@@ -502,6 +508,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
   unsigned long long* drain = acc_empty + 2;
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drain + 1);
   int* failed = reinterpret_cast<int*>(tmem_base + 1);
+  uint32_t* counts = tmem_base + 2;  // stages that the two loading warps loaded
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   const int64_t mt = (p.m + kSM - 1) / kSM, nt = (p.n + BN - 1) / BN;
@@ -544,7 +551,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
       ns_tile<BN, kSym>(t, mt, nt, m0, n0);
       if (!ld.tile(&tm_a, A_MN, int(m0), n_kb)) break;
     }
-    ld.drain();
+    if (ld.lead) counts[0] = ld.n;
   } else if (warp == kSLoadB) {
     NsLoader<BN, false> ld(sm, full, empty, failed);
     for (int64_t t = blockIdx.x; t < n_tiles; t += gridDim.x) {
@@ -552,7 +559,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
       ns_tile<BN, kSym>(t, mt, nt, m0, n0);
       if (!ld.tile(&tm_b, B_MN, int(n0), n_kb)) break;
     }
-    ld.drain();
+    if (ld.lead) counts[1] = ld.n;
   } else if (warp == 1) {
     NsIssuer<BN> mma(sm, full, empty, tmem, failed);
     mma.operands(A_MN, B_MN);
@@ -583,6 +590,15 @@ __global__ void __launch_bounds__(kSThreads, 1)
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
                  "r"(L::kTmemCols));
+  // (last, where only the loading warps come by: before the two lines above it
+  // cost each launch of 256 x 512 0.2 us)
+  if (warp != 0 && warp != kSLoadB) return;
+  if (__builtin_expect(failed_flag(failed), 0)) {
+    if (warp == 0)
+      NsLoader<BN, true>(sm, full, empty, failed, counts[0]).drain(&tm_a, A_MN, counts);
+    else
+      NsLoader<BN, false>(sm, full, empty, failed, counts[1]).drain(&tm_b, B_MN, counts);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -661,6 +677,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
   unsigned long long* drain = acc_empty + 2;
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(drain + 1);
   int* failed = reinterpret_cast<int*>(tmem_base + 1);
+  uint32_t* counts = tmem_base + 2;  // stages that the two loading warps loaded
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);
   uint32_t rank;
@@ -719,14 +736,30 @@ __global__ void __launch_bounds__(kSThreads, 1)
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  if (warp == 0 || warp == kSLoadB) {
-    // A's warp of the leading CTA announces the whole stage: four loads of
-    // 16 KB (a load may complete before that: the count goes below zero)
-    const bool is_a = warp == 0, lead = elect_one();
+  // The loading warps (A's and B's of both CTAs). A's warp of the leading CTA
+  // announces the whole stage: four loads of 16 KB (a load may complete before
+  // that: the count goes below zero). `loaded`: stages so far.
+  const bool loader = warp == 0 || warp == kSLoadB, is_a = warp == 0;
+  const bool mn = is_a ? A_MN : B_MN;
+  uint32_t s = 0, ph = 0, loaded = 0;
+  auto load = [&](bool lead, int row0, int k0) {
     const CUtensorMap* const map = is_a ? &tm_a : &tm_b;
-    const bool mn = is_a ? A_MN : B_MN;
-    uint8_t* const base = is_a ? sm : sm + L::kBOff;
-    uint32_t s = 0, ph = 0;
+    uint8_t* const to = (is_a ? sm : sm + L::kBOff) + s * L::kA;
+    const uint32_t bar = peer_addr(&full[s], 0);
+    if (lead) {
+      if (is_a && rank == 0) expect_tx(&full[s], 2 * (L::kA + L::kB));
+      if (mn) {
+        pair_load(to, map, row0, k0, bar);
+        pair_load(to + 8192, map, row0 + 64, k0, bar);
+      } else {
+        pair_load(to, map, k0, row0, bar);
+      }
+    }
+    if (++s == L::kStages) s = 0, ph ^= 1u;
+    ++loaded;
+  };
+  if (loader) {
+    const bool lead = elect_one();
     bool ok = true;
     for (int64_t t = first; t < n_tiles && ok; t += step) {
       int64_t m0, n0;
@@ -737,28 +770,12 @@ __global__ void __launch_bounds__(kSThreads, 1)
           ok = false;
           break;
         }
-        const uint32_t bar = peer_addr(&full[s], 0);
-        uint8_t* const to = base + s * L::kA;
-        const int k0 = kb * kSK;
-        if (lead) {
-          if (is_a && rank == 0) expect_tx(&full[s], 2 * (L::kA + L::kB));
-          if (mn) {
-            pair_load(to, map, row0, k0, bar);
-            pair_load(to + 8192, map, row0 + 64, k0, bar);
-          } else {
-            pair_load(to, map, k0, row0, bar);
-          }
-        }
-        if (++s == L::kStages) s = 0, ph ^= 1u;
+        load(lead, row0, kb * kSK);
       }
       ok = ok && __all_sync(0xFFFFFFFFu, !failed_flag(failed));
     }
-    if (!ok) {
-      // loads may be in flight that no barrier here accounts for any more:
-      // give them a millisecond to land
-      fail();
-      for (int i = 0; i < 1000; ++i) __nanosleep(1000);
-    }
+    if (!ok) fail();
+    if (lead) counts[is_a ? 0 : 1] = loaded;
     __syncwarp();
   } else if (warp == 1) {
     if (rank == 0) {
@@ -766,7 +783,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
       const uint64_t a0 = A_MN ? smem_desc_mn(sm) : smem_desc_sw128(sm);
       const uint64_t b0 = B_MN ? smem_desc_mn(sm + L::kBOff) : smem_desc_sw128(sm + L::kBOff);
       constexpr uint32_t ka = A_MN ? 128u : 2u, kb_ = B_MN ? 128u : 2u;
-      uint32_t s = 0, ph = 0, ti = 0;
+      uint32_t ti = 0;
       bool ok = true;
       for (int64_t t = first; t < n_tiles && ok; t += step, ++ti) {
         const uint32_t buf = ti & 1, bph = (ti >> 1) & 1u;
@@ -797,7 +814,7 @@ __global__ void __launch_bounds__(kSThreads, 1)
         __syncwarp();
       }
       if (!ok) fail();
-      // every MMA issued has completed, and with them every load of both CTAs
+      // every MMA issued has completed, and with them the loads that they read
       if (lead)
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -831,6 +848,34 @@ __global__ void __launch_bounds__(kSThreads, 1)
   asm volatile("tcgen05.fence::before_thread_sync;");
   __syncthreads();
   pair_sync();  // neither CTA ends while the other's MMAs, loads or arrivals reach it
+  if (failed_flag(failed)) {  // (in both CTAs or in neither)
+    // The loading warps stopped at different stages, and loads that nobody
+    // read may be in flight. All of them load as many stages as the furthest
+    // did (whose space was free when that one took it), so that every phase
+    // begun completes, and the leading CTA waits for these.
+    if (loader) {
+      uint32_t most = 0;
+      for (uint32_t r = 0; r < 2; ++r) {
+        for (uint32_t i = 0; i < 2; ++i) {
+          uint32_t c;
+          asm volatile("ld.shared::cluster.u32 %0, [%1];"
+                       : "=r"(c)
+                       : "r"(peer_addr(&counts[i], r))
+                       : "memory");
+          most = c > most ? c : most;
+        }
+      }
+      const bool lead = elect_one();
+      while (loaded < most) load(lead, 0, 0);
+      if (is_a && rank == 0) {
+        const uint32_t from = most < L::kStages ? 0 : most - L::kStages;
+        for (uint32_t i = from; i < most; ++i)
+          wait_parity(&full[i % L::kStages], (i / L::kStages) & 1u);
+      }
+      __syncwarp();
+    }
+    pair_sync();
+  }
   report_failure(p.status, failed);
   if (warp == 1)
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));

@@ -225,3 +225,37 @@ def test_timeout_sets_status_and_poisons(tmp_path):
     torch.cuda.synchronize()
     assert int(st.item()) == m.STATUS_WAIT_TIMEOUT and torch.isnan(out).all()
     assert torch.isfinite(m.newton_schulz(g)).all()
+
+
+def test_timeout_of_pairs_and_of_several_tiles(tmp_path):
+    """The build whose accumulator waits give up at once, on matrices whose
+    products run as CTA pairs (the last one of 2944 x 2944, all of 4096 x
+    4096) and as several tiles of 128 x 128 a CTA (the first two of 2944): the
+    warps that load operands stop wherever they are, and every load still
+    lands before its CTA ends, in no more than a moment."""
+    path = str(tmp_path / "libmxfp4_shortwait.so")
+    B.build_variant(path, ["MXFP4_ACC_WAIT_POLLS=0"])
+    L = ctypes.CDLL(path)
+    vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+    L.mxfp4_newton_schulz.argtypes = [vp, i32, i64, i64, i32, f32, f32, f32, f32, f32, vp, i32,
+                                      vp, i64, vp, vp]
+    for side in (2944, 4096):
+        g = matrix(side, side, F, 12)
+        want = m.newton_schulz(g, 1)
+        out = torch.zeros_like(g)
+        need = m.lib().mxfp4_newton_schulz_workspace(side, side)
+        ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+        for _ in range(5):
+            st = torch.zeros(1, dtype=torch.int32, device="cuda")
+            begin, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+            begin.record()
+            assert L.mxfp4_newton_schulz(g.data_ptr(), m.F32, side, side, 1, *MUON, 1e-7, 1.0,
+                                         out.data_ptr(), m.F32, ws.data_ptr(), need,
+                                         st.data_ptr(),
+                                         torch.cuda.current_stream().cuda_stream) == 0
+            end.record()
+            torch.cuda.synchronize()
+            assert int(st.item()) == m.STATUS_WAIT_TIMEOUT and torch.isnan(out).all()
+            # a wait for a load that never comes takes seconds
+            assert begin.elapsed_time(end) < 500
+            assert torch.equal(m.newton_schulz(g, 1), want)
