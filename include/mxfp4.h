@@ -446,12 +446,16 @@ int64_t mxfp4_newton_schulz_workspace(int64_t rows, int64_t cols);
  * (for rows > cols the same with X^T). Each step moves every singular value s
  * of X to a s + b s^3 + c s^5. The products take fp16 operands with fp32
  * sums, X is carried with about 22 bits between steps, the norm is summed in
- * fp64: OUT is within about 2e-3 of the exact result relative to its norm
- * (before the rounding to out_dtype; measured for five steps of 3.4445,
- * -4.775, 2.0315 on normal and on nearly low-rank matrices). The
+ * fp64. The result differs from the exact one (before the rounding to
+ * out_dtype, relative to its norm, for 3.4445, -4.775, 2.0315 on normal and
+ * on nearly low-rank matrices) by at most 3e-3 for up to six steps where the
+ * shorter side is 64 or more (measured: 2e-4 to 2.7e-3), and by at most 1e-2
+ * for five steps where it is less (measured: up to 6.4e-3); each further step
+ * carries the error on (ten steps: measured up to 6e-3, 4e-2 on 2 x 2). The
  * same inputs give the same bits. Values are held times 2^12 in fp16, so the
- * entries of X, A and B must stay below 15.9 in magnitude; coefficients that
- * keep the singular values of X below 2 do.
+ * entries of X, A and B must stay below 15.9 in magnitude, which those
+ * coefficients do (below 3); a result with Inf or NaN shows where others do
+ * not.
  *   g        device, [rows][cols] of dtype, 16-byte aligned, read only
  *   steps    1 to 1000; a, b, c within 1e4 in magnitude; eps >= 0
  *   out      device, [rows][cols] of out_dtype, 16-byte aligned, written; it

@@ -259,3 +259,60 @@ def test_timeout_of_pairs_and_of_several_tiles(tmp_path):
             # a wait for a load that never comes takes seconds
             assert begin.elapsed_time(end) < 500
             assert torch.equal(m.newton_schulz(g, 1), want)
+
+
+def rounded64(x, c, steps):
+    """The iteration in 64 bits with the operands' stated roundings: X carried
+    as two fp16 values, A and B as one, all times 2^12."""
+    h = lambda t: t.half().double()
+    x = 4096 * x
+    for _ in range(steps):
+        hi = h(x)
+        lo = h(x - hi)
+        A = h(hi @ hi.T / 4096)
+        Bm = h(c[1] * A + c[2] * (A @ A) / 4096)
+        x = c[0] * (hi + lo) + Bm @ hi / 4096
+    return x / 4096
+
+
+@pytest.mark.parametrize("steps", [4, 5, 6])
+@pytest.mark.parametrize("shape,kind", [
+    (s, k) for s in [(64, 64), (64, 1000), (130, 70), (256, 512), (300, 2049), (1000, 200),
+                     (513, 513), (1537, 1001), (96, 14336), (2944, 2944)]
+    for k in ("normal", "lowrank")])
+def test_error_is_that_of_the_stated_roundings(shape, kind, steps):
+    """fp32 results against 64 bits, norm-wise: no further off than the header
+    says (3e-3 for up to six steps, shorter side from 64 on), and no further
+    than the roundings that it names take the same iteration. What the kernels
+    add to those are fp32 sums, off by about sqrt(k) 2^-24, a thirtieth of an
+    fp16 half step; but each such difference moves a later rounding by chance,
+    so the two errors are of one size and not the same: half as much again
+    bounds the difference of two norms of thousands of such roundings."""
+    g = matrix(*shape, F, 13, kind)
+    got = m.newton_schulz(g, steps, MUON, out_dtype=F).double()
+    x = start64(g, 1e-7)
+    if shape[0] > shape[1]:
+        x, got = x.T, got.T
+    near = rounded64(x, MUON, steps)
+    for _ in range(steps):
+        x = step64(x, MUON)
+    norm = float(x.norm())
+    off, model = float((got - x).norm()) / norm, float((near - x).norm()) / norm
+    assert off <= 3e-3 and off <= 1.5 * model + 2.0 ** -20, (off, model)
+
+
+@pytest.mark.parametrize("shape", [(1, 1), (1, 7), (9, 1), (3, 5), (16, 16), (33, 1000),
+                                   (1000, 33)])
+def test_error_of_few_singular_values(shape):
+    """A shorter side below 64: the header's 1e-2 for five steps. (A step moves
+    a singular value by up to 1e-3 through the roundings of A and B, and the
+    steps that follow, with |f'| up to 1.3 around 1, multiply that.)"""
+    for seed in range(5):
+        g = matrix(*shape, F, 14 + seed)
+        got = m.newton_schulz(g, 5, MUON, out_dtype=F).double()
+        x = start64(g, 1e-7)
+        if shape[0] > shape[1]:
+            x, got = x.T, got.T
+        for _ in range(5):
+            x = step64(x, MUON)
+        assert float((got - x).norm()) <= 1e-2 * float(x.norm())
