@@ -560,7 +560,8 @@ def layernorm(x, weight=None, bias=None, eps=1e-5, want_stats=False, out=None, s
     """mxfp4_layernorm: y = (x - mean) rstd weight + bias over the rows of x
     (bf16 or fp32, contiguous rows, any row stride), weight and bias fp32
     [cols] or None. Returns y, or (y, mean, rstd) with want_stats (out then
-    holds the three)."""
+    holds the three). No autograd graph is recorded, whatever requires grad:
+    layernorm_backward gives the gradients."""
     ldx, dt = _norm_inputs(x, weight, bias)
     R, C = x.shape
     d = x.device
@@ -588,7 +589,8 @@ def layernorm_quantize(x, weight=None, bias=None, eps=1e-5, want_y=False, want_s
                        out=None, stream=None):
     """mxfp4_layernorm_quantize: the ROWS-layout (codes, scales) of the
     nearest-even quantization of layernorm(x, weight, bias, eps), and y, mean
-    and rstd where wanted: (codes, scales[, y][, mean, rstd])."""
+    and rstd where wanted: (codes, scales[, y][, mean, rstd]). No autograd
+    graph is recorded."""
     ldx, dt = _norm_inputs(x, weight, bias)
     R, C = x.shape
     d = x.device
