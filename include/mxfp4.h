@@ -481,7 +481,10 @@ mxfp4_status mxfp4_newton_schulz(const void* g, int dtype, int64_t rows, int64_t
  *   rstd = (var + eps)^(-1/2),
  *   Y[r][c] = (X[r][c] - mean) * rstd * weight[c] + bias[c]
  * in fp32 (the squares are summed around the mean, not as E[x^2] - mean^2),
- * rounded once to dtype.
+ * rounded once to dtype. The mean is an fp32 sum, off by some 2^-24 of the
+ * row's mean |X|, and y by that times rstd * weight: data far from zero beside
+ * its spread loses that much, a row of one value its exact zeros with it.
+ * Squares and sums are fp32 too: |X - mean| below about 2^63 / sqrt(cols).
  *   x      device, rows of cols elements of dtype, row r at x + r * ldx
  *          elements (ldx >= cols); element alignment suffices, 16-byte
  *          aligned rows are faster
@@ -502,7 +505,9 @@ mxfp4_status mxfp4_layernorm(const void* x, int dtype, int64_t rows, int64_t col
  * mxfp4_layernorm fused with the forward quantization of its output: codes
  * and scales are those of mxfp4_quantize(y, dtype, rows, cols, ROWS, RNE,
  * ...), bit for bit, without y being read back; y itself is written only
- * where it is wanted. Source: "Oscillation-Reduced MXFP4 Training for Vision
+ * where it is wanted. y has the bits that mxfp4_layernorm gives, except where
+ * x and y lie equally far off a 16-byte boundary and x is dense: the two then
+ * sum a row in different orders. Source: "Oscillation-Reduced MXFP4 Training for Vision
  * Transformers", rebuttal Question 2 (Q_D of a linear layer's input in the
  * forward pass).
  *   y       as in mxfp4_layernorm, or NULL

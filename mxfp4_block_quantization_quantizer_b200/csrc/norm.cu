@@ -17,8 +17,9 @@
 // read itself, so no barrier orders them, and no register holds them. Every
 // statistic is fp32: each warp takes its own mean first and sums squares
 // around it, and the warps' pairs (sum, squares) are joined with the exact
-// correction n_w (mean_w - mean)^2, so a large common offset costs no
-// precision. Persistent grid: the warps keep their columns from row to row,
+// correction n_w (mean_w - mean)^2, so the variance of data far from zero does
+// not cancel (the mean itself has the error of an fp32 sum, some 2^-24 of the
+// row's mean |x|, which reaches y times rstd w). Persistent grid: the warps keep their columns from row to row,
 // so w and b stay in registers, and so do the column sums of the backward
 // pass; each CTA writes one partial row of dw and db and a second small
 // kernel adds those in a fixed order (no atomics: the same inputs give the
@@ -488,7 +489,8 @@ __global__ void __launch_bounds__(512)
       if (mean_out != nullptr) mean_out[row] = mean;
       if (rstd_out != nullptr) rstd_out[row] = rstd;
     }
-    // (x - mean) rstd, not x rstd - mean rstd: rows of one value stay at b
+    // (x - mean) rstd, not x rstd - mean rstd: what is left of x - mean is
+    // exact, and a row of one value whose mean has no error gives b
     const F2 nm = f2(-mean, -mean), rs = f2(rstd, rstd);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {

@@ -379,3 +379,33 @@ def test_threads_take_turns_at_one_kernel(dt, wide, narrow):
         assert not failures, failures
         for p, q in zip(work(x, dy, w, b), want):
             assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("dt", [BF, F])
+@pytest.mark.parametrize("cols", [96, 1024, 17024])
+def test_quantize_of_strided_and_unaligned_rows(dt, cols):
+    """Rows of a wider tensor, on and off 16-byte boundaries, and dense rows
+    that start one element late: the codes are those of the y that the same
+    call writes, which is layernorm's."""
+    x, _, w, b = inputs(30, 2 * cols + 8, dt, 20)
+    w, b = w[:cols].clone(), b[:cols].clone()
+    late = torch.zeros(30 * cols + 1, dtype=dt, device="cuda")[1:].view(30, cols)
+    late.copy_(x[:, :cols])
+    for xv in (x[::3, 8:cols + 8], x[:, 1:cols + 1], late):
+        y, mean, rstd = m.layernorm(xv, w, b, want_stats=True)
+        check_forward(xv, w, b, 1e-5, y, mean, rstd)
+        codes, scales = m.quantize(y)
+        got = m.layernorm_quantize(xv, w, b, want_y=True, want_stats=True)
+        for p, q in zip(got, (codes, scales, y, mean, rstd)):
+            assert torch.equal(p, q)
+        alone = m.layernorm_quantize(xv, w, b)
+        assert torch.equal(alone[0], codes) and torch.equal(alone[1], scales)
+    # x and y equally late: each call has its own order of sums, and the codes
+    # follow the y beside them
+    out = torch.zeros(30 * cols + 1, dtype=dt, device="cuda")[1:].view(30, cols)
+    got = m.layernorm_quantize(late, w, b, want_y=True, want_stats=True, out=(
+        torch.empty(30, cols // 2, dtype=torch.uint8, device="cuda"),
+        torch.empty(30, cols // 32, dtype=torch.uint8, device="cuda"), out, mean, rstd))
+    check_forward(late, w, b, 1e-5, out, mean, rstd)
+    codes, scales = m.quantize(out.clone())
+    assert torch.equal(got[0], codes) and torch.equal(got[1], scales)
