@@ -201,3 +201,46 @@ def test_gemv_past_32_bit_offsets(rows):
     want = x.double() @ w.T
     bound = (k + 64) * 2.0 ** -24 * 1.25 * (x.double().abs() @ w.abs().T) + 1e-6
     assert ((y[:, last:].double() - want).abs() <= bound).all()
+
+
+FIRST_CALLS = """
+import torch
+import mxfp4_block_quantization_quantizer_b200 as m
+g = torch.Generator(device="cuda")
+g.manual_seed(40)
+new = lambda *s: torch.randn(s, generator=g, device="cuda")
+x, dy, wide = new(700, 1024).bfloat16(), new(700, 1024).bfloat16(), new(20, 14336)
+codes = torch.randint(0, 256, (256, 512), generator=g, device="cuda", dtype=torch.uint8)
+blocked = torch.full((256, 32), 120, dtype=torch.uint8, device="cuda")
+
+def work():
+    out = []
+    for t, d in ((x, dy), (wide, wide)):
+        y, mean, rstd = m.layernorm(t, want_stats=True)
+        out += [y, mean, rstd, *m.layernorm_backward(d, t, mean, rstd)]
+        out += list(m.layernorm_quantize(t))
+    out += [m.gemv(x[:n], codes, blocked) for n in (1, 5, 12, 40)]
+    return out + [m.newton_schulz(t) for t in (x, wide)]
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    got = work()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got]
+for a, b in zip(got, work()):
+    assert torch.equal(a, b)
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_are_captured():
+    """No call before the capture has loaded a kernel or set its limits."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True,
+                          text=True, timeout=300)
+    assert done.returncode == 0 and "same" in done.stdout, done.stderr[-2000:]
