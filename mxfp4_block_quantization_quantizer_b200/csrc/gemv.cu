@@ -40,8 +40,8 @@
 // them, and k_gemv is launched over it: it sets up and loads weights
 // meanwhile and waits before it reads digits.
 //
-// Measured: 1 x 8192 x 28672 24.1 us (5.2 TB/s, 79% of a plain copy's rate),
-// 1 x 4096 x 4096 6.5 us, 16 x 4096 x 14336 14.1 us. What is left is the
+// Measured: 1 x 8192 x 28672 24.2 us (5.2 TB/s, 79% of a plain copy's rate),
+// 1 x 4096 x 4096 6.5 us, 16 x 4096 x 14336 14.5 us. What is left is the
 // start of a launch and the joining of slabs, about 5 us together. (MMAs that
 // took turns on up to four accumulators were 2 to 9% slower than one.)
 #include <cuda.h>

@@ -33,10 +33,11 @@
 // a neighbouring row are read whole and masked, and stored element by
 // element).
 //
-// Measured, of a plain copy's rate: forward 12608 x 1536 bf16 15.0 us (78%),
-// 8192 x 4096 bf16 24.4 us (84%), 4096 x 14336 fp32 84 us (85%), 5000 x 2563
-// bf16 (off the boundary) 21 us (38%); backward 12608 x 1536 bf16 27.6 us
-// (65%), 8192 x 4096 bf16 42.5 us (72%), 4096 x 14336 fp32 153 us (71%).
+// Measured, of a plain copy's rate: forward 12608 x 1536 bf16 15.2 us (78%),
+// 8192 x 4096 bf16 25.5 us (81%), 4096 x 14336 fp32 86 us (83%), 5000 x 2563
+// bf16 (off the boundary) 21.5 us (36%), with the quantization 12608 x 1536
+// bf16 20.7 us (36%; y too: 21.3 us, 63%); backward 12608 x 1536 bf16 28.4 us
+// (63%), 8192 x 4096 bf16 44.7 us (69%), 4096 x 14336 fp32 158 us (68%).
 #include "launch.cuh"
 #include "mxfp4_device.cuh"
 

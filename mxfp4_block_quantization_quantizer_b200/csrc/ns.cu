@@ -12,9 +12,12 @@
 // and written to both sides. (The sums of a tile stay in one accumulator: four
 // that a stage's MMAs took in turn made small products 2 to 5% slower.) Small
 // matrices are bound by the latency of launches that depend on one another,
-// about 5 us each (256 x 512, five steps, 17 launches: 84 us); each may set
-// itself up while the one before it ends. Large ones: 4096 x 14336, five
-// steps, 3.4 to 3.5 ms, 1.13 to 1.16 PFLOP/s of the flops above.
+// about 5 us each (256 x 512, five steps, 17 launches: 82 us); each may set
+// itself up while the one before it ends. A short side of few tiles with a
+// long one leaves A to few SMs, which walk all of K (128 x 14336: 225 us).
+// Large ones: 4096 x 14336, five steps, 3.1 to 3.5 ms in a short run, 3.6 to
+// 3.9 ms where the GPU has reached its power limit: 1.27 to 1.01 PFLOP/s of
+// the flops above.
 //
 // Numbers: operands are fp16, not bf16, at the same tensor rate and with
 // three more significant bits. Their range suffices because everything here
