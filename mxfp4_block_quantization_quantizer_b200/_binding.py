@@ -512,6 +512,11 @@ def _apart(written, read=()):
         taken.append((a0, a1))
 
 
+def _used(workspace, need):
+    """The part of a workspace that a call writes: its first `need` bytes."""
+    return None if workspace is None else workspace.view(-1)[:need]
+
+
 def gemv(x, b_codes, b_blocked, out_dtype=torch.bfloat16, out=None, workspace=None, stream=None,
          status=None):
     """mxfp4_gemv: Y = x B^T for a few bf16 rows x [m, k] (contiguous rows,
@@ -539,7 +544,7 @@ def gemv(x, b_codes, b_blocked, out_dtype=torch.bfloat16, out=None, workspace=No
     need = _workspace_size("mxfp4_gemv_workspace", m, n, k)
     workspace = _workspace(workspace, need, d, stream) if need > 0 else None
     if given:
-        _apart((("out", out), ("workspace", workspace), ("status", status)),
+        _apart((("out", out), ("workspace", _used(workspace, need)), ("status", status)),
                (x, b_codes, b_blocked))
     _call("mxfp4_gemv", d, stream, x.data_ptr(), m, n, k, ldx, b_codes.data_ptr(),
           b_blocked.data_ptr(), out.data_ptr(), _dtype_code(out), _addr(workspace), max(need, 0),
@@ -669,17 +674,18 @@ def layernorm_backward(dy, x, mean, rstd, weight=None, want_params=True, out=Non
             _buffer(dw, "dw", torch.float32, C, d)
             _buffer(db, "db", torch.float32, C, d)
         _buffer(dx, "out", x.dtype, R * C, d)
-    size = 0
+    need = size = 0
     if want_params:
-        workspace = _workspace(workspace, _workspace_size("mxfp4_layernorm_backward_workspace", R, C),
-                               d, stream)
+        need = _workspace_size("mxfp4_layernorm_backward_workspace", R, C)
+        workspace = _workspace(workspace, need, d, stream)
         size = workspace.numel()
     else:
         workspace = None
     if given:
         # dw and db are written when all inputs have been read
-        _apart((("out", dx), ("workspace", workspace)), (x, dy, mean, rstd, weight))
-        _apart((("out", dx), ("workspace", workspace), ("dw", dw), ("db", db)))
+        used = _used(workspace, need)
+        _apart((("out", dx), ("workspace", used)), (x, dy, mean, rstd, weight))
+        _apart((("out", dx), ("workspace", used), ("dw", dw), ("db", db)))
     _call("mxfp4_layernorm_backward", d, stream, dy.data_ptr(), x.data_ptr(), dt, R, C, lddy, ldx,
           _addr(weight), mean.data_ptr(), rstd.data_ptr(), dx.data_ptr(), _addr(dw), _addr(db),
           _addr(workspace), size)
@@ -708,7 +714,7 @@ def newton_schulz(g, steps=5, coeffs=(3.4445, -4.7750, 2.0315), eps=1e-7, scale=
     st = None if status is None else _addr(_buffer(status, "status", torch.int32, 1, d))
     if given:
         in_place = out.data_ptr() == g.data_ptr() and out.dtype == g.dtype
-        _apart((("out", out), ("workspace", workspace), ("status", status)),
+        _apart((("out", out), ("workspace", _used(workspace, need)), ("status", status)),
                () if in_place else (g,))
     a, b, c = coeffs
     _call("mxfp4_newton_schulz", d, stream, g.data_ptr(), dt, R, C, steps, a, b, c, eps, scale,

@@ -286,3 +286,24 @@ def test_written_memory_that_meets_another_argument_is_refused(fake):
     each(lambda g, out, ws, st: m.newton_schulz(g, out=out, workspace=ws, status=st),
          dict(g=(R * C * 4, view(F, R, C)), out=(R * C * 4, view(F, R, C)), ws=(ws, view(U8, ws)),
               st=(4, view(torch.int32, 1))), ("out", "ws", "st"))
+
+
+def test_what_lies_behind_a_workspace_of_more_than_enough_bytes_is_free(fake):
+    """A workspace may be longer than a call needs, and tensors may lie in the
+    rest of it."""
+    L = m.lib()
+    x, st = torch.zeros(4, 96), torch.zeros(4)
+    need = L.mxfp4_layernorm_backward_workspace(4, 96)
+    arena = torch.zeros(need + 4 * 96 * 4, dtype=U8)
+    tail = arena[need:].view(F).view(4, 96)
+    m.layernorm_backward(x, x, st, st, out=(tail, torch.zeros(96), torch.zeros(96)),
+                         workspace=arena)
+    need = L.mxfp4_newton_schulz_workspace(4, 96)
+    arena = torch.zeros(need + 4 * 96 * 4, dtype=U8)
+    m.newton_schulz(x, out=arena[need:].view(F).view(4, 96), workspace=arena)
+    c, s = torch.zeros(20, 128, dtype=U8), torch.zeros(128, 8, dtype=U8)
+    need = L.mxfp4_gemv_workspace(3, 20, 256)
+    arena = torch.zeros(need + 3 * 20 * 4, dtype=U8)
+    m.gemv(torch.zeros(3, 256, dtype=BF), c, s, out=arena[need:].view(F).view(3, 20),
+           workspace=arena)
+    assert len(fake) == 3
